@@ -12,9 +12,9 @@ import ctypes
 import os
 import threading
 
-ABI_VERSION = 2
+ABI_VERSION = 3
 
-VAE4_U8, VAE4_I32, VAE4_F16, VAE4_F32 = 1, 2, 3, 4
+VAE4_U8, VAE4_I32, VAE4_F16, VAE4_F32, VAE4_BF16 = 1, 2, 3, 4, 5
 
 FLAG_WARP_MMA = 0x1
 FLAG_KV_E5M2 = 0x2
@@ -26,6 +26,8 @@ STATUS_BAD_LENGTH = 0x2
 STATUS_BAD_QLEN = 0x4
 STATUS_TIMEOUT = 0x8
 STATUS_PLAN = 0x10
+STATUS_BAD_SCALE = 0x20
+STATUS_BAD_VALUE = 0x40
 
 ERRORS = {
     0: "VAE4_OK", -1: "VAE4_ERR_NULL", -2: "VAE4_ERR_DTYPE", -3: "VAE4_ERR_SHAPE",
@@ -43,6 +45,9 @@ EXPORTS = (
     "verify_attn_e4m3_clear_status", "verify_attn_e4m3_decode_table",
     "verify_attn_e4m3_noalloc", "verify_attn_e4m3_kv_read",
     "verify_attn_e4m3_bridge_fp16", "verify_attn_e4m3_kv",
+    "verify_attn_e4m3_append", "verify_attn_e4m3_block_scaled",
+    "verify_attn_e4m3_block_scores", "verify_attn_e4m3_select_blocks",
+    "verify_attn_e4m3_sparse", "verify_attn_e4m3_sparse_workspace_bytes",
 )
 
 NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -129,6 +134,17 @@ def load(build_if_stale: bool = True):
         if v != ABI_VERSION:
             raise RuntimeError(f"stale library: ABI revision {v}, binding expects "
                                f"{ABI_VERSION}; rebuild it")
+        VP, I, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float
+        O = ctypes.POINTER(Options)
+        for name, args in (("append", [P] * 8 + [VP, I, VP]),
+                           ("block_scaled", [P] * 8 + [VP, O]),
+                           ("sparse", [P] * 9 + [VP, O]),
+                           ("block_scores", [P] * 6 + [I, F, VP, I, VP]),
+                           ("select_blocks", [P] * 3 + [I, I, I, VP, VP])):
+            fn = getattr(lib, "verify_attn_e4m3_" + name)
+            fn.argtypes, fn.restype = args, ctypes.c_int
+        lib.verify_attn_e4m3_sparse_workspace_bytes.argtypes = [ctypes.c_int] * 9
+        lib.verify_attn_e4m3_sparse_workspace_bytes.restype = ctypes.c_int64
         _lib = lib
         return lib
 
@@ -369,4 +385,163 @@ def alloc_workspace(B, Hq, Hkv, Qmax, D, max_seq_len, partition_tokens=0, device
     """A zeroed workspace of the right size (torch allocation, 256-B aligned)."""
     import torch
     n = workspace_bytes(B, Hq, Hkv, Qmax, D, max_seq_len, partition_tokens)
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+# ----------------------------------------------------------------------------
+# the block-scaled cache
+# ----------------------------------------------------------------------------
+def cache_views(kv_pages):
+    """(K, V) views [n_pages][page][Hkv][D] of a pool [n_pages][2][Hkv][page][D]
+    (no copy): the form the block-scaled cache's calls take."""
+    return kv_pages[:, 0].transpose(1, 2), kv_pages[:, 1].transpose(1, 2)
+
+
+def alloc_block_scales(n_pages, Hkv, page, block_tokens, device=None):
+    """Block scales f32 [n_pages][2][Hkv][page / block_tokens] of an empty
+    cache (torch allocation)."""
+    import torch
+    if block_tokens < 16 or block_tokens % 16 or page % block_tokens:
+        raise ValueError("block_tokens: a multiple of 16 that divides the page")
+    return torch.ones(n_pages, 2, Hkv, page // block_tokens, dtype=torch.float32,
+                      device=device or "cuda")
+
+
+def alloc_k_bounds(n_pages, Hkv, page, block_tokens, D, device=None):
+    """Block bounds uint8 [n_pages][Hkv][page / block_tokens][2][D] of an empty
+    cache (torch allocation)."""
+    import torch
+    if block_tokens < 16 or block_tokens % 16 or page % block_tokens:
+        raise ValueError("block_tokens: a multiple of 16 that divides the page")
+    return torch.zeros(n_pages, Hkv, page // block_tokens, 2, D, dtype=torch.uint8,
+                       device=device or "cuda")
+
+
+_CODES = None  # torch dtype -> code, filled on first use (torch is imported lazily)
+_I64x5 = ctypes.c_int64 * 5
+
+
+def _refs(*tensors):
+    """vae4_tensor views of torch tensors, passed by reference (None stays
+    None); every tensor has to be on the current device."""
+    global _CODES
+    import torch
+    if _CODES is None:
+        _CODES = {torch.uint8: VAE4_U8, torch.int32: VAE4_I32, torch.float16: VAE4_F16,
+                  torch.float32: VAE4_F32, torch.bfloat16: VAE4_BF16,
+                  torch.float8_e4m3fn: VAE4_U8, torch.float8_e5m2: VAE4_U8}
+    dev = -1
+    out = []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        if not t.is_cuda or (t.get_device() != dev and dev >= 0):
+            raise ValueError("tensors have to be on one CUDA device")
+        dev = t.get_device()
+        code = _CODES.get(t.dtype)
+        if code is None:
+            raise TypeError(f"unsupported dtype {t.dtype}")
+        if t.dim() > 5:
+            raise ValueError("at most 5 dimensions")
+        out.append(Tensor(t.data_ptr() or None, code, t.dim(), _I64x5(*t.shape),
+                          _I64x5(*t.stride())))
+    if dev != torch.cuda.current_device():
+        raise ValueError("tensors have to be on the current device")
+    return out
+
+
+def _status_pointer(status):
+    import torch
+    if status is None:
+        return None
+    if status.dtype != torch.int32 or status.numel() < 1 or not status.is_cuda:
+        raise ValueError("status: an int32 tensor on the device")
+    return status.data_ptr()
+
+
+def verify_attn_e4m3_append(k_new, v_new, k_cache, v_cache, block_table, seq_lens, block_scales, *,
+                            k_bounds=None, status=None, flags: int = 0, stream=None):
+    """Quantise new K and V rows (f16 or bf16 [B][Qmax][Hkv][D]) into the
+    block-scaled cache, its scales and (optionally) its bounds, in place; see
+    the header.  ``status``: an optional int32 device tensor whose first
+    element receives the status bits."""
+    refs = _refs(k_new, v_new, k_cache, v_cache, block_table, seq_lens, block_scales, k_bounds)
+    rc = load().verify_attn_e4m3_append(*refs, _status_pointer(status), flags,
+                                        _stream_handle(stream))
+    _check(rc, "verify_attn_e4m3_append")
+
+
+def verify_attn_e4m3_block_scaled(q, k_cache, v_cache, block_table, seq_lens, block_scales, out,
+                                  workspace, *, softmax_scale: float = 0.0,
+                                  partition_tokens: int = 0, max_seq_len: int = 0,
+                                  num_sms: int = 0, flags: int = 0, stream=None):
+    """The verify step over a cache with one scale per block of tokens and KV
+    head (f32 [n_pages][2][Hkv][page / block]) into ``out``; other arguments
+    as verify_attn_e4m3_kv."""
+    opt = Options(softmax_scale, partition_tokens, max_seq_len, num_sms, flags, 0)
+    refs = _refs(q, k_cache, v_cache, block_table, seq_lens, block_scales, out, workspace)
+    rc = load().verify_attn_e4m3_block_scaled(*refs, _stream_handle(stream), ctypes.byref(opt))
+    _check(rc, "verify_attn_e4m3_block_scaled")
+    return out
+
+
+def verify_attn_e4m3_sparse(q, k_cache, v_cache, block_table, seq_lens, block_scales, block_ids,
+                            out, workspace, *, softmax_scale: float = 0.0, max_seq_len: int = 0,
+                            num_sms: int = 0, flags: int = 0, stream=None):
+    """Block-scaled attention in which each query attends only to the blocks
+    that ``block_ids`` (int32 [B][Qmax][Hkv][k]) lists for it; see the header.
+    ``workspace`` from alloc_sparse_workspace."""
+    opt = Options(softmax_scale, 0, max_seq_len, num_sms, flags, 0)
+    refs = _refs(q, k_cache, v_cache, block_table, seq_lens, block_scales, block_ids, out,
+                 workspace)
+    rc = load().verify_attn_e4m3_sparse(*refs, _stream_handle(stream), ctypes.byref(opt))
+    _check(rc, "verify_attn_e4m3_sparse")
+    return out
+
+
+def verify_attn_e4m3_block_scores(q, k_bounds, block_table, seq_lens, block_scales, scores, *,
+                                  block_tokens: int, softmax_scale: float = 0.0, status=None,
+                                  flags: int = 0, stream=None):
+    """Scores (f32 [B][Qmax][Hkv][columns]) of every block for every query: an
+    upper bound of the group's logits in the block; see the header."""
+    refs = _refs(q, k_bounds, block_table, seq_lens, block_scales, scores)
+    rc = load().verify_attn_e4m3_block_scores(*refs, block_tokens, softmax_scale,
+                                              _status_pointer(status), flags,
+                                              _stream_handle(stream))
+    _check(rc, "verify_attn_e4m3_block_scores")
+    return scores
+
+
+def verify_attn_e4m3_select_blocks(scores, seq_lens, block_ids, *, block_tokens: int,
+                                   sink_blocks: int = 0, local_blocks: int = 1, status=None,
+                                   stream=None):
+    """Fill ``block_ids`` (int32 [B][Qmax][Hkv][k]) with the k blocks each
+    query attends to: the first ``sink_blocks`` and last ``local_blocks`` it
+    sees, then the highest scores, equal ones by the lowest number; ascending,
+    -1 padded.  See the header."""
+    refs = _refs(scores, seq_lens, block_ids)
+    rc = load().verify_attn_e4m3_select_blocks(*refs, block_tokens, sink_blocks, local_blocks,
+                                               _status_pointer(status), _stream_handle(stream))
+    _check(rc, "verify_attn_e4m3_select_blocks")
+    return block_ids
+
+
+def verify_attn_e4m3_sparse_workspace_bytes(B, Hq, Hkv, Qmax, D, max_seq_len, block_tokens, blocks,
+                                            num_sms=0) -> int:
+    n = load().verify_attn_e4m3_sparse_workspace_bytes(B, Hq, Hkv, Qmax, D, max_seq_len,
+                                                       block_tokens, blocks, num_sms)
+    if n < 0:
+        raise Vae4Error(int(n), "sparse_workspace_bytes")
+    return int(n)
+
+
+sparse_workspace_bytes = verify_attn_e4m3_sparse_workspace_bytes
+
+
+def alloc_sparse_workspace(B, Hq, Hkv, Qmax, D, max_seq_len, block_tokens, blocks, device=None):
+    """A zeroed workspace for verify_attn_e4m3_sparse (torch allocation,
+    256-B aligned)."""
+    import torch
+    n = sparse_workspace_bytes(B, Hq, Hkv, Qmax, D, max_seq_len, block_tokens, blocks)
     return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")

@@ -235,7 +235,7 @@ const char *verify_attn_e4m3_strerror(int code) {
     case VAE4_ERR_SHAPE: return "inconsistent or out-of-range shape";
     case VAE4_ERR_STRIDE: return "unsupported strides";
     case VAE4_ERR_MISALIGNED: return "base address or row not 16-byte aligned";
-    case VAE4_ERR_UNSUPPORTED: return "head dim, page size or row count not supported";
+    case VAE4_ERR_UNSUPPORTED: return "head dim, page, block or row count not supported";
     case VAE4_ERR_GQA: return "q heads not a multiple of KV heads";
     case VAE4_ERR_WORKSPACE: return "workspace too small or not 256-byte aligned";
     case VAE4_ERR_CUDA: return "CUDA runtime error";

@@ -213,6 +213,8 @@ inline int check_kv(const vae4_tensor *k, const vae4_tensor *v, int64_t D, KvSrc
 struct Prepared {
   SplitParams sp;
   CombineParams cp;
+  ListParams lp;         // sparse only
+  bool blocked, sparse;
   int64_t ws_needed;
   bool empty;
   bool warp_mma;
@@ -232,11 +234,71 @@ inline cudaError_t launch_split(const Prepared &pr, cudaStream_t st) {
                      : launch_split_tc(pr.sp, pr.wait_limit, st);
 }
 
-// kv: the pool; or k and v (kv == null): separate caches
+// block scales: F32 [n_pages][2][Hkv][blocks per page], blocks of a multiple of 16 tokens
+inline int check_block_scales(const vae4_tensor *sc, int64_t n_pages, int64_t Hkv, int64_t page) {
+  if (sc->dtype != VAE4_F32) return VAE4_ERR_DTYPE;
+  if (sc->ndim != 4 || sc->shape[0] != n_pages || sc->shape[1] != 2 || sc->shape[2] != Hkv ||
+      sc->shape[3] < 1)
+    return VAE4_ERR_SHAPE;
+  if (page % sc->shape[3] != 0 || (page / sc->shape[3]) % 16 != 0) return VAE4_ERR_UNSUPPORTED;
+  if (sc->stride[3] != 1 && sc->shape[3] != 1) return VAE4_ERR_STRIDE;
+  for (int k = 0; k < 3; ++k)
+    if (sc->stride[k] < 0 || sc->stride[k] >= ((int64_t)1 << 40)) return VAE4_ERR_STRIDE;
+  if ((reinterpret_cast<uintptr_t>(sc->data) & 3u) != 0) return VAE4_ERR_MISALIGNED;
+  return VAE4_OK;
+}
+
+// block ids: I32 [B][Qmax][Hkv][k]
+inline int check_ids(const vae4_tensor *ids, int64_t B, int64_t Qmax, int64_t Hkv) {
+  if (ids->dtype != VAE4_I32) return VAE4_ERR_DTYPE;
+  if (ids->ndim != 4 || ids->shape[0] != B || ids->shape[1] != Qmax || ids->shape[2] != Hkv ||
+      ids->shape[3] < 1 || ids->shape[3] > INT32_MAX / 32)
+    return VAE4_ERR_SHAPE;
+  if (ids->stride[3] != 1 && ids->shape[3] != 1) return VAE4_ERR_STRIDE;
+  for (int k = 0; k < 3; ++k)
+    if (ids->stride[k] < 0 || ids->stride[k] >= ((int64_t)1 << 40)) return VAE4_ERR_STRIDE;
+  if ((reinterpret_cast<uintptr_t>(ids->data) & 3u) != 0) return VAE4_ERR_MISALIGNED;
+  return VAE4_OK;
+}
+
+// Visit lists of sparse attention: the most blocks a stream can list, the
+// partitions per stream and the workspace (the split stage's, then the stream
+// records and the lists).  Streams are planned as sequences with one KV head.
+struct SparsePlan {
+  int64_t streams, list_cap;
+  int T, P, G;       // static partitions; CTAs of the device plan
+  bool dev_plan;
+  WsLayout lay;
+  int64_t rec_off, list_off, total;
+};
+
+inline int plan_sparse(int64_t B, int64_t Hkv, int64_t Qmax, int64_t rows, int64_t D, int64_t cap,
+                       int64_t blk, int64_t k, int sms, SparsePlan *o) {
+  const int64_t nblk = (cap + blk - 1) / blk;
+  if (nblk > kMaxListBlocks) return VAE4_ERR_UNSUPPORTED;
+  o->streams = B * Hkv;
+  o->list_cap = std::min<int64_t>(nblk, Qmax * k);
+  if (o->streams > 65535) return VAE4_ERR_SHAPE;
+  const int rc = do_plan((int)o->streams, 1, (int)(o->list_cap * blk), 0, sms, &o->T, &o->P);
+  if (rc) return rc;
+  const int n_rg = vae4_tc_groups((int)rows);
+  o->dev_plan = o->streams > 1 && o->streams <= kDevPlanMaxB && o->streams * n_rg <= 65535;
+  o->G = (int)(o->dev_plan ? dev_plan_ctas((int)o->streams, 1, n_rg, sms) : 0);
+  const int64_t slots = std::max<int64_t>(o->streams * o->P, o->G);
+  o->lay = ws_layout(slots, (int)ws_rows((int)rows), (int)D, o->streams);
+  o->rec_off = align_up(o->lay.total, 256);
+  o->list_off = align_up(o->rec_off + o->streams * (int64_t)sizeof(BlockStream), 256);
+  o->total = o->list_off + o->streams * o->list_cap * (int64_t)sizeof(BlockEntry);
+  return VAE4_OK;
+}
+
+// kv: the pool; or k and v (kv == null): separate caches.  blocked: sc holds
+// one scale per block; ids (blocked only): attend to these blocks alone.
 inline int prepare(const vae4_tensor *q, const vae4_tensor *kv, const vae4_tensor *kc,
             const vae4_tensor *vc, const vae4_tensor *bt, const vae4_tensor *seq,
             const vae4_tensor *sc, const vae4_tensor *out, const vae4_tensor *ws,
-            const vae4_options *opt, Prepared *pr) {
+            const vae4_options *opt, Prepared *pr, bool blocked = false,
+            const vae4_tensor *ids = nullptr) {
   if (!q || !(kv || (kc && vc)) || !bt || !seq || !sc || !out || !ws) return VAE4_ERR_NULL;
   vae4_options o;
   memset(&o, 0, sizeof(o));
@@ -244,6 +306,7 @@ inline int prepare(const vae4_tensor *q, const vae4_tensor *kv, const vae4_tenso
   if ((o.flags & ~(VAE4_FLAG_WARP_MMA | VAE4_FLAG_KV_E5M2 | VAE4_FLAG_TEST_SHORT_WAITS)) != 0)
     return VAE4_ERR_OPTIONS;
   if (o.hilo_pv != 0 && o.hilo_pv != 1) return VAE4_ERR_OPTIONS;
+  if (blocked && ((o.flags & VAE4_FLAG_WARP_MMA) || o.hilo_pv)) return VAE4_ERR_UNSUPPORTED;
   if ((o.flags & VAE4_FLAG_WARP_MMA) &&
       ((o.flags & (VAE4_FLAG_KV_E5M2 | VAE4_FLAG_TEST_SHORT_WAITS)) || o.hilo_pv || !kv))
     return VAE4_ERR_UNSUPPORTED;
@@ -288,10 +351,20 @@ inline int prepare(const vae4_tensor *q, const vae4_tensor *kv, const vae4_tenso
   }
   if (seq->stride[0] < 0 || seq->stride[0] > INT32_MAX) return VAE4_ERR_STRIDE;
 
-  // scales: F32 [Hkv][2]
-  if (sc->dtype != VAE4_F32) return VAE4_ERR_DTYPE;
-  if (sc->ndim != 2 || sc->shape[0] != Hkv || sc->shape[1] != 2) return VAE4_ERR_SHAPE;
-  if (sc->stride[1] != 1 || sc->stride[0] < 0 || sc->stride[0] > INT32_MAX) return VAE4_ERR_STRIDE;
+  // scales: F32 [Hkv][2], or per block
+  if (blocked) {
+    rc = check_block_scales(sc, n_pages, Hkv, page);
+    if (rc) return rc;
+  } else {
+    if (sc->dtype != VAE4_F32) return VAE4_ERR_DTYPE;
+    if (sc->ndim != 2 || sc->shape[0] != Hkv || sc->shape[1] != 2) return VAE4_ERR_SHAPE;
+    if (sc->stride[1] != 1 || sc->stride[0] < 0 || sc->stride[0] > INT32_MAX) return VAE4_ERR_STRIDE;
+  }
+  if (ids) {
+    rc = check_ids(ids, B, Qmax, Hkv);
+    if (rc) return rc;
+    if (o.partition_tokens != 0) return VAE4_ERR_PARTITION;  // the lists are planned on the device
+  }
 
   // workspace: U8 [bytes], 256-byte aligned
   if (ws->dtype != VAE4_U8) return VAE4_ERR_DTYPE;
@@ -315,9 +388,9 @@ inline int prepare(const vae4_tensor *q, const vae4_tensor *kv, const vae4_tenso
   }
   // automatic plans: one sequence takes its partition length from its L on
   // the device (static grid); a batch gets the device-side balanced plan
-  const bool dev_plan = B > 1 && o.partition_tokens == 0 && B <= kDevPlanMaxB &&
+  const bool dev_plan = !blocked && B > 1 && o.partition_tokens == 0 && B <= kDevPlanMaxB &&
                         B * Hkv * vae4_tc_groups((int)rows) <= 65535;
-  const bool t_from_len = o.partition_tokens == 0 && !dev_plan;
+  const bool t_from_len = !blocked && o.partition_tokens == 0 && !dev_plan;
   // rows per CTA: row groups of the tcgen05 kernel, all rows on the mma.sync path
   int n_rg = 1, n_rows = (int)rows_pad;
   if (!(o.flags & VAE4_FLAG_WARP_MMA)) tc_row_groups((int)rows, &n_rg, &n_rows);
@@ -325,12 +398,22 @@ inline int prepare(const vae4_tensor *q, const vae4_tensor *kv, const vae4_tenso
   const WsLayout lay = ws_layout(ws_slots((int)B, (int)Hkv, P, o.partition_tokens, sms,
                                           vae4_tc_groups((int)rows)),
                                  (int)rows_pad, (int)D, B * Hkv);
-  pr->ws_needed = lay.total;
+  const int64_t blk = blocked ? page / sc->shape[3] : 0;
+  SparsePlan sparse;
+  memset(&sparse, 0, sizeof(sparse));
+  if (ids && B > 0) {
+    rc = plan_sparse(B, Hkv, Qmax, rows, D, cap, blk, ids->shape[3], sms, &sparse);
+    if (rc) return rc;
+  }
+  pr->sparse = ids != nullptr;
+  pr->blocked = blocked;
+  pr->ws_needed = ids ? sparse.total : lay.total;
   pr->empty = (B == 0);
   pr->warp_mma = (o.flags & VAE4_FLAG_WARP_MMA) != 0;
   pr->wait_limit = (o.flags & VAE4_FLAG_TEST_SHORT_WAITS) ? kShortWaitCycles : kWaitLimitCycles;
   pr->num_sms = sms;
-  if (B > 0 && ws->shape[0] < lay.total) return VAE4_ERR_WORKSPACE;
+  if (B > 0 && ws->shape[0] < pr->ws_needed) return VAE4_ERR_WORKSPACE;
+  if (ids && !ids->data && B > 0) return VAE4_ERR_NULL;
   if (!q->data || !src.kb || !src.vb || !bt->data || !seq->data || !sc->data || !out->data ||
       !ws->data) {
     if (B > 0) return VAE4_ERR_NULL;
@@ -365,8 +448,16 @@ inline int prepare(const vae4_tensor *q, const vae4_tensor *kv, const vae4_tenso
   s.seq = static_cast<const int32_t *>(seq->data);
   s.seq_sb = (int32_t)seq->stride[0];
   s.seq_has_qlen = has_qlen;
-  s.scales = static_cast<const float *>(sc->data);
-  s.scale_sh = (int32_t)sc->stride[0];
+  if (!blocked) {
+    s.scales = static_cast<const float *>(sc->data);
+    s.scale_sh = (int32_t)sc->stride[0];
+  } else {
+    s.bs.scales = static_cast<const float *>(sc->data);
+    s.bs.s_page = sc->stride[0];
+    s.bs.s_kv = sc->stride[1];
+    s.bs.s_head = sc->stride[2];
+    s.bs.blk = (int32_t)blk;
+  }
   s.ws_ml = reinterpret_cast<float *>(wsb + lay.ml_off);
   s.ws_o = reinterpret_cast<float *>(wsb + lay.o_off);
   s.plan_tab = reinterpret_cast<int2 *>(wsb + lay.tab_off);
@@ -426,6 +517,58 @@ inline int prepare(const vae4_tensor *q, const vae4_tensor *kv, const vae4_tenso
   c.plan_tab = s.plan_tab;
   c.status = s.status;
   c.num_sms = sms;
+
+  if (ids && B > 0) {
+    s.ws_ml = reinterpret_cast<float *>(wsb + sparse.lay.ml_off);
+    s.ws_o = reinterpret_cast<float *>(wsb + sparse.lay.o_off);
+    s.plan_tab = reinterpret_cast<int2 *>(wsb + sparse.lay.tab_off);
+    c.ws_ml = s.ws_ml;
+    c.ws_o = s.ws_o;
+    c.plan_tab = s.plan_tab;
+    BlockStream *rec = reinterpret_cast<BlockStream *>(wsb + sparse.rec_off);
+    BlockEntry *list = reinterpret_cast<BlockEntry *>(wsb + sparse.list_off);
+    s.bs.streams = rec;
+    s.bs.list = list;
+    s.bs.list_cap = (int32_t)sparse.list_cap;
+    s.T = c.T = sparse.T;
+    s.P = sparse.P;
+    s.dev_plan = c.dev_plan = 0;
+    s.t_from_len = c.t_from_len = 0;
+    s.plan_G = c.plan_G = (int32_t)std::max<int64_t>(sparse.streams * sparse.P, sparse.G);
+    c.P = std::max(sparse.P, sparse.G);
+    c.sparse = 1;
+
+    ListParams &l = pr->lp;
+    memset(&l, 0, sizeof(l));
+    l.ids = static_cast<const int32_t *>(ids->data);
+    l.i_sb = ids->stride[0];
+    l.i_si = ids->stride[1];
+    l.i_sh = ids->stride[2];
+    l.k = (int32_t)ids->shape[3];
+    l.bt = s.bt;
+    l.bt_sb = s.bt_sb;
+    l.max_pages = s.max_pages;
+    l.seq = s.seq;
+    l.seq_sb = s.seq_sb;
+    l.seq_has_qlen = s.seq_has_qlen;
+    l.scales = s.bs.scales;
+    l.s_page = s.bs.s_page;
+    l.s_kv = s.bs.s_kv;
+    l.s_head = s.bs.s_head;
+    l.n_pages = s.n_pages;
+    l.list = list;
+    l.streams = rec;
+    l.tab = s.plan_tab;
+    l.status = s.status;
+    l.B = s.B;
+    l.Qmax = s.Qmax;
+    l.Hkv = s.Hkv;
+    l.page = s.page;
+    l.blk = (int32_t)blk;
+    l.capacity = s.capacity;
+    l.list_cap = s.bs.list_cap;
+    l.alpha = sm_scale * 1.4426950408889634f;
+  }
   return VAE4_OK;
 }
 

@@ -1,0 +1,240 @@
+// Writer of the block-scaled FP8 cache: quantises the step's new K and V rows
+// into their pages, with one power-of-two scale per block of `blk` tokens,
+// KV head and K | V, and keeps each block's per-channel bounds of K.
+//
+// For the block's new rows x and the rows it already holds (codes c, scale
+// s_old):
+//     a    = max |x| over the finite values
+//     need = the smallest 2^e with a <= 2^e * FPMAX, -30 <= e <= 30
+//     s    = need if the block holds no earlier row, else max(s_old, need)
+//     code(x) = rn(clamp(x / s)),  c <- rn(dec(c) * s_old / s) if s > s_old
+// FPMAX = 1.75 * 2^8 (E4M3) or 1.75 * 2^15 (E5M2), so need follows from a's
+// exponent and one comparison of its significand.  A power of two costs no
+// precision (the codes are floating-point), makes x / s exact before the one
+// rounding to 8 bits, and makes a later growth of s exact for every code but
+// those that become subnormal.  The floor 2^-30 lies below what FP16 inputs
+// can need; it is also the scale of an all-zero block, so that the next row
+// of the block is free to choose.
+//
+// One CTA per (block, head and K | V, sequence).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "verify_attn_e4m3.h"
+
+namespace vae4 {
+
+namespace {
+
+constexpr int kAppendThreads = 256;
+
+template <bool BF16>
+__device__ __forceinline__ void unpack8(const uint4 &w, float (&f)[8]) {
+  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (BF16) {
+      f[2 * e] = __uint_as_float(v[e] << 16);
+      f[2 * e + 1] = __uint_as_float(v[e] & 0xFFFF0000u);
+    } else {
+      const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(&v[e]));
+      f[2 * e] = t.x;
+      f[2 * e + 1] = t.y;
+    }
+  }
+}
+
+// two floats -> two FP8 codes (a in the low byte), to nearest even, saturating
+template <bool E5M2>
+__device__ __forceinline__ uint32_t fp8x2(float a, float b) {
+  unsigned short d;
+  if constexpr (E5M2)
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;\n" : "=h"(d) : "f"(b), "f"(a));
+  else
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(d) : "f"(b), "f"(a));
+  return d;
+}
+// f16x2 that holds two FP8 values -> their codes (exact)
+template <bool E5M2>
+__device__ __forceinline__ uint32_t fp8x2_of_f16x2(uint32_t h) {
+  if constexpr (E5M2) return __byte_perm(h, 0u, 0x4431) & 0xFFFFu;
+  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+  return fp8x2<false>(f.x, f.y);
+}
+
+__device__ __forceinline__ bool scale_ok(float s) { return s >= kMinScale && s <= kMaxScale; }
+
+template <int D, bool BF16, bool E5M2>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
+  constexpr int CH = D / 8;                    // 8-element chunks per row
+  constexpr int RG = kAppendThreads / CH;      // rows per pass
+  constexpr int LEAD = E5M2 ? 15 : 8;          // FPMAX = 1.75 * 2^LEAD
+  __shared__ uint32_t red[kAppendThreads / 32];
+  __shared__ uint4 lohi[2][kAppendThreads];
+  const int tid = threadIdx.x, c = tid % CH, g = tid / CH;
+  const int b = blockIdx.z, h = blockIdx.y >> 1, w = blockIdx.y & 1;
+  const int L = p.seq[(int64_t)b * p.seq_sb];
+  const int n = p.seq_has_qlen ? p.seq[(int64_t)b * p.seq_sb + 1] : p.Qmax;
+  const bool bad_l = L < 0 || (int64_t)L > (int64_t)p.max_pages * p.page;
+  if (bad_l || n < 0 || n > p.Qmax || (L > 0 && n > L)) {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0 && p.status)
+      atomicOr(p.status, bad_l ? VAE4_STATUS_BAD_LENGTH : VAE4_STATUS_BAD_QLEN);
+    return;
+  }
+  if (L == 0 || n == 0) return;
+  const int new0 = L - n;                              // first new token
+  const int64_t t0 = ((int64_t)(new0 / p.blk) + blockIdx.x) * p.blk;  // first token of the block
+  if (t0 >= L) return;
+  const int a = max((int)(new0 - t0), 0);              // rows the block holds already
+  const int z = (int)min((int64_t)p.blk, L - t0);      // rows it holds afterwards
+  const int lp = (int)(t0 / p.page), slot = (int)(t0 - (int64_t)lp * p.page);
+  const int phys = p.bt[(int64_t)b * p.bt_sb + lp];
+  if (phys < 0 || phys >= p.n_pages) {
+    if (tid == 0 && p.status) atomicOr(p.status, VAE4_STATUS_BAD_BLOCK);
+    return;
+  }
+  float *sp = p.scales + (int64_t)phys * p.s_page + w * p.s_kv + (int64_t)h * p.s_head + slot / p.blk;
+  float s_old = 0.f;
+  if (a > 0) {
+    s_old = *sp;
+    if (!scale_ok(s_old)) {  // the same for every thread
+      if (tid == 0 && p.status) atomicOr(p.status, VAE4_STATUS_BAD_SCALE);
+      return;
+    }
+  }
+  const uint16_t *x = static_cast<const uint16_t *>(p.x[w]) + (int64_t)b * p.x_sb[w] +
+                      (t0 - new0) * p.x_si[w] + (int64_t)h * p.x_sh[w] + 8 * c;
+  uint8_t *dst = p.c[w] + (int64_t)phys * p.c_ps[w] + (int64_t)slot * p.c_ts[w] +
+                 (int64_t)h * p.c_hs[w] + 8 * c;
+
+  // ---- largest finite magnitude of the new rows (bits order as integers)
+  uint32_t am = 0u;
+  bool odd = false;  // a NaN, an infinity or a value beyond the largest scale
+  for (int r = a + g; r < z; r += RG) {
+    float f[8];
+    unpack8<BF16>(__ldg(reinterpret_cast<const uint4 *>(x + r * p.x_si[w])), f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t u = __float_as_uint(f[e]) & 0x7FFFFFFFu;
+      if (u < 0x7F800000u)
+        am = max(am, u);
+      else
+        odd = true;
+    }
+  }
+  am = __reduce_max_sync(0xffffffffu, am);
+  if ((tid & 31) == 0) red[tid >> 5] = am;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kAppendThreads / 32; ++k) am = max(am, red[k]);
+  // ---- the scale
+  const int e_need = (int)(am >> 23) - 127 - LEAD + ((am & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  odd |= e_need > 30;
+  const float need = __uint_as_float((uint32_t)(min(max(e_need, -30), 30) + 127) << 23);
+  const float s = a > 0 ? fmaxf(s_old, need) : need;
+  const bool pow2 = (__float_as_uint(s) & 0x7FFFFFu) == 0u;
+  const float inv = 1.f / s;  // exact for a power of two
+  if (odd && p.status) atomicOr(p.status, VAE4_STATUS_BAD_VALUE);
+  const bool bounds = w == 0 && p.bounds != nullptr;
+  __half2 lo[4], hi[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    lo[e] = __halves2half2(__ushort_as_half(0x7C00), __ushort_as_half(0x7C00));
+    hi[e] = __halves2half2(__ushort_as_half(0xFC00), __ushort_as_half(0xFC00));
+  }
+  auto bound8 = [&](uint2 codes) {
+    const uint32_t h4[4] = {fp8x2_to_f16x2<E5M2>(codes.x), fp8x2_to_f16x2<E5M2>(codes.x >> 16),
+                            fp8x2_to_f16x2<E5M2>(codes.y), fp8x2_to_f16x2<E5M2>(codes.y >> 16)};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const __half2 v = *reinterpret_cast<const __half2 *>(&h4[e]);
+      lo[e] = __hmin2(lo[e], v);
+      hi[e] = __hmax2(hi[e], v);
+    }
+  };
+  // ---- new rows
+  for (int r = a + g; r < z; r += RG) {
+    float f[8];
+    unpack8<BF16>(__ldg(reinterpret_cast<const uint4 *>(x + r * p.x_si[w])), f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float v = f[e] == f[e] ? f[e] : 0.f;  // a NaN is stored as zero
+      f[e] = pow2 ? v * inv : __fdiv_rn(v, s);
+    }
+    const uint2 codes = make_uint2(fp8x2<E5M2>(f[0], f[1]) | fp8x2<E5M2>(f[2], f[3]) << 16,
+                                   fp8x2<E5M2>(f[4], f[5]) | fp8x2<E5M2>(f[6], f[7]) << 16);
+    *reinterpret_cast<uint2 *>(dst + r * p.c_ts[w]) = codes;
+    if (bounds) bound8(codes);
+  }
+  // ---- rows the block holds already: under a larger scale, and in the bounds
+  const bool grow = a > 0 && s > s_old;
+  if (grow || bounds) {
+    const float f = s_old / s;
+    for (int r = g; r < a; r += RG) {
+      uint2 codes = *reinterpret_cast<const uint2 *>(dst + r * p.c_ts[w]);
+      if (grow) {
+        const uint32_t in[4] = {codes.x, codes.x >> 16, codes.y, codes.y >> 16};
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t hh = fp8x2_to_f16x2<E5M2>(in[e]);
+          const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&hh));
+          o[e] = fp8x2<E5M2>(v.x * f, v.y * f);
+        }
+        codes = make_uint2(o[0] | o[1] << 16, o[2] | o[3] << 16);
+        *reinterpret_cast<uint2 *>(dst + r * p.c_ts[w]) = codes;
+      }
+      if (bounds) bound8(codes);
+    }
+  }
+  if (tid == 0) *sp = s;
+  // ---- bounds: over the row groups
+  if (bounds) {
+    lohi[0][tid] = *reinterpret_cast<const uint4 *>(lo);
+    lohi[1][tid] = *reinterpret_cast<const uint4 *>(hi);
+    __syncthreads();
+    if (tid < 2 * CH) {
+      const int mm = tid / CH, cc = tid % CH;
+      const __half2 *v = reinterpret_cast<const __half2 *>(&lohi[mm][cc]);
+      __half2 t[4] = {v[0], v[1], v[2], v[3]};
+      for (int k = 1; k < RG; ++k) {
+        const __half2 *u = reinterpret_cast<const __half2 *>(&lohi[mm][cc + k * CH]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[e] = mm ? __hmax2(t[e], u[e]) : __hmin2(t[e], u[e]);
+      }
+      const uint32_t *u = reinterpret_cast<const uint32_t *>(t);
+      *reinterpret_cast<uint2 *>(p.bounds + (int64_t)phys * p.b_page + (int64_t)h * p.b_head +
+                                 (int64_t)(slot / p.blk) * p.b_blk + mm * p.b_mm + 8 * cc) =
+          make_uint2(fp8x2_of_f16x2<E5M2>(u[0]) | fp8x2_of_f16x2<E5M2>(u[1]) << 16,
+                     fp8x2_of_f16x2<E5M2>(u[2]) | fp8x2_of_f16x2<E5M2>(u[3]) << 16);
+    }
+  }
+}
+
+template <int D>
+cudaError_t launch_d(const AppendParams &p, bool bf16, bool e5m2, dim3 grid, cudaStream_t st) {
+  if (bf16) {
+    if (e5m2) append_kernel<D, true, true><<<grid, kAppendThreads, 0, st>>>(p);
+    else append_kernel<D, true, false><<<grid, kAppendThreads, 0, st>>>(p);
+  } else {
+    if (e5m2) append_kernel<D, false, true><<<grid, kAppendThreads, 0, st>>>(p);
+    else append_kernel<D, false, false><<<grid, kAppendThreads, 0, st>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_append(const AppendParams &p, bool bf16, bool e5m2, cudaStream_t stream) {
+  const dim3 grid((unsigned)p.touched, 2u * p.Hkv, (unsigned)p.B);
+  switch (p.D) {
+    case 64: return launch_d<64>(p, bf16, e5m2, grid, stream);
+    case 128: return launch_d<128>(p, bf16, e5m2, grid, stream);
+    case 256: return launch_d<256>(p, bf16, e5m2, grid, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace vae4

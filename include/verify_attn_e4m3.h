@@ -54,7 +54,7 @@ extern "C" {
 /* ABI revision.  A wrapper refuses a library whose revision differs from the
  * one it was written for, so an out-of-date library is refused rather than
  * used (PR #524, Scope and non-duplication; PR #560, Purpose). */
-#define VAE4_ABI_VERSION 2
+#define VAE4_ABI_VERSION 3
 
 /* Same object as cudaStream_t; NULL is the legacy default stream. */
 typedef struct CUstream_st *vae4_stream;
@@ -63,7 +63,8 @@ enum vae4_dtype {
   VAE4_U8 = 1,  /* E4M3 bytes */
   VAE4_I32 = 2,
   VAE4_F16 = 3,
-  VAE4_F32 = 4
+  VAE4_F32 = 4,
+  VAE4_BF16 = 5 /* verify_attn_e4m3_append's new rows only */
 };
 
 /* A strided view.  `data` is a device pointer unless an entry point says
@@ -158,6 +159,9 @@ enum vae4_error {
 #define VAE4_STATUS_TIMEOUT 0x8u    /* a bounded pipeline wait ran out */
 #define VAE4_STATUS_PLAN 0x10u      /* a stream's record of the device-side plan is out of
                                        range (an internal invariant; the rows are zeroed) */
+#define VAE4_STATUS_BAD_SCALE 0x20u /* a block scale is not within 2^-40 .. 2^40 */
+#define VAE4_STATUS_BAD_VALUE 0x40u /* append: a NaN (stored as 0), or an infinity or a value
+                                       beyond 2^30 times the format's largest (saturated) */
 
 /*
  * verify_attn_e4m3 -- the verify step (split kernel + combine kernel).
@@ -431,6 +435,161 @@ int verify_attn_e4m3_noalloc(const vae4_tensor *q, const vae4_tensor *kv_pages,
                              const vae4_tensor *seq_lens,
                              const vae4_tensor *kv_scales, const vae4_tensor *out,
                              vae4_stream stream, const vae4_options *opt);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The block-scaled cache.  (No counterpart on the pages, whose caches have
+ * one scale per KV head: these are additions of this library.)
+ *
+ * K and V caches as for verify_attn_e4m3_kv, U8 [n_pages][page][Hkv][D] in
+ * any strided layout (the pool form is the two views kv[:, 0] and kv[:, 1]
+ * with heads and tokens swapped), with one scale for every block of S tokens
+ * of a page and KV head:
+ *
+ *  block_scales F32 [n_pages][2][Hkv][page / S] (index 0 of dim 1: K, 1: V),
+ *              stride[3] == 1; S is a multiple of 16 that divides the page.
+ *              Token t of a sequence lies in its block t / S; the block's
+ *              codes stand for dec(code) * scale.  Scales of blocks that hold
+ *              tokens lie within 2^-40 .. 2^40 (others: BAD_SCALE).
+ *  k_bounds    U8 [n_pages][Hkv][page / S][2][D], stride[4] == 1, other
+ *              strides multiples of 16, 16-byte aligned: per channel the
+ *              smallest (index 0) and the largest (1) code of K in the block.
+ *
+ * The usual step: verify_attn_e4m3_append writes the step's K and V, then
+ * either verify_attn_e4m3_block_scaled attends to the whole context, or
+ * verify_attn_e4m3_block_scores, verify_attn_e4m3_select_blocks and
+ * verify_attn_e4m3_sparse attend to chosen blocks of it.  All take the same
+ * seq_lens, (L, q) pairs whose L counts the step's own q tokens.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * verify_attn_e4m3_append -- quantise new K and V rows into the cache.
+ *
+ *  k_new, v_new F16 or BF16 [B][Qmax][Hkv][D] (both the same type and shape),
+ *              D in {64, 128, 256}, Qmax >= 1 (a prompt's length too);
+ *              stride[3] == 1, other strides multiples of 8 elements, 16-byte
+ *              aligned.  Row i < q of sequence b is the token at position
+ *              L - q + i; later rows are padding and are not read.
+ *  k_cache, v_cache, block_table, seq_lens: as for verify_attn_e4m3_kv.
+ *  block_scales, k_bounds: see above; k_bounds may be NULL (none kept).
+ *  dev_status  optional device pointer to a status word (NULL = none).
+ *  flags       0 or VAE4_FLAG_KV_E5M2 (the codes are E5M2).
+ *
+ * For every block that receives rows, per KV head and separately for K and V:
+ *   need  = the smallest power of two s with max |x| <= s * M over the new
+ *           rows' finite values (M = 448, E5M2: 57344), within 2^-30 .. 2^30;
+ *   scale = need if the block holds no earlier token of the sequence, else
+ *           max(old scale, need);
+ *   code  = round to nearest even of clamp(x / scale), the division in FP32;
+ *   earlier codes of the block are requantised when the scale grows:
+ *           round of dec(code) * (old / scale), exact but for subnormals when
+ *           both are powers of two;
+ *   bounds are those of all codes that the block then holds.
+ * Slots past L, blocks without new rows and everything of sequences with
+ * q = 0 or L = 0 are left as they were.  NaN and infinity: BAD_VALUE.  A block
+ * with an invalid page id (BAD_BLOCK) or old scale (BAD_SCALE) is not written,
+ * nor is a sequence with invalid lengths.  Repeating a call changes nothing.
+ * The blocks written must not be shared between sequences of the call, and
+ * the caches, scales and bounds must not overlap one another or the inputs.
+ * Two calls at once may write different blocks.
+ */
+int verify_attn_e4m3_append(const vae4_tensor *k_new, const vae4_tensor *v_new,
+                            const vae4_tensor *k_cache, const vae4_tensor *v_cache,
+                            const vae4_tensor *block_table, const vae4_tensor *seq_lens,
+                            const vae4_tensor *block_scales, const vae4_tensor *k_bounds,
+                            uint32_t *dev_status, int32_t flags, vae4_stream stream);
+
+/*
+ * verify_attn_e4m3_block_scaled -- the verify step over a block-scaled cache:
+ *
+ *     z_t = softmax_scale * s_K[t / S] * q . dec(K_t)
+ *     out = sum_t e^(z_t - max z) s_V[t / S] dec(V_t) / sum_t e^(z_t - max z)
+ *
+ * Arguments, workspace, plans, results and errors as verify_attn_e4m3_kv with
+ * block_scales in the place of kv_scales.  A block with an invalid scale sets
+ * BAD_SCALE and zeroes the rows of its sequence and KV head, as an invalid
+ * page does.  hilo_pv and VAE4_FLAG_WARP_MMA: VAE4_ERR_UNSUPPORTED.
+ */
+int verify_attn_e4m3_block_scaled(const vae4_tensor *q, const vae4_tensor *k_cache,
+                                  const vae4_tensor *v_cache, const vae4_tensor *block_table,
+                                  const vae4_tensor *seq_lens, const vae4_tensor *block_scales,
+                                  const vae4_tensor *out, const vae4_tensor *workspace,
+                                  vae4_stream stream, const vae4_options *opt);
+
+/*
+ * verify_attn_e4m3_block_scores -- a cheap score of every block for every
+ * query: an upper bound of the logits that the heads of the group can have in
+ * the block, from its bounds (lo, hi) of K:
+ *
+ *     score[b][i][h][j] = softmax_scale * s_K[j] *
+ *         max_g sum_d (max(q_d, 0) dec(hi_d) + min(q_d, 0) dec(lo_d))
+ *
+ * in FP32, -inf for blocks that query i does not see (j * S > L - q + i).
+ *  q           F16 [B][Qmax][Hq][D] as for verify_attn_e4m3 (Qmax <= 16, at
+ *              most 96 rows per KV head).
+ *  scores      F32 [B][Qmax][Hkv][columns], stride[3] == 1; columns >=
+ *              ceil(L / S) (else BAD_LENGTH and nothing of the sequence is
+ *              written).  Columns at or past ceil(L / S) and rows i >= q are
+ *              left as they were.
+ *  block_tokens S; page = S * k_bounds->shape[2].
+ *  softmax_scale 0 -> 1/sqrt(D).
+ *  dev_status, flags as for verify_attn_e4m3_append.
+ * A block with an invalid page id scores -inf (BAD_BLOCK).
+ */
+int verify_attn_e4m3_block_scores(const vae4_tensor *q, const vae4_tensor *k_bounds,
+                                  const vae4_tensor *block_table, const vae4_tensor *seq_lens,
+                                  const vae4_tensor *block_scales, const vae4_tensor *scores,
+                                  int32_t block_tokens, float softmax_scale, uint32_t *dev_status,
+                                  int32_t flags, vae4_stream stream);
+
+/*
+ * verify_attn_e4m3_select_blocks -- the k blocks each query attends to.
+ *  scores      F32 [B][Qmax][Hkv][columns], stride[3] == 1 (any Qmax >= 1).
+ *  seq_lens    as for verify_attn_e4m3.
+ *  block_ids   I32 [B][Qmax][Hkv][k], stride[3] == 1, written in full:
+ *              ascending block numbers, then -1.
+ * Of the v = (L - q + i) / S + 1 blocks that query i sees: all, if v <= k;
+ * else the first sink_blocks, the last local_blocks, and those of the others
+ * with the highest scores, equal scores by the lowest number (a NaN ranks
+ * with -inf, -0 with 0).  Padding rows and sequences without tokens or with
+ * invalid lengths (BAD_LENGTH, also if ceil(L / S) > columns; BAD_QLEN) get
+ * -1 alone.  sink_blocks + local_blocks <= k, else VAE4_ERR_OPTIONS.
+ */
+int verify_attn_e4m3_select_blocks(const vae4_tensor *scores, const vae4_tensor *seq_lens,
+                                   const vae4_tensor *block_ids, int32_t block_tokens,
+                                   int32_t sink_blocks, int32_t local_blocks,
+                                   uint32_t *dev_status, vae4_stream stream);
+
+/*
+ * verify_attn_e4m3_sparse -- verify_attn_e4m3_block_scaled in which query i
+ * of KV head h attends to the tokens that it sees of the blocks listed in
+ * block_ids[b][i][h], and to no others.
+ *  block_ids   I32 [B][Qmax][Hkv][k], stride[3] == 1.  A list is a set: its
+ *              order and repetitions do not matter, and numbers outside
+ *              0 .. ceil(L / S) - 1 (such as -1) are ignored.  A query whose
+ *              set holds no visible token gets zeros.
+ *  workspace   at least verify_attn_e4m3_sparse_workspace_bytes(...) bytes.
+ * A block that several queries of a KV head list is read once.  A sequence
+ * may have at most 98304 blocks (capacity / S; else VAE4_ERR_UNSUPPORTED).
+ * opt->partition_tokens must be 0 (VAE4_ERR_PARTITION): the lists are divided
+ * among the SMs on the device.  Pages and scales of blocks outside every list
+ * are not looked at.
+ */
+int verify_attn_e4m3_sparse(const vae4_tensor *q, const vae4_tensor *k_cache,
+                            const vae4_tensor *v_cache, const vae4_tensor *block_table,
+                            const vae4_tensor *seq_lens, const vae4_tensor *block_scales,
+                            const vae4_tensor *block_ids, const vae4_tensor *out,
+                            const vae4_tensor *workspace, vae4_stream stream,
+                            const vae4_options *opt);
+
+/* Bytes of workspace of a verify_attn_e4m3_sparse call: the partials of the
+ * split stage and a list of up to min(ceil(max_seq_len / block_tokens),
+ * Qmax * blocks) 32-byte entries for every (sequence, KV head).  Arguments and
+ * errors as verify_attn_e4m3_workspace_bytes; blocks = k. */
+int64_t verify_attn_e4m3_sparse_workspace_bytes(int B, int Hq, int Hkv, int Qmax, int D,
+                                                int max_seq_len, int block_tokens, int blocks,
+                                                int num_sms);
 
 #ifdef __cplusplus
 }
