@@ -58,7 +58,7 @@ cudaStream_t cu(vae4_stream s) { return reinterpret_cast<cudaStream_t>(s); }
 
 int run_attention(const Prepared &pr, cudaStream_t st) {
   if (pr.sparse && launch_block_list(pr.lp, st) != cudaSuccess) return VAE4_ERR_CUDA;
-  if (launch_split_blocks(pr.sp, st) != cudaSuccess) return VAE4_ERR_CUDA;
+  if (launch_split(pr, st) != cudaSuccess) return VAE4_ERR_CUDA;
   if (launch_combine(pr.cp, st) != cudaSuccess) return VAE4_ERR_CUDA;
   return VAE4_OK;
 }

@@ -388,9 +388,9 @@ inline int prepare(const vae4_tensor *q, const vae4_tensor *kv, const vae4_tenso
   }
   // automatic plans: one sequence takes its partition length from its L on
   // the device (static grid); a batch gets the device-side balanced plan
-  const bool dev_plan = !blocked && B > 1 && o.partition_tokens == 0 && B <= kDevPlanMaxB &&
+  const bool dev_plan = B > 1 && o.partition_tokens == 0 && B <= kDevPlanMaxB &&
                         B * Hkv * vae4_tc_groups((int)rows) <= 65535;
-  const bool t_from_len = !blocked && o.partition_tokens == 0 && !dev_plan;
+  const bool t_from_len = o.partition_tokens == 0 && !dev_plan;
   // rows per CTA: row groups of the tcgen05 kernel, all rows on the mma.sync path
   int n_rg = 1, n_rows = (int)rows_pad;
   if (!(o.flags & VAE4_FLAG_WARP_MMA)) tc_row_groups((int)rows, &n_rg, &n_rows);
@@ -532,10 +532,11 @@ inline int prepare(const vae4_tensor *q, const vae4_tensor *kv, const vae4_tenso
     s.bs.list_cap = (int32_t)sparse.list_cap;
     s.T = c.T = sparse.T;
     s.P = sparse.P;
-    s.dev_plan = c.dev_plan = 0;
-    s.t_from_len = c.t_from_len = 0;
-    s.plan_G = c.plan_G = (int32_t)std::max<int64_t>(sparse.streams * sparse.P, sparse.G);
-    c.P = std::max(sparse.P, sparse.G);
+    s.dev_plan = c.dev_plan = sparse.dev_plan ? 1 : 0;
+    s.t_from_len = c.t_from_len = sparse.dev_plan ? 0 : 1;
+    s.plan_G = sparse.G;
+    c.plan_G = sparse.dev_plan ? sparse.G : (int32_t)(sparse.streams * sparse.P);  // slots in use
+    c.P = sparse.dev_plan ? sparse.G : sparse.P;
     c.sparse = 1;
 
     ListParams &l = pr->lp;

@@ -44,6 +44,7 @@ struct BlockScaled {
   const BlockEntry *list;        // [B * Hkv][list_cap]
   const BlockStream *streams;    // [B * Hkv]
   int32_t list_cap;
+  int32_t heads;                 // KV heads per sequence (stream = sequence * heads + head)
 };
 
 // The visit-list kernel's parameters.
