@@ -8,6 +8,7 @@ library cannot be built or loaded, every call raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import threading
@@ -136,11 +137,11 @@ def load(build_if_stale: bool = True):
                                f"{ABI_VERSION}; rebuild it")
         VP, I, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float
         O = ctypes.POINTER(Options)
-        for name, args in (("append", [P] * 8 + [VP, I, VP]),
-                           ("block_scaled", [P] * 8 + [VP, O]),
-                           ("sparse", [P] * 9 + [VP, O]),
-                           ("block_scores", [P] * 6 + [I, F, VP, I, VP]),
-                           ("select_blocks", [P] * 3 + [I, I, I, VP, VP])):
+        for name, args in (("append", [VP] * 9 + [I, VP]),
+                           ("block_scaled", [VP] * 9 + [O]),
+                           ("sparse", [VP] * 10 + [O]),
+                           ("block_scores", [VP] * 6 + [I, F, VP, I, VP]),
+                           ("select_blocks", [VP] * 3 + [I, I, I, VP, VP])):
             fn = getattr(lib, "verify_attn_e4m3_" + name)
             fn.argtypes, fn.restype = args, ctypes.c_int
         lib.verify_attn_e4m3_sparse_workspace_bytes.argtypes = [ctypes.c_int] * 9
@@ -417,44 +418,65 @@ def alloc_k_bounds(n_pages, Hkv, page, block_tokens, D, device=None):
                        device=device or "cuda")
 
 
-_CODES = None  # torch dtype -> code, filled on first use (torch is imported lazily)
-_I64x5 = ctypes.c_int64 * 5
+# What the calls below need of torch, looked up on first use (torch is imported
+# lazily): these calls run once per layer and step, so their host time counts.
+_torch = None
+_CODES = {}      # torch dtype -> vae4_dtype
+_raw_stream = None
+_PAD = [(0,) * (5 - n) for n in range(6)]
 
 
-def _refs(*tensors):
-    """vae4_tensor views of torch tensors, passed by reference (None stays
-    None); every tensor has to be on the current device."""
-    global _CODES
+def _setup():
+    global _torch, _raw_stream
     import torch
-    if _CODES is None:
-        _CODES = {torch.uint8: VAE4_U8, torch.int32: VAE4_I32, torch.float16: VAE4_F16,
-                  torch.float32: VAE4_F32, torch.bfloat16: VAE4_BF16,
-                  torch.float8_e4m3fn: VAE4_U8, torch.float8_e5m2: VAE4_U8}
-    dev = -1
-    out = []
+    _CODES.update({torch.uint8: VAE4_U8, torch.int32: VAE4_I32, torch.float16: VAE4_F16,
+                   torch.float32: VAE4_F32, torch.bfloat16: VAE4_BF16,
+                   torch.float8_e4m3fn: VAE4_U8, torch.float8_e5m2: VAE4_U8})
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    _torch = torch
+
+
+def _call(name, tensors, rest, stream, opt=None):
+    """lib.verify_attn_e4m3_<name>(tensors..., rest..., stream[, opt]), the
+    tensors (None: a null pointer) as vae4_tensor structures of 12 64-bit
+    words each in one array.  Every tensor has to be on the current device."""
+    if _torch is None:
+        _setup()
+    words, ptrs, dev = [], [], -1
     for t in tensors:
         if t is None:
-            out.append(None)
+            ptrs.append(-1)
             continue
-        if not t.is_cuda or (t.get_device() != dev and dev >= 0):
+        d = t.get_device()
+        if d < 0 or (d != dev and dev >= 0):
             raise ValueError("tensors have to be on one CUDA device")
-        dev = t.get_device()
+        dev = d
         code = _CODES.get(t.dtype)
         if code is None:
             raise TypeError(f"unsupported dtype {t.dtype}")
-        if t.dim() > 5:
+        shape = t.shape
+        n = len(shape)
+        if n > 5:
             raise ValueError("at most 5 dimensions")
-        out.append(Tensor(t.data_ptr() or None, code, t.dim(), _I64x5(*t.shape),
-                          _I64x5(*t.stride())))
-    if dev != torch.cuda.current_device():
+        ptrs.append(8 * len(words))
+        words += (t.data_ptr(), code | n << 32, *shape, *_PAD[n], *t.stride(), *_PAD[n])
+    if dev != _torch.cuda.current_device():
         raise ValueError("tensors have to be on the current device")
-    return out
+    buf = array.array("q", words)
+    base = buf.buffer_info()[0]
+    st = _raw_stream(dev) if stream is None else _stream_handle(stream)
+    args = [base + p if p >= 0 else None for p in ptrs]
+    fn = getattr(_lib or load(), name)
+    rc = fn(*args, *rest, st) if opt is None else fn(*args, *rest, st, ctypes.byref(opt))
+    if rc != 0:
+        raise Vae4Error(rc, name)
 
 
 def _status_pointer(status):
-    import torch
     if status is None:
         return None
+    import torch
     if status.dtype != torch.int32 or status.numel() < 1 or not status.is_cuda:
         raise ValueError("status: an int32 tensor on the device")
     return status.data_ptr()
@@ -466,10 +488,9 @@ def verify_attn_e4m3_append(k_new, v_new, k_cache, v_cache, block_table, seq_len
     block-scaled cache, its scales and (optionally) its bounds, in place; see
     the header.  ``status``: an optional int32 device tensor whose first
     element receives the status bits."""
-    refs = _refs(k_new, v_new, k_cache, v_cache, block_table, seq_lens, block_scales, k_bounds)
-    rc = load().verify_attn_e4m3_append(*refs, _status_pointer(status), flags,
-                                        _stream_handle(stream))
-    _check(rc, "verify_attn_e4m3_append")
+    _call("verify_attn_e4m3_append", (k_new, v_new, k_cache, v_cache, block_table, seq_lens,
+                                      block_scales, k_bounds),
+          (_status_pointer(status), flags), stream)
 
 
 def verify_attn_e4m3_block_scaled(q, k_cache, v_cache, block_table, seq_lens, block_scales, out,
@@ -480,9 +501,8 @@ def verify_attn_e4m3_block_scaled(q, k_cache, v_cache, block_table, seq_lens, bl
     head (f32 [n_pages][2][Hkv][page / block]) into ``out``; other arguments
     as verify_attn_e4m3_kv."""
     opt = Options(softmax_scale, partition_tokens, max_seq_len, num_sms, flags, 0)
-    refs = _refs(q, k_cache, v_cache, block_table, seq_lens, block_scales, out, workspace)
-    rc = load().verify_attn_e4m3_block_scaled(*refs, _stream_handle(stream), ctypes.byref(opt))
-    _check(rc, "verify_attn_e4m3_block_scaled")
+    _call("verify_attn_e4m3_block_scaled", (q, k_cache, v_cache, block_table, seq_lens,
+                                            block_scales, out, workspace), (), stream, opt)
     return out
 
 
@@ -493,10 +513,8 @@ def verify_attn_e4m3_sparse(q, k_cache, v_cache, block_table, seq_lens, block_sc
     that ``block_ids`` (int32 [B][Qmax][Hkv][k]) lists for it; see the header.
     ``workspace`` from alloc_sparse_workspace."""
     opt = Options(softmax_scale, 0, max_seq_len, num_sms, flags, 0)
-    refs = _refs(q, k_cache, v_cache, block_table, seq_lens, block_scales, block_ids, out,
-                 workspace)
-    rc = load().verify_attn_e4m3_sparse(*refs, _stream_handle(stream), ctypes.byref(opt))
-    _check(rc, "verify_attn_e4m3_sparse")
+    _call("verify_attn_e4m3_sparse", (q, k_cache, v_cache, block_table, seq_lens, block_scales,
+                                      block_ids, out, workspace), (), stream, opt)
     return out
 
 
@@ -505,11 +523,9 @@ def verify_attn_e4m3_block_scores(q, k_bounds, block_table, seq_lens, block_scal
                                   flags: int = 0, stream=None):
     """Scores (f32 [B][Qmax][Hkv][columns]) of every block for every query: an
     upper bound of the group's logits in the block; see the header."""
-    refs = _refs(q, k_bounds, block_table, seq_lens, block_scales, scores)
-    rc = load().verify_attn_e4m3_block_scores(*refs, block_tokens, softmax_scale,
-                                              _status_pointer(status), flags,
-                                              _stream_handle(stream))
-    _check(rc, "verify_attn_e4m3_block_scores")
+    _call("verify_attn_e4m3_block_scores", (q, k_bounds, block_table, seq_lens, block_scales,
+                                            scores),
+          (block_tokens, softmax_scale, _status_pointer(status), flags), stream)
     return scores
 
 
@@ -520,10 +536,8 @@ def verify_attn_e4m3_select_blocks(scores, seq_lens, block_ids, *, block_tokens:
     query attends to: the first ``sink_blocks`` and last ``local_blocks`` it
     sees, then the highest scores, equal ones by the lowest number; ascending,
     -1 padded.  See the header."""
-    refs = _refs(scores, seq_lens, block_ids)
-    rc = load().verify_attn_e4m3_select_blocks(*refs, block_tokens, sink_blocks, local_blocks,
-                                               _status_pointer(status), _stream_handle(stream))
-    _check(rc, "verify_attn_e4m3_select_blocks")
+    _call("verify_attn_e4m3_select_blocks", (scores, seq_lens, block_ids),
+          (block_tokens, sink_blocks, local_blocks, _status_pointer(status)), stream)
     return block_ids
 
 
