@@ -6,7 +6,15 @@
 // FP32 sums of exact FP16 x FP8 products.  Blocks that query i does not see
 // (their first token lies past its position) score -inf.
 //
-// One warp per block, the lanes over the channels.
+// u is a matrix product over 2 D channels, [hi | lo] of 16 blocks (rows of A)
+// times [max(q, 0) | min(q, 0)] of the group's rows (columns of B): warp-level
+// tensor-core products m16n8k16, one warp per 16 blocks.  The order of the
+// channels is free as long as A and B agree, so a thread takes 16 consecutive
+// bytes of a block's bounds as its share of four k-steps: A goes from memory
+// to the fragments with one 16-byte load per 16 channels and no shared memory,
+// and the matching share of B is 4 consecutive halves of a query's row.  The
+// bytes of the bounds bound it (2 D per block and head, read once); the tensor
+// products of up to 96 rows stay below them.
 #include <algorithm>
 
 #include "common.cuh"
@@ -18,85 +26,202 @@ namespace vae4 {
 namespace {
 
 constexpr int kScoreThreads = 128;
+constexpr int kScoreWarps = kScoreThreads / 32;
 
-template <int D, bool E5M2>
+// halves per row of B in shared memory: 16 bytes past a multiple of 32, so
+// that the 16-byte reads of a quarter warp (2 rows, 4 chunks 32 bytes apart)
+// fall on different banks
+constexpr int b_stride(int D) { return D + 8; }
+constexpr int score_smem(int D, int NT) {
+  return 2 * NT * 8 * b_stride(D) * 2 + kScoreWarps * 16 * (NT * 8 + 1) * 4;
+}
+
+template <int D, int NT, bool E5M2>
 __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const ScoreParams p) {
-  constexpr int CPL = D / 32;  // channels per lane
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int BS = b_stride(D), RS = NT * 8 + 1;
+  constexpr int NC = D / 64;  // 64-channel chunks of hi, and of lo
+  extern __shared__ __align__(16) uint8_t smem[];
+  __half *qs = reinterpret_cast<__half *>(smem);  // [2][NT * 8][BS]: max(q, 0), min(q, 0)
+  float *us = reinterpret_cast<float *>(smem + 2 * NT * 8 * BS * 2) + (threadIdx.x >> 5) * 16 * RS;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t = lane & 3;
   const int h = blockIdx.y, b = blockIdx.z;
   const int L = p.seq[(int64_t)b * p.seq_sb];
   const int n = p.seq_has_qlen ? p.seq[(int64_t)b * p.seq_sb + 1] : p.Qmax;
   const bool long_l = L > 0 && (L - 1) / p.blk >= p.cols;  // more blocks than columns
   const bool bad_l = L < 0 || (int64_t)L > (int64_t)p.max_pages * p.nb * p.blk || long_l;
   if (bad_l || n < 0 || n > p.Qmax || (L > 0 && n > L)) {
-    if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0 && p.status)
+    if (blockIdx.x == 0 && h == 0 && tid == 0 && p.status)
       atomicOr(p.status, bad_l ? VAE4_STATUS_BAD_LENGTH : VAE4_STATUS_BAD_QLEN);
     return;
   }
-  const int nblk = L > 0 ? (L - 1) / p.blk + 1 : 0;
-  const float ninf = -__int_as_float(0x7f800000);
-  for (int j = blockIdx.x * (kScoreThreads / 32) + warp; j < nblk;
-       j += gridDim.x * (kScoreThreads / 32)) {
-    const int lp = j / p.nb, sub = j - lp * p.nb;
-    const int phys = p.bt[(int64_t)b * p.bt_sb + lp];
-    const bool ok = phys >= 0 && phys < p.n_pages;
-    if (!ok && lane == 0 && p.status) atomicOr(p.status, VAE4_STATUS_BAD_BLOCK);
-    float lo[CPL], hi[CPL], s = 0.f;
-    if (ok) {
-      const uint8_t *bd = p.bounds + (int64_t)phys * p.b_page + (int64_t)h * p.b_head + (int64_t)sub * p.b_blk;
+  const int nblk = L > 0 && n > 0 ? (L - 1) / p.blk + 1 : 0;
+  const int step = gridDim.x * kScoreWarps * 16;
+  int j0 = (blockIdx.x * kScoreWarps + warp) * 16;
+  if (blockIdx.x * kScoreWarps * 16 >= nblk) return;
+  // the page and scale of block j0 + lane (lanes 0 .. 15)
+  auto page_of = [&](int jj) -> int {
+    const int j = jj + lane;
+    return lane < 16 && j < nblk ? __ldg(p.bt + (int64_t)b * p.bt_sb + j / p.nb) : 0;
+  };
+  int phys = page_of(j0);
+  // ---- B: the group's rows, split by sign
+  const int rows = n * p.G;
+  for (int x = tid; x < NT * 8 * (D / 8); x += kScoreThreads) {
+    const int r = x / (D / 8), c = x - r * (D / 8), i = r / p.G;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (r < rows)
+      v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __half *>(p.q) + (int64_t)b * p.q_sb +
+                                                (int64_t)i * p.q_si +
+                                                (int64_t)(h * p.G + r - i * p.G) * p.q_sh + 8 * c));
+    uint4 lo, hi;
+    const __half2 z = __float2half2_rn(0.f);
+    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+    uint32_t ph[4], nl[4];
 #pragma unroll
-      for (int k = 0; k < CPL; ++k) {
-        const uint32_t a = fp8x2_to_f16x2<E5M2>(bd[lane + 32 * k] | (uint32_t)bd[p.b_mm + lane + 32 * k] << 8);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&a));
-        lo[k] = f.x;
-        hi[k] = f.y;
-      }
-      s = p.scales[(int64_t)phys * p.s_page + (int64_t)h * p.s_head + sub] * p.sm_scale;
+    for (int e = 0; e < 4; ++e) {
+      const __half2 w = *reinterpret_cast<const __half2 *>(&in[e]);
+      const __half2 a = __hmax2_nan(w, z), m = __hmin2_nan(w, z);
+      ph[e] = *reinterpret_cast<const uint32_t *>(&a);
+      nl[e] = *reinterpret_cast<const uint32_t *>(&m);
     }
-    for (int i = 0; i < n; ++i) {
-      float best = ninf;
-      for (int g = 0; g < p.G; ++g) {
-        const __half *q = static_cast<const __half *>(p.q) + (int64_t)b * p.q_sb + (int64_t)i * p.q_si +
-                          (int64_t)(h * p.G + g) * p.q_sh;
-        float u = 0.f;
-        if (ok) {
+    hi = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+    lo = make_uint4(nl[0], nl[1], nl[2], nl[3]);
+    *reinterpret_cast<uint4 *>(qs + r * BS + 8 * c) = hi;
+    *reinterpret_cast<uint4 *>(qs + (NT * 8 + r) * BS + 8 * c) = lo;
+  }
+  __syncthreads();
+  const float ninf = -__int_as_float(0x7f800000);
+  for (; j0 < nblk; j0 += step) {
+    // ---- this lane's block: address and scale
+    const int j = j0 + lane;
+    bool ok = lane < 16 && j < nblk && phys >= 0 && phys < p.n_pages;
+    if (lane < 16 && j < nblk && !ok && p.status) atomicOr(p.status, VAE4_STATUS_BAD_BLOCK);
+    int64_t off = 0;
+    float s = 0.f;
+    if (ok) {
+      const int sub = j % p.nb;
+      off = (int64_t)phys * p.b_page + (int64_t)h * p.b_head + (int64_t)sub * p.b_blk;
+      s = __ldg(p.scales + (int64_t)phys * p.s_page + (int64_t)h * p.s_head + sub) * p.sm_scale;
+    }
+    phys = page_of(j0 + step);  // in flight with this step's bounds
+    const unsigned okm = __ballot_sync(0xffffffffu, ok);
+    // ---- A: rows g and g + 8 of the 16 blocks, 16 bytes per 64 channels
+    uint4 a[2][2][NC];  // [hi, lo][row][chunk]
 #pragma unroll
-          for (int k = 0; k < CPL; ++k) {
-            const float f = __half2float(q[lane + 32 * k]);
-            u += fmaxf(f, 0.f) * hi[k] + fminf(f, 0.f) * lo[k];
+    for (int r = 0; r < 2; ++r) {
+      const int src = g + 8 * r;
+      const int64_t o = __shfl_sync(0xffffffffu, off, src);
+      const bool live = (okm >> src) & 1u;
+      const uint8_t *base = p.bounds + o + 16 * t;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        a[0][r][c] = live ? __ldg(reinterpret_cast<const uint4 *>(base + p.b_mm + 64 * c))
+                          : make_uint4(0u, 0u, 0u, 0u);
+        a[1][r][c] = live ? __ldg(reinterpret_cast<const uint4 *>(base + 64 * c))
+                          : make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+    float acc[NT][4];
+#pragma unroll
+    for (int x = 0; x < NT; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[x][e] = 0.f;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const uint32_t w0[4] = {a[m][0][c].x, a[m][0][c].y, a[m][0][c].z, a[m][0][c].w};
+        const uint32_t w1[4] = {a[m][1][c].x, a[m][1][c].y, a[m][1][c].z, a[m][1][c].w};
+        const __half *qb = qs + (m * NT * 8 + g) * BS + 64 * c + 16 * t;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {  // two k-steps each
+          uint32_t fa[2][4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            fa[e][0] = fp8x2_to_f16x2<E5M2>(w0[2 * hf + e]);
+            fa[e][1] = fp8x2_to_f16x2<E5M2>(w1[2 * hf + e]);
+            fa[e][2] = fp8x2_to_f16x2<E5M2>(w0[2 * hf + e] >> 16);
+            fa[e][3] = fp8x2_to_f16x2<E5M2>(w1[2 * hf + e] >> 16);
+          }
+#pragma unroll
+          for (int x = 0; x < NT; ++x) {
+            const uint4 bq = *reinterpret_cast<const uint4 *>(qb + x * 8 * BS + 8 * hf);
+            mma16816(acc[x], fa[0], bq.x, bq.y);
+            mma16816(acc[x], fa[1], bq.z, bq.w);
           }
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-        best = fmaxf(best, u);
       }
-      if (lane == 0) {
-        const bool seen = (int64_t)j * p.blk <= L - n + i;
-        p.scores[(int64_t)b * p.o_sb + (int64_t)i * p.o_si + (int64_t)h * p.o_sh + j] =
-            ok && seen ? best * s : ninf;
+    }
+    // ---- the maximum over each query's heads, through shared memory
+    __syncwarp();
+#pragma unroll
+    for (int x = 0; x < NT; ++x) {
+      us[g * RS + 8 * x + 2 * t] = acc[x][0];
+      us[g * RS + 8 * x + 2 * t + 1] = acc[x][1];
+      us[(g + 8) * RS + 8 * x + 2 * t] = acc[x][2];
+      us[(g + 8) * RS + 8 * x + 2 * t + 1] = acc[x][3];
+    }
+    __syncwarp();
+    const float sj = __shfl_sync(0xffffffffu, s, lane & 15);
+    const bool live = (okm >> (lane & 15)) & 1u;
+    const int jo = j0 + (lane & 15);
+    for (int i = lane >> 4; i < n; i += 2) {  // 16 blocks of two queries at a time
+      float best = ninf;
+      for (int x = 0; x < p.G; ++x) best = fmaxf(best, us[(lane & 15) * RS + i * p.G + x]);
+      if (jo < nblk) {
+        const bool seen = (int64_t)jo * p.blk <= L - n + i;
+        p.scores[(int64_t)b * p.o_sb + (int64_t)i * p.o_si + (int64_t)h * p.o_sh + jo] =
+            live && seen ? best * sj : ninf;
       }
     }
   }
 }
 
+template <int D, int NT, bool E5M2>
+cudaError_t launch_t(const ScoreParams &p, cudaStream_t stream) {
+  constexpr int smem = score_smem(D, NT);
+  if (smem > 48 * 1024) {  // beyond the default dynamic shared-memory limit
+    const cudaError_t e = cudaFuncSetAttribute(block_scores_kernel<D, NT, E5M2>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  // enough CTAs for a full load of every SM (16 warps each, as far as shared
+  // memory allows); beyond that the warps take several steps, so that fewer
+  // CTAs read the queries
+  const int64_t per = kScoreWarps * 16, rows = (int64_t)p.Hkv * p.B;
+  const int64_t need = std::max<int64_t>(1, (p.cols + per - 1) / per);
+  const int64_t res = std::max<int64_t>(1, std::min<int64_t>(8, 220 * 1024 / (smem + 1024)));
+  const int64_t want = std::max<int64_t>(1, (2 * res * p.num_sms + rows - 1) / rows);
+  const int64_t steps = (need + want - 1) / want;
+  const dim3 grid((unsigned)std::min<int64_t>((need + steps - 1) / steps, 0x7fffffff),
+                  (unsigned)p.Hkv, (unsigned)p.B);
+  block_scores_kernel<D, NT, E5M2><<<grid, kScoreThreads, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D, bool E5M2>
+cudaError_t launch_n(const ScoreParams &p, cudaStream_t stream) {
+  const int nt = (p.Qmax * p.G + 7) / 8;
+  if (nt <= 1) return launch_t<D, 1, E5M2>(p, stream);
+  if (nt <= 2) return launch_t<D, 2, E5M2>(p, stream);
+  if (nt <= 3) return launch_t<D, 3, E5M2>(p, stream);
+  if (nt <= 6) return launch_t<D, 6, E5M2>(p, stream);
+  return launch_t<D, 12, E5M2>(p, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_block_scores(const ScoreParams &p, bool e5m2, cudaStream_t stream) {
-  const int per = kScoreThreads / 32;
-  const int64_t rows = (int64_t)p.Hkv * p.B;
-  int64_t gx = std::min<int64_t>(((int64_t)p.cols + per - 1) / per, 65535);
-  gx = std::max<int64_t>(1, std::min<int64_t>(gx, (32768 + rows - 1) / rows));
-  const dim3 grid((unsigned)gx, (unsigned)p.Hkv, (unsigned)p.B);
   switch (p.D * 2 + (e5m2 ? 1 : 0)) {
-    case 128: block_scores_kernel<64, false><<<grid, kScoreThreads, 0, stream>>>(p); break;
-    case 129: block_scores_kernel<64, true><<<grid, kScoreThreads, 0, stream>>>(p); break;
-    case 256: block_scores_kernel<128, false><<<grid, kScoreThreads, 0, stream>>>(p); break;
-    case 257: block_scores_kernel<128, true><<<grid, kScoreThreads, 0, stream>>>(p); break;
-    case 512: block_scores_kernel<256, false><<<grid, kScoreThreads, 0, stream>>>(p); break;
-    case 513: block_scores_kernel<256, true><<<grid, kScoreThreads, 0, stream>>>(p); break;
+    case 128: return launch_n<64, false>(p, stream);
+    case 129: return launch_n<64, true>(p, stream);
+    case 256: return launch_n<128, false>(p, stream);
+    case 257: return launch_n<128, true>(p, stream);
+    case 512: return launch_n<256, false>(p, stream);
+    case 513: return launch_n<256, true>(p, stream);
     default: return cudaErrorInvalidValue;
   }
-  return cudaGetLastError();
 }
 
 }  // namespace vae4
