@@ -29,6 +29,7 @@ namespace vae4 {
 namespace {
 
 constexpr int kAppendThreads = 256;
+constexpr int kHold = 4;  // rows a thread keeps: a block of 64 tokens at D = 128 is read once
 
 template <bool BF16>
 __device__ __forceinline__ void unpack8(const uint4 &w, float (&f)[8]) {
@@ -109,26 +110,53 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   uint8_t *dst = p.c[w] + (int64_t)phys * p.c_ps[w] + (int64_t)slot * p.c_ts[w] +
                  (int64_t)h * p.c_hs[w] + 8 * c;
 
-  // ---- largest finite magnitude of the new rows (bits order as integers)
-  uint32_t am = 0u;
-  bool odd = false;  // a NaN, an infinity or a value beyond the largest scale
-  for (int r = a + g; r < z; r += RG) {
-    float f[8];
-    unpack8<BF16>(__ldg(reinterpret_cast<const uint4 *>(x + r * p.x_si[w])), f);
+  // ---- largest magnitude of the new rows (as integers the bits order alike).
+  // The first kHold rows of a thread stay in registers for the second pass.
+  auto load = [&](int r) { return __ldcs(reinterpret_cast<const uint4 *>(x + r * p.x_si[w])); };
+  uint4 held[kHold];
+  uint32_t am2 = 0u;  // two 16-bit maxima
+  auto magnitude = [&](const uint4 &v) {
+    am2 = __vmaxu2(am2, __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu));
+    am2 = __vmaxu2(am2, __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+  };
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t u = __float_as_uint(f[e]) & 0x7FFFFFFFu;
-      if (u < 0x7F800000u)
-        am = max(am, u);
-      else
-        odd = true;
-    }
+  for (int k = 0; k < kHold; ++k) {
+    const int r = a + g + k * RG;
+    held[k] = r < z ? load(r) : make_uint4(0u, 0u, 0u, 0u);
   }
-  am = __reduce_max_sync(0xffffffffu, am);
-  if ((tid & 31) == 0) red[tid >> 5] = am;
-  __syncthreads();
 #pragma unroll
-  for (int k = 0; k < kAppendThreads / 32; ++k) am = max(am, red[k]);
+  for (int k = 0; k < kHold; ++k) magnitude(held[k]);
+  for (int r = a + g + kHold * RG; r < z; r += RG) magnitude(load(r));
+  auto block_max = [&](uint32_t v) -> uint32_t {
+    v = __reduce_max_sync(0xffffffffu, v);
+    if ((tid & 31) == 0) red[tid >> 5] = v;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kAppendThreads / 32; ++k) v = max(v, red[k]);
+    return v;
+  };
+  uint32_t am = block_max(max(am2 & 0xFFFFu, am2 >> 16));
+  bool odd = false;  // a NaN, an infinity or a value beyond the largest scale
+  if (am >= (BF16 ? 0x7F80u : 0x7C00u)) {  // rare, the same for every thread: the finite values'
+    odd = true;
+    am = 0u;
+    for (int r = a + g; r < z; r += RG) {
+      const uint4 v = load(r);
+      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t l = u[e] & 0x7FFFu, m = (u[e] >> 16) & 0x7FFFu;
+        if (l < (BF16 ? 0x7F80u : 0x7C00u)) am = max(am, l);
+        if (m < (BF16 ? 0x7F80u : 0x7C00u)) am = max(am, m);
+      }
+    }
+    __syncthreads();
+    am = block_max(am);
+  }
+  if constexpr (BF16)
+    am <<= 16;
+  else
+    am = __float_as_uint(__half2float(__ushort_as_half((unsigned short)am)));
   // ---- the scale
   const int e_need = (int)(am >> 23) - 127 - LEAD + ((am & 0x7FFFFFu) > 0x600000u ? 1 : 0);
   odd |= e_need > 30;
@@ -136,7 +164,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   const float s = a > 0 ? fmaxf(s_old, need) : need;
   const bool pow2 = (__float_as_uint(s) & 0x7FFFFFu) == 0u;
   const float inv = 1.f / s;  // exact for a power of two
-  if (odd && p.status) atomicOr(p.status, VAE4_STATUS_BAD_VALUE);
+  if (odd && tid == 0 && p.status) atomicOr(p.status, VAE4_STATUS_BAD_VALUE);
   const bool bounds = w == 0 && p.bounds != nullptr;
   __half2 lo[4], hi[4];
 #pragma unroll
@@ -155,19 +183,26 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
     }
   };
   // ---- new rows
-  for (int r = a + g; r < z; r += RG) {
+  auto store = [&](int r, const uint4 &v) {
     float f[8];
-    unpack8<BF16>(__ldg(reinterpret_cast<const uint4 *>(x + r * p.x_si[w])), f);
+    unpack8<BF16>(v, f);
+    if (odd) {  // a NaN is stored as zero
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float v = f[e] == f[e] ? f[e] : 0.f;  // a NaN is stored as zero
-      f[e] = pow2 ? v * inv : __fdiv_rn(v, s);
+      for (int e = 0; e < 8; ++e) f[e] = f[e] == f[e] ? f[e] : 0.f;
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = pow2 ? f[e] * inv : __fdiv_rn(f[e], s);
     const uint2 codes = make_uint2(fp8x2<E5M2>(f[0], f[1]) | fp8x2<E5M2>(f[2], f[3]) << 16,
                                    fp8x2<E5M2>(f[4], f[5]) | fp8x2<E5M2>(f[6], f[7]) << 16);
     *reinterpret_cast<uint2 *>(dst + r * p.c_ts[w]) = codes;
     if (bounds) bound8(codes);
+  };
+#pragma unroll
+  for (int k = 0; k < kHold; ++k) {
+    const int r = a + g + k * RG;
+    if (r < z) store(r, held[k]);
   }
+  for (int r = a + g + kHold * RG; r < z; r += RG) store(r, load(r));
   // ---- rows the block holds already: under a larger scale, and in the bounds
   const bool grow = a > 0 && s > s_old;
   if (grow || bounds) {
