@@ -5,11 +5,16 @@
 // places past the last choice hold -1.
 //
 // Radix selection, one CTA per row: scores map to unsigned keys of the same
-// order; three passes over the candidates (11, 11 and 10 bits) histogram the
-// keys that agree with the digits found so far and find the digit in which
-// the m-th largest lies, so that at the end the m-th largest key itself and
-// the number of its equals to take are known.  A last pass writes the chosen
-// indices in order: every warp counts and then writes a contiguous segment.
+// order; up to three passes over the candidates (11, 11 and 10 bits)
+// histogram the keys that agree with the digits found so far and find the
+// digit in which the m-th largest lies, so that at the end the m-th largest
+// key itself and the number of its equals to take are known (a pass that
+// leaves no choice ends the search).  Then the chosen indices are written in
+// order: every warp counts and then writes a contiguous segment.
+//
+// A warp owns a contiguous segment of the row and each of its lanes every
+// 32nd key of it, in registers where the row allows (up to kKeys per lane):
+// the row is then read once.  Longer rows are read again in each pass.
 #include "common.cuh"
 #include "kernels.h"
 #include "verify_attn_e4m3.h"
@@ -18,8 +23,6 @@ namespace vae4 {
 
 namespace {
 
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 
 // unsigned keys in the order of the scores; -0 and 0 are equal, NaN = -inf
@@ -29,10 +32,14 @@ __device__ __forceinline__ uint32_t score_key(float x) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const SelectParams p) {
+// kKeys > 0: rows of up to kThreads * kKeys blocks, in registers; 0: any row
+template <int kThreads, int kKeys>
+__global__ void __launch_bounds__(kThreads) select_blocks_kernel(const SelectParams p) {
+  constexpr int kWarps = kThreads / 32;
+  constexpr int kOwn = kBins / kThreads;  // bins per thread
   __shared__ uint32_t hist[kBins];
-  __shared__ uint32_t wsum[kSelWarps], wgt[kSelWarps], weq[kSelWarps];
-  __shared__ uint32_t pick[2];  // digit of the m-th largest, rank left below it
+  __shared__ uint32_t wsum[kWarps], weq[kWarps];
+  __shared__ uint32_t pick[3];  // digit of the m-th largest, rank left in it, its count
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int i = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   int32_t *ids = p.ids + (int64_t)b * p.i_sb + (int64_t)i * p.i_si + (int64_t)h * p.i_sh;
@@ -44,96 +51,120 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(const Select
     atomicOr(p.status, bad_l ? VAE4_STATUS_BAD_LENGTH : VAE4_STATUS_BAD_QLEN);
   const int v = bad || L == 0 || i >= n ? 0 : (L - n + i) / p.blk + 1;  // visible blocks
   if (v <= p.k) {
-    for (int x = tid; x < p.k; x += kSelThreads) ids[x] = x < v ? x : -1;
+    for (int x = tid; x < p.k; x += kThreads) ids[x] = x < v ? x : -1;
     return;
   }
   const float *sc = p.scores + (int64_t)b * p.s_sb + (int64_t)i * p.s_si + (int64_t)h * p.s_sh;
   const int c0 = p.sink, c1 = v - p.local;  // candidates
-  uint32_t m = (uint32_t)(p.k - p.sink - p.local);  // how many of them (fewer than there are)
-  uint32_t prefix = 0xFFFFFFFFu, mask = 0u;
-  if (m > 0) {
-    prefix = 0u;
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-      const int bits = pass == 2 ? 10 : 11;
-      for (int x = tid; x < kBins; x += kSelThreads) hist[x] = 0u;
-      __syncthreads();
-      for (int x = c0 + tid; x < c1; x += kSelThreads) {
-        const uint32_t key = score_key(sc[x]);
-        if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1u)], 1u);
-      }
-      __syncthreads();
-      // thread t owns bins 4t .. 4t+3; counts of all higher bins by a suffix scan
-      uint32_t own[4], sum = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sum += own[e] = hist[4 * tid + e];
-      uint32_t suf = sum;  // over this and the higher lanes
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t t = __shfl_down_sync(0xffffffffu, suf, o);
-        if (lane + o < 32) suf += t;
-      }
-      if (lane == 0) wsum[warp] = suf;
-      __syncthreads();
-      for (int k = warp + 1; k < kSelWarps; ++k) suf += wsum[k];
-      uint32_t above = suf - sum;  // candidates in bins past 4t+3
-#pragma unroll
-      for (int e = 3; e >= 0; --e) {
-        if (above < m && m <= above + own[e]) {
-          pick[0] = 4 * tid + e;
-          pick[1] = m - above;
-        }
-        above += own[e];
-      }
-      __syncthreads();
-      prefix |= pick[0] << shift;
-      mask |= ((1u << bits) - 1u) << shift;
-      m = pick[1];
-      __syncthreads();
-    }
-  }
-  // prefix: the m-th largest key; m: how many of its equals to take
-  const int seg = ((v + kSelWarps - 1) / kSelWarps + 31) & ~31;
+  const int seg = ((v + kWarps - 1) / kWarps + 31) & ~31;  // a warp's segment
   const int x0 = min(warp * seg, v), x1 = min(x0 + seg, v);
-  auto state = [&](int x) -> int {  // 0 no, 1 equal, 2 chosen
+  // key of a candidate; 0 for every other place (no score maps to it)
+  auto read_key = [&](int x) -> uint32_t {
+    return x >= c0 && x < min(c1, x1) ? score_key(__ldg(sc + x)) : 0u;
+  };
+  uint32_t key[kKeys > 0 ? kKeys : 1];
+  if constexpr (kKeys > 0) {
+#pragma unroll
+    for (int e = 0; e < kKeys; ++e) key[e] = read_key(x0 + 32 * e + lane);
+  }
+  auto each_key = [&](auto &&f) {
+    if constexpr (kKeys > 0) {
+#pragma unroll
+      for (int e = 0; e < kKeys; ++e)
+        if (32 * e < x1 - x0) f(x0 + 32 * e + lane, key[e]);
+    } else {
+      for (int x = x0; x < x1; x += 32) f(x + lane, read_key(x + lane));
+    }
+  };
+  uint32_t m = (uint32_t)(p.k - p.sink - p.local);  // how many of them (fewer than there are)
+  uint32_t prefix = 0u, mask = 0u;
+  bool all_equal = m == 0;  // m == 0: no candidate is chosen
+  for (int pass = 0; pass < 3 && !all_equal; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const uint32_t digits = pass == 2 ? 0x3FFu : 0x7FFu;
+#pragma unroll
+    for (int e = 0; e < kOwn; ++e) hist[tid + e * kThreads] = 0u;
+    __syncthreads();
+    each_key([&](int, uint32_t u) {
+      if (u != 0u && (u & mask) == prefix) atomicAdd(&hist[(u >> shift) & digits], 1u);
+    });
+    __syncthreads();
+    // thread t owns kOwn bins; counts of all higher bins by a suffix scan
+    uint32_t own[kOwn], sum = 0;
+#pragma unroll
+    for (int e = 0; e < kOwn; ++e) sum += own[e] = hist[kOwn * tid + e];
+    uint32_t suf = sum;  // over this and the higher lanes
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t t = __shfl_down_sync(0xffffffffu, suf, o);
+      if (lane + o < 32) suf += t;
+    }
+    if (lane == 0) wsum[warp] = suf;
+    __syncthreads();
+    // (the sums of the higher warps, one per lane)
+    suf += __reduce_add_sync(0xffffffffu, lane > warp && lane < kWarps ? wsum[lane] : 0u);
+    uint32_t above = suf - sum;  // candidates in bins past the thread's
+#pragma unroll
+    for (int e = kOwn - 1; e >= 0; --e) {
+      if (above < m && m <= above + own[e]) {
+        pick[0] = kOwn * tid + e;
+        pick[1] = m - above;
+        pick[2] = own[e];
+      }
+      above += own[e];
+    }
+    __syncthreads();
+    prefix |= pick[0] << shift;
+    mask |= digits << shift;
+    m = pick[1];
+    all_equal = pick[2] == m;  // every key of the digit is chosen
+    __syncthreads();
+  }
+  // chosen: the forced places, keys above the digits found, and of those that
+  // agree with them the first m
+  auto state = [&](int x, uint32_t u) -> int {  // 0 no, 1 agrees, 2 chosen
     if (x >= x1) return 0;
     if (x < c0 || x >= c1) return 2;
     if (mask == 0u) return 0;  // no place for candidates
-    const uint32_t key = score_key(sc[x]);
-    return key > prefix ? 2 : key == prefix ? 1 : 0;
+    return (u & mask) > prefix ? 2 : (u & mask) == prefix ? 1 : 0;
   };
   uint32_t gt = 0, eq = 0;
-  for (int x = x0; x < x1; x += 32) {
-    const int s = state(x + lane);
+  each_key([&](int x, uint32_t u) {
+    const int s = state(x, u);
     gt += __popc(__ballot_sync(0xffffffffu, s == 2));
     eq += __popc(__ballot_sync(0xffffffffu, s == 1));
-  }
+  });
   if (lane == 0) {
-    wgt[warp] = gt;
+    wsum[warp] = gt;
     weq[warp] = eq;
   }
   __syncthreads();
-  uint32_t base_gt = 0, base_eq = 0;
-  for (int k = 0; k < warp; ++k) {
-    base_gt += wgt[k];
-    base_eq += weq[k];
-  }
-  for (int x = x0; x < x1; x += 32) {
-    const int s = state(x + lane);
+  uint32_t base_gt = __reduce_add_sync(0xffffffffu, lane < warp ? wsum[lane] : 0u);
+  uint32_t base_eq = __reduce_add_sync(0xffffffffu, lane < warp ? weq[lane] : 0u);
+  each_key([&](int x, uint32_t u) {
+    const int s = state(x, u);
     const uint32_t bg = __ballot_sync(0xffffffffu, s == 2), be = __ballot_sync(0xffffffffu, s == 1);
     const uint32_t below = (1u << lane) - 1u;
-    const uint32_t g = base_gt + __popc(bg & below), e = base_eq + __popc(be & below);
-    if (s == 2 || (s == 1 && e < m)) ids[g + min(e, m)] = x + lane;
+    const uint32_t gr = base_gt + __popc(bg & below), e = base_eq + __popc(be & below);
+    if (s == 2 || (s == 1 && e < m)) ids[gr + min(e, m)] = x;
     base_gt += __popc(bg);
     base_eq += __popc(be);
-  }
+  });
 }
 
 }  // namespace
 
 cudaError_t launch_select_blocks(const SelectParams &p, cudaStream_t stream) {
   const dim3 grid((unsigned)p.Qmax, (unsigned)p.Hkv, (unsigned)p.B);
-  select_blocks_kernel<<<grid, kSelThreads, 0, stream>>>(p);
+  // a row has at most `cols` blocks: the smallest CTA that holds it in registers
+  if (p.cols <= 256 * 8)
+    select_blocks_kernel<256, 8><<<grid, 256, 0, stream>>>(p);
+  else if (p.cols <= 1024 * 8)
+    select_blocks_kernel<1024, 8><<<grid, 1024, 0, stream>>>(p);
+  else if (p.cols <= 1024 * 16)
+    select_blocks_kernel<1024, 16><<<grid, 1024, 0, stream>>>(p);
+  else
+    select_blocks_kernel<1024, 0><<<grid, 1024, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
