@@ -48,7 +48,8 @@ EXPORTS = (
     "verify_attn_e4m3_bridge_fp16", "verify_attn_e4m3_kv",
     "verify_attn_e4m3_append", "verify_attn_e4m3_block_scaled",
     "verify_attn_e4m3_block_scores", "verify_attn_e4m3_select_blocks",
-    "verify_attn_e4m3_sparse", "verify_attn_e4m3_sparse_workspace_bytes",
+    "verify_attn_e4m3_sparse", "verify_attn_e4m3_block_scaled_workspace_bytes",
+    "verify_attn_e4m3_sparse_workspace_bytes",
 )
 
 NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -144,6 +145,8 @@ def load(build_if_stale: bool = True):
                            ("select_blocks", [VP] * 3 + [I, I, I, VP, VP])):
             fn = getattr(lib, "verify_attn_e4m3_" + name)
             fn.argtypes, fn.restype = args, ctypes.c_int
+        lib.verify_attn_e4m3_block_scaled_workspace_bytes.argtypes = [ctypes.c_int] * 7
+        lib.verify_attn_e4m3_block_scaled_workspace_bytes.restype = ctypes.c_int64
         lib.verify_attn_e4m3_sparse_workspace_bytes.argtypes = [ctypes.c_int] * 9
         lib.verify_attn_e4m3_sparse_workspace_bytes.restype = ctypes.c_int64
         _lib = lib
@@ -383,9 +386,11 @@ decode_table = verify_attn_e4m3_decode_table
 
 
 def alloc_workspace(B, Hq, Hkv, Qmax, D, max_seq_len, partition_tokens=0, device=None):
-    """A zeroed workspace of the right size (torch allocation, 256-B aligned)."""
+    """A zeroed workspace of the right size (torch allocation, 256-B aligned),
+    for the head-scaled calls and verify_attn_e4m3_block_scaled alike."""
     import torch
-    n = workspace_bytes(B, Hq, Hkv, Qmax, D, max_seq_len, partition_tokens)
+    n = max(workspace_bytes(B, Hq, Hkv, Qmax, D, max_seq_len, partition_tokens),
+            block_scaled_workspace_bytes(B, Hq, Hkv, Qmax, D, max_seq_len))
     return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
 
 
@@ -495,12 +500,12 @@ def verify_attn_e4m3_append(k_new, v_new, k_cache, v_cache, block_table, seq_len
 
 def verify_attn_e4m3_block_scaled(q, k_cache, v_cache, block_table, seq_lens, block_scales, out,
                                   workspace, *, softmax_scale: float = 0.0,
-                                  partition_tokens: int = 0, max_seq_len: int = 0,
-                                  num_sms: int = 0, flags: int = 0, stream=None):
+                                  max_seq_len: int = 0, num_sms: int = 0, flags: int = 0,
+                                  stream=None):
     """The verify step over a cache with one scale per block of tokens and KV
     head (f32 [n_pages][2][Hkv][page / block]) into ``out``; other arguments
-    as verify_attn_e4m3_kv."""
-    opt = Options(softmax_scale, partition_tokens, max_seq_len, num_sms, flags, 0)
+    as verify_attn_e4m3_kv.  ``workspace`` from alloc_workspace."""
+    opt = Options(softmax_scale, 0, max_seq_len, num_sms, flags, 0)
     _call("verify_attn_e4m3_block_scaled", (q, k_cache, v_cache, block_table, seq_lens,
                                             block_scales, out, workspace), (), stream, opt)
     return out
@@ -539,6 +544,18 @@ def verify_attn_e4m3_select_blocks(scores, seq_lens, block_ids, *, block_tokens:
     _call("verify_attn_e4m3_select_blocks", (scores, seq_lens, block_ids),
           (block_tokens, sink_blocks, local_blocks, _status_pointer(status)), stream)
     return block_ids
+
+
+def verify_attn_e4m3_block_scaled_workspace_bytes(B, Hq, Hkv, Qmax, D, max_seq_len,
+                                                  num_sms=0) -> int:
+    n = load().verify_attn_e4m3_block_scaled_workspace_bytes(B, Hq, Hkv, Qmax, D, max_seq_len,
+                                                             num_sms)
+    if n < 0:
+        raise Vae4Error(int(n), "block_scaled_workspace_bytes")
+    return int(n)
+
+
+block_scaled_workspace_bytes = verify_attn_e4m3_block_scaled_workspace_bytes
 
 
 def verify_attn_e4m3_sparse_workspace_bytes(B, Hq, Hkv, Qmax, D, max_seq_len, block_tokens, blocks,

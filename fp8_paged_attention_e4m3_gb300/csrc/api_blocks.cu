@@ -58,9 +58,31 @@ cudaStream_t cu(vae4_stream s) { return reinterpret_cast<cudaStream_t>(s); }
 
 int run_attention(const Prepared &pr, cudaStream_t st) {
   if (pr.sparse && launch_block_list(pr.lp, st) != cudaSuccess) return VAE4_ERR_CUDA;
-  if (launch_split(pr, st) != cudaSuccess) return VAE4_ERR_CUDA;
-  if (launch_combine(pr.cp, st) != cudaSuccess) return VAE4_ERR_CUDA;
+  if (launch_seg(pr.gp, st) != cudaSuccess) return VAE4_ERR_CUDA;
+  if (launch_seg_combine(pr.gp, st) != cudaSuccess) return VAE4_ERR_CUDA;
   return VAE4_OK;
+}
+
+// bytes of workspace of attention over a block-scaled cache (blocks = 0: dense)
+int64_t attention_bytes(int B, int Hq, int Hkv, int Qmax, int D, int max_seq_len, int block_tokens,
+                        int blocks, int num_sms) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Qmax < 1 || Qmax > kMaxQmax || max_seq_len < 1 ||
+      max_seq_len > INT32_MAX / 2)
+    return VAE4_ERR_SHAPE;
+  if (D != 64 && D != 128 && D != 256) return VAE4_ERR_UNSUPPORTED;
+  if (Hq % Hkv != 0) return VAE4_ERR_GQA;
+  const int rows = Qmax * (Hq / Hkv);
+  if (align_up(rows, 16) > kMaxRowsPad) return VAE4_ERR_UNSUPPORTED;
+  int sms = num_sms;
+  if (sms < 0) return VAE4_ERR_SHAPE;
+  if (sms == 0) {
+    const int rc = device_sms(&sms);
+    if (rc) return rc;
+  }
+  BlockPlan plan;
+  const int rc =
+      plan_blocks(B, Hkv, Qmax, rows, D, max_seq_len, block_tokens, blocks, sms, &plan);
+  return rc ? rc : plan.total;
 }
 
 }  // namespace
@@ -191,24 +213,15 @@ int verify_attn_e4m3_sparse(const vae4_tensor *q, const vae4_tensor *k_cache,
 int64_t verify_attn_e4m3_sparse_workspace_bytes(int B, int Hq, int Hkv, int Qmax, int D,
                                                 int max_seq_len, int block_tokens, int blocks,
                                                 int num_sms) {
-  if (B < 1 || Hq < 1 || Hkv < 1 || Qmax < 1 || Qmax > kMaxQmax || max_seq_len < 1 ||
-      max_seq_len > INT32_MAX / 2 || blocks < 1 || blocks > INT32_MAX / 32)
-    return VAE4_ERR_SHAPE;
-  if (D != 64 && D != 128 && D != 256) return VAE4_ERR_UNSUPPORTED;
+  if (blocks < 1 || blocks > INT32_MAX / 32) return VAE4_ERR_SHAPE;
   if (block_tokens < 16 || block_tokens % 16 != 0 || block_tokens > 65536)
     return VAE4_ERR_UNSUPPORTED;
-  if (Hq % Hkv != 0) return VAE4_ERR_GQA;
-  const int rows = Qmax * (Hq / Hkv);
-  if (align_up(rows, 16) > kMaxRowsPad) return VAE4_ERR_UNSUPPORTED;
-  int sms = num_sms;
-  if (sms < 0) return VAE4_ERR_SHAPE;
-  if (sms == 0) {
-    const int rc = device_sms(&sms);
-    if (rc) return rc;
-  }
-  SparsePlan sp;
-  const int rc = plan_sparse(B, Hkv, Qmax, rows, D, max_seq_len, block_tokens, blocks, sms, &sp);
-  return rc ? rc : sp.total;
+  return attention_bytes(B, Hq, Hkv, Qmax, D, max_seq_len, block_tokens, blocks, num_sms);
+}
+
+int64_t verify_attn_e4m3_block_scaled_workspace_bytes(int B, int Hq, int Hkv, int Qmax, int D,
+                                                      int max_seq_len, int num_sms) {
+  return attention_bytes(B, Hq, Hkv, Qmax, D, max_seq_len, 16, 0, num_sms);
 }
 
 int verify_attn_e4m3_block_scores(const vae4_tensor *q, const vae4_tensor *k_bounds,

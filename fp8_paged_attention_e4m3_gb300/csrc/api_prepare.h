@@ -213,8 +213,9 @@ inline int check_kv(const vae4_tensor *k, const vae4_tensor *v, int64_t D, KvSrc
 struct Prepared {
   SplitParams sp;
   CombineParams cp;
-  ListParams lp;         // sparse only
-  bool blocked, sparse;
+  SegParams gp;          // block-scaled caches (sp and cp are not used then)
+  ListParams lp;         // sparse attention
+  bool sparse;
   int64_t ws_needed;
   bool empty;
   bool warp_mma;
@@ -261,34 +262,41 @@ inline int check_ids(const vae4_tensor *ids, int64_t B, int64_t Qmax, int64_t Hk
   return VAE4_OK;
 }
 
-// Visit lists of sparse attention: the most blocks a stream can list, the
-// partitions per stream and the workspace (the split stage's, then the stream
-// records and the lists).  Streams are planned as sequences with one KV head.
-struct SparsePlan {
+// Attention over a block-scaled cache: the CTAs, and the workspace: status |
+// (max, sum) [2 CTAs][N][2] | unnormalised O [2 CTAs][N][D] | (first CTA,
+// parts) [streams][row groups] | sparse attention (k > 0): stream records |
+// visit lists [streams][list_cap].
+struct BlockPlan {
   int64_t streams, list_cap;
-  int T, P, G;       // static partitions; CTAs of the device plan
-  bool dev_plan;
-  WsLayout lay;
-  int64_t rec_off, list_off, total;
+  int n_rg, N, ctas;
+  int64_t ml_off, o_off, tab_off, rec_off, list_off, total;
 };
 
-inline int plan_sparse(int64_t B, int64_t Hkv, int64_t Qmax, int64_t rows, int64_t D, int64_t cap,
-                       int64_t blk, int64_t k, int sms, SparsePlan *o) {
-  const int64_t nblk = (cap + blk - 1) / blk;
-  if (nblk > kMaxListBlocks) return VAE4_ERR_UNSUPPORTED;
+inline int plan_blocks(int64_t B, int64_t Hkv, int64_t Qmax, int64_t rows, int64_t D, int64_t cap,
+                       int64_t blk, int64_t k, int sms, BlockPlan *o) {
+  memset(o, 0, sizeof(*o));
   o->streams = B * Hkv;
-  o->list_cap = std::min<int64_t>(nblk, Qmax * k);
-  if (o->streams > 65535) return VAE4_ERR_SHAPE;
-  const int rc = do_plan((int)o->streams, 1, (int)(o->list_cap * blk), 0, sms, &o->T, &o->P);
-  if (rc) return rc;
-  const int n_rg = vae4_tc_groups((int)rows);
-  o->dev_plan = o->streams > 1 && o->streams <= kDevPlanMaxB && o->streams * n_rg <= 65535;
-  o->G = (int)(o->dev_plan ? dev_plan_ctas((int)o->streams, 1, n_rg, sms) : 0);
-  const int64_t slots = std::max<int64_t>(o->streams * o->P, o->G);
-  o->lay = ws_layout(slots, (int)ws_rows((int)rows), (int)D, o->streams);
-  o->rec_off = align_up(o->lay.total, 256);
-  o->list_off = align_up(o->rec_off + o->streams * (int64_t)sizeof(BlockStream), 256);
-  o->total = o->list_off + o->streams * o->list_cap * (int64_t)sizeof(BlockEntry);
+  if (o->streams > INT32_MAX / 64 || sms < 1) return VAE4_ERR_SHAPE;
+  int64_t tokens = cap;  // most that a stream walks
+  if (k > 0) {
+    const int64_t nblk = (cap + blk - 1) / blk;
+    if (nblk > kMaxListBlocks) return VAE4_ERR_UNSUPPORTED;
+    o->list_cap = std::min<int64_t>(nblk, Qmax * k);
+    tokens = o->list_cap * blk;
+  }
+  tc_row_groups((int)rows, &o->n_rg, &o->N);
+  o->ctas = (int)std::min<int64_t>(sms, o->streams * o->n_rg * ((tokens + 63) / 64));
+  // places of the plan's line (see seg_tc.cuh), in 32 bits on the device
+  if (o->streams * o->n_rg * ((tokens + 63) / 64 + 3) >= (1ll << 30)) return VAE4_ERR_SHAPE;
+  o->ml_off = kStatusBytes;
+  o->o_off = align_up(o->ml_off + 2ll * o->ctas * o->N * 2 * 4, 256);
+  o->tab_off = align_up(o->o_off + 2ll * o->ctas * o->N * D * 4, 256);
+  o->total = o->tab_off + o->streams * o->n_rg * 8;
+  if (k > 0) {
+    o->rec_off = align_up(o->total, 256);
+    o->list_off = align_up(o->rec_off + o->streams * (int64_t)sizeof(BlockStream), 256);
+    o->total = o->list_off + o->streams * o->list_cap * (int64_t)sizeof(BlockEntry);
+  }
   return VAE4_OK;
 }
 
@@ -363,8 +371,8 @@ inline int prepare(const vae4_tensor *q, const vae4_tensor *kv, const vae4_tenso
   if (ids) {
     rc = check_ids(ids, B, Qmax, Hkv);
     if (rc) return rc;
-    if (o.partition_tokens != 0) return VAE4_ERR_PARTITION;  // the lists are planned on the device
   }
+  if (blocked && o.partition_tokens != 0) return VAE4_ERR_PARTITION;  // planned on the device
 
   // workspace: U8 [bytes], 256-byte aligned
   if (ws->dtype != VAE4_U8) return VAE4_ERR_DTYPE;
@@ -399,15 +407,14 @@ inline int prepare(const vae4_tensor *q, const vae4_tensor *kv, const vae4_tenso
                                           vae4_tc_groups((int)rows)),
                                  (int)rows_pad, (int)D, B * Hkv);
   const int64_t blk = blocked ? page / sc->shape[3] : 0;
-  SparsePlan sparse;
-  memset(&sparse, 0, sizeof(sparse));
-  if (ids && B > 0) {
-    rc = plan_sparse(B, Hkv, Qmax, rows, D, cap, blk, ids->shape[3], sms, &sparse);
+  BlockPlan plan;
+  memset(&plan, 0, sizeof(plan));
+  if (blocked && B > 0) {
+    rc = plan_blocks(B, Hkv, Qmax, rows, D, cap, blk, ids ? ids->shape[3] : 0, sms, &plan);
     if (rc) return rc;
   }
   pr->sparse = ids != nullptr;
-  pr->blocked = blocked;
-  pr->ws_needed = ids ? sparse.total : lay.total;
+  pr->ws_needed = blocked ? plan.total : lay.total;
   pr->empty = (B == 0);
   pr->warp_mma = (o.flags & VAE4_FLAG_WARP_MMA) != 0;
   pr->wait_limit = (o.flags & VAE4_FLAG_TEST_SHORT_WAITS) ? kShortWaitCycles : kWaitLimitCycles;
@@ -448,16 +455,8 @@ inline int prepare(const vae4_tensor *q, const vae4_tensor *kv, const vae4_tenso
   s.seq = static_cast<const int32_t *>(seq->data);
   s.seq_sb = (int32_t)seq->stride[0];
   s.seq_has_qlen = has_qlen;
-  if (!blocked) {
-    s.scales = static_cast<const float *>(sc->data);
-    s.scale_sh = (int32_t)sc->stride[0];
-  } else {
-    s.bs.scales = static_cast<const float *>(sc->data);
-    s.bs.s_page = sc->stride[0];
-    s.bs.s_kv = sc->stride[1];
-    s.bs.s_head = sc->stride[2];
-    s.bs.blk = (int32_t)blk;
-  }
+  s.scales = static_cast<const float *>(sc->data);
+  s.scale_sh = blocked ? 0 : (int32_t)sc->stride[0];
   s.ws_ml = reinterpret_cast<float *>(wsb + lay.ml_off);
   s.ws_o = reinterpret_cast<float *>(wsb + lay.o_off);
   s.plan_tab = reinterpret_cast<int2 *>(wsb + lay.tab_off);
@@ -518,26 +517,76 @@ inline int prepare(const vae4_tensor *q, const vae4_tensor *kv, const vae4_tenso
   c.status = s.status;
   c.num_sms = sms;
 
+  if (blocked && B > 0) {
+    SegParams &g = pr->gp;
+    memset(&g, 0, sizeof(g));
+    g.q = q->data;
+    g.q_sb = q->stride[0];
+    g.q_si = q->stride[1];
+    g.q_sh = q->stride[2];
+    g.out = out->data;
+    g.o_sb = out->stride[0];
+    g.o_si = out->stride[1];
+    g.o_sh = out->stride[2];
+    g.k_base = src.kb;
+    g.v_base = src.vb;
+    g.k_ps = src.k_ps;
+    g.k_ts = src.k_ts;
+    g.k_hs = src.k_hs;
+    g.v_ps = src.v_ps;
+    g.v_ts = src.v_ts;
+    g.v_hs = src.v_hs;
+    g.n_pages = n_pages;
+    g.bt = s.bt;
+    g.bt_sb = s.bt_sb;
+    g.max_pages = s.max_pages;
+    g.seq = s.seq;
+    g.seq_sb = s.seq_sb;
+    g.seq_has_qlen = s.seq_has_qlen;
+    g.seq_capacity = s.capacity;
+    g.scales = static_cast<const float *>(sc->data);
+    g.s_page = sc->stride[0];
+    g.s_kv = sc->stride[1];
+    g.s_head = sc->stride[2];
+    g.blk = (int32_t)blk;
+    g.pairs = s.seq;
+    g.pair_sb = s.seq_sb;
+    g.has_qlen = s.seq_has_qlen;
+    g.groups = (int32_t)B;
+    g.unit_heads = (int32_t)Hkv;
+    g.capacity = s.capacity;
+    g.ws_ml = reinterpret_cast<float *>(wsb + plan.ml_off);
+    g.ws_o = reinterpret_cast<float *>(wsb + plan.o_off);
+    g.tab = reinterpret_cast<int2 *>(wsb + plan.tab_off);
+    g.status = s.status;
+    g.B = s.B;
+    g.Qmax = s.Qmax;
+    g.Hkv = s.Hkv;
+    g.G = s.G;
+    g.D = s.D;
+    g.page = s.page;
+    g.e5m2 = s.kv_e5m2;
+    g.N = plan.N;
+    g.n_rg = plan.n_rg;
+    g.ctas = plan.ctas;
+    g.sm_scale = sm_scale;
+    g.wait_limit = pr->wait_limit;
+    g.drain_limit = kWaitLimitCycles;
+  }
   if (ids && B > 0) {
-    s.ws_ml = reinterpret_cast<float *>(wsb + sparse.lay.ml_off);
-    s.ws_o = reinterpret_cast<float *>(wsb + sparse.lay.o_off);
-    s.plan_tab = reinterpret_cast<int2 *>(wsb + sparse.lay.tab_off);
-    c.ws_ml = s.ws_ml;
-    c.ws_o = s.ws_o;
-    c.plan_tab = s.plan_tab;
-    BlockStream *rec = reinterpret_cast<BlockStream *>(wsb + sparse.rec_off);
-    BlockEntry *list = reinterpret_cast<BlockEntry *>(wsb + sparse.list_off);
-    s.bs.streams = rec;
-    s.bs.list = list;
-    s.bs.list_cap = (int32_t)sparse.list_cap;
-    s.T = c.T = sparse.T;
-    s.P = sparse.P;
-    s.dev_plan = c.dev_plan = sparse.dev_plan ? 1 : 0;
-    s.t_from_len = c.t_from_len = sparse.dev_plan ? 0 : 1;
-    s.plan_G = sparse.G;
-    c.plan_G = sparse.dev_plan ? sparse.G : (int32_t)(sparse.streams * sparse.P);  // slots in use
-    c.P = sparse.dev_plan ? sparse.G : sparse.P;
-    c.sparse = 1;
+    SegParams &g = pr->gp;
+    BlockStream *rec = reinterpret_cast<BlockStream *>(wsb + plan.rec_off);
+    BlockEntry *list = reinterpret_cast<BlockEntry *>(wsb + plan.list_off);
+    g.streams = rec;
+    g.list = list;
+    g.list_cap = (int32_t)plan.list_cap;
+    // a stream's record starts with its (tokens, queries) pair
+    g.pairs = reinterpret_cast<const int32_t *>(rec);
+    g.pair_sb = sizeof(BlockStream) / sizeof(int32_t);
+    g.has_qlen = 1;
+    g.groups = (int32_t)plan.streams;
+    g.unit_heads = 1;
+    g.capacity = (int32_t)(plan.list_cap * blk);
 
     ListParams &l = pr->lp;
     memset(&l, 0, sizeof(l));
@@ -552,14 +601,15 @@ inline int prepare(const vae4_tensor *q, const vae4_tensor *kv, const vae4_tenso
     l.seq = s.seq;
     l.seq_sb = s.seq_sb;
     l.seq_has_qlen = s.seq_has_qlen;
-    l.scales = s.bs.scales;
-    l.s_page = s.bs.s_page;
-    l.s_kv = s.bs.s_kv;
-    l.s_head = s.bs.s_head;
+    l.scales = g.scales;
+    l.s_page = g.s_page;
+    l.s_kv = g.s_kv;
+    l.s_head = g.s_head;
     l.n_pages = s.n_pages;
     l.list = list;
     l.streams = rec;
-    l.tab = s.plan_tab;
+    l.tab = g.tab;
+    l.n_rg = g.n_rg;
     l.status = s.status;
     l.B = s.B;
     l.Qmax = s.Qmax;
@@ -567,7 +617,7 @@ inline int prepare(const vae4_tensor *q, const vae4_tensor *kv, const vae4_tenso
     l.page = s.page;
     l.blk = (int32_t)blk;
     l.capacity = s.capacity;
-    l.list_cap = s.bs.list_cap;
+    l.list_cap = g.list_cap;
     l.alpha = sm_scale * 1.4426950408889634f;
   }
   return VAE4_OK;

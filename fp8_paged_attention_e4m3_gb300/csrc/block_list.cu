@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kListThreads) block_list_kernel(const ListPara
       s.L = L;
     }
     p.streams[stream] = s;
-    p.tab[stream] = make_int2(0, 0);
+    for (int r = 0; r < p.n_rg; ++r) p.tab[stream * p.n_rg + r] = make_int2(0, 0);
   }
 }
 

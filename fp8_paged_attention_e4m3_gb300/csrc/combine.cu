@@ -80,22 +80,16 @@ __global__ void __launch_bounds__(kRowThreads) combine_rows_kernel(const Combine
   const int L = p.seq[(int64_t)b * p.seq_sb];
   const int ql = p.seq_has_qlen ? p.seq[(int64_t)b * p.seq_sb + 1] : p.Qmax;
   // partitions of this (sequence, KV head): slots slot0 .. slot0 + nP - 1
-  int slot0 = (b * p.Hkv + h) * p.P;
+  const int slot0 = (b * p.Hkv + h) * p.P;
   const int T = (p.t_from_len && L > 0 && L <= p.capacity) ? max(64, plan_t_from_len(L, p.P)) : p.T;
   const bool dead = L <= 0 || L > p.capacity || ql < 0 || ql > p.Qmax || ql > L || i >= ql;
-  int nP = dead ? 0 : (L + T - 1) / T;
-  // the head's V scale (an input); none if the weights carry block scales
-  const float sv = p.scales ? __ldg(p.scales + h * p.scale_sh + 1) : 1.f;
+  const int nP = dead ? 0 : (L + T - 1) / T;
+  const float sv = __ldg(p.scales + h * p.scale_sh + 1);  // the head's V scale (an input)
   // wait until the split kernel's partials are complete and visible
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) {  // invalid lengths, once per sequence
     if (L < 0 || L > p.capacity) atomicOr(p.status, VAE4_STATUS_BAD_LENGTH);
     else if (ql < 0 || ql > p.Qmax || (L > 0 && ql > L)) atomicOr(p.status, VAE4_STATUS_BAD_QLEN);
-  }
-  if (p.sparse && !dead) {  // partitions of the stream's visit list
-    const int2 e = p.plan_tab[b * p.Hkv + h];
-    slot0 = e.x;
-    nP = min(e.y, p.P);
   }
   const RowScratch sc{rsm, rsm + p.P, red, accs};
   combine_row_unit(p, b, h, r, dsl, slot0, nP, sv, threadIdx.x, 0, sc);
@@ -123,7 +117,7 @@ __global__ void __launch_bounds__(kCombineThreads, 2) combine_kernel(const Combi
   __shared__ int wsum[kWarps];
   const int nb_cache = p.B <= kCacheB ? p.B : 0;
   int2 *lens = reinterpret_cast<int2 *>(csm);  // (L, q_len) per sequence
-  const int ntab = ((p.dev_plan || p.sparse) && p.B * p.Hkv <= kCacheTab) ? p.B * p.Hkv : 0;
+  const int ntab = (p.dev_plan && p.B * p.Hkv <= kCacheTab) ? p.B * p.Hkv : 0;
   int2 *tab = lens + nb_cache;                          // (first slot, partitions)
   int *ustart = reinterpret_cast<int *>(tab + ntab);    // first live unit per sequence
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -259,7 +253,7 @@ __global__ void __launch_bounds__(kCombineThreads, 2) combine_kernel(const Combi
     const int i = r / p.G, gg = r - i * p.G;
     // partitions of this (sequence, KV head): slots slot0 .. slot0 + nP - 1
     int slot0 = 0, nP = 0;
-    if (!p.dev_plan && !p.sparse) {
+    if (!p.dev_plan) {
       slot0 = (b * p.Hkv + h) * p.P;
       const int T = p.t_from_len ? max(64, plan_t_from_len(l.L, p.P)) : p.T;
       nP = (l.L + T - 1) / T;
@@ -267,8 +261,7 @@ __global__ void __launch_bounds__(kCombineThreads, 2) combine_kernel(const Combi
       const int2 e = b * p.Hkv + h < ntab ? tab[b * p.Hkv + h] : p.plan_tab[b * p.Hkv + h];
       slot0 = e.x;
       nP = e.y;
-      // (a stream of sparse attention may have nothing to visit)
-      if (slot0 < 0 || nP < (p.sparse ? 0 : 1) || nP > p.P || slot0 + nP > p.plan_G) {  // never: a library bug
+      if (slot0 < 0 || nP < 1 || nP > p.P || slot0 + nP > p.plan_G) {  // never: a library bug
         if (lane == 0) atomicOr(p.status, VAE4_STATUS_PLAN);
         nP = 0;
       }
@@ -279,7 +272,7 @@ __global__ void __launch_bounds__(kCombineThreads, 2) combine_kernel(const Combi
     const int64_t ostride = pstride * p.D;
 
     // the head's V scale, requested with the partials (not after them)
-    const float sv = p.scales ? __ldg(p.scales + h * p.scale_sh + 1) : 1.f;
+    const float sv = __ldg(p.scales + h * p.scale_sh + 1);
     float M = kNegInf, lam = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     bool bad = false;
@@ -408,7 +401,7 @@ cudaError_t launch_combine(const CombineParams &p, cudaStream_t stream) {
   cfg.gridDim = dim3((unsigned)nblk, 1, 1);
   cfg.blockDim = dim3(kCombineThreads);
   const int nb_cache = p.B <= kCacheB ? p.B : 0;
-  const int ntab = ((p.dev_plan || p.sparse) && p.B * p.Hkv <= kCacheTab) ? p.B * p.Hkv : 0;
+  const int ntab = (p.dev_plan && p.B * p.Hkv <= kCacheTab) ? p.B * p.Hkv : 0;
   // lengths, stream table, first live unit per sequence
   cfg.dynamicSmemBytes = (size_t)(nb_cache + ntab) * sizeof(int2) +
                          (size_t)(nb_cache + 1) * sizeof(int);

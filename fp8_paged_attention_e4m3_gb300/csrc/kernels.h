@@ -40,6 +40,9 @@ cudaError_t launch_block_scores(const ScoreParams &p, bool e5m2, cudaStream_t st
 cudaError_t launch_select_blocks(const SelectParams &p, cudaStream_t stream);
 constexpr int kMaxListBlocks = 98304;  // blocks of a sequence sparse attention can list
 cudaError_t launch_block_list(const ListParams &p, cudaStream_t stream);
+// Attention over a block-scaled cache: split kernel and combine.
+cudaError_t launch_seg(const SegParams &p, cudaStream_t stream);
+cudaError_t launch_seg_combine(const SegParams &p, cudaStream_t stream);
 
 // Decode-table test hook.
 cudaError_t launch_decode_table(uint16_t *out, bool integer_path, bool e5m2,

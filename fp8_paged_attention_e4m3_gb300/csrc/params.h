@@ -35,16 +35,45 @@ struct alignas(16) BlockStream {
   int32_t L;    // the sequence's length
 };
 
-// Block-scaled caches: what the attention kernels need beyond SplitParams.
-struct BlockScaled {
-  const float *scales;           // f32 [n_pages][2][Hkv][page / blk]
-  int64_t s_page, s_kv, s_head;  // strides in elements
-  int32_t blk;                   // tokens per scale (a multiple of 16 that divides the page)
-  // sparse attention (list != null): the visit lists of the streams
-  const BlockEntry *list;        // [B * Hkv][list_cap]
-  const BlockStream *streams;    // [B * Hkv]
+// Attention over a block-scaled cache: the split kernel and its combine.
+// Strides are in elements (bytes for the caches).
+struct SegParams {
+  const void *q;               // fp16 [B][Qmax][Hq][D]
+  int64_t q_sb, q_si, q_sh;
+  void *out;                   // the same shape
+  int64_t o_sb, o_si, o_sh;
+  // token t of KV head h in page ph: base + ph * ps + (t % page) * ts + h * hs
+  const uint8_t *k_base, *v_base;
+  int64_t k_ps, k_ts, k_hs, v_ps, v_ts, v_hs;
+  int64_t n_pages;
+  int32_t cpasync;             // strides are multiples of 8 but not all of 16 (8-byte copies)
+  int32_t box_log2;            // log2 of the keys per tensor copy (4, 5 or 6)
+  const int32_t *bt;
+  int64_t bt_sb;
+  int32_t max_pages;
+  const int32_t *seq;          // i32 [B] or [B][2]
+  int32_t seq_sb, seq_has_qlen;
+  int32_t seq_capacity;        // most tokens of a sequence
+  const float *scales;         // f32 [n_pages][2][Hkv][page / blk]
+  int64_t s_page, s_kv, s_head;
+  int32_t blk;
+  // groups of units: the sequences (unit_heads = Hkv), or sparse attention's
+  // streams (unit_heads = 1), with their (tokens, queries) pairs
+  const int32_t *pairs;
+  int32_t pair_sb, has_qlen, groups, unit_heads, capacity;
+  const BlockEntry *list;      // sparse: [B * Hkv][list_cap], else null
+  const BlockStream *streams;  // sparse: [B * Hkv]
   int32_t list_cap;
-  int32_t heads;                 // KV heads per sequence (stream = sequence * heads + head)
+  float *ws_ml;                // f32 [2 ctas][N][2]
+  float *ws_o;                 // f32 [2 ctas][N][D]
+  int2 *tab;                   // (first CTA, parts) [B * Hkv][n_rg]
+  uint32_t *status;
+  int32_t B, Qmax, Hkv, G, D, page, e5m2;
+  int32_t N, n_rg;             // rows per unit, row groups
+  int32_t ctas;
+  float sm_scale;
+  long long wait_limit;        // SM cycles before a pipeline wait gives up
+  long long drain_limit;       // SM cycles the wind-down waits for copies and MMAs in flight
 };
 
 // The visit-list kernel's parameters.
@@ -62,7 +91,8 @@ struct ListParams {
   int64_t n_pages;
   BlockEntry *list;
   BlockStream *streams;
-  int2 *tab;                     // (first slot, partitions) per stream, cleared here
+  int2 *tab;                     // (first CTA, parts) [B * Hkv][n_rg], cleared here
+  int32_t n_rg;
   uint32_t *status;
   int32_t B, Qmax, Hkv, page, blk, capacity, list_cap;
   float alpha;                   // softmax_scale * log2(e)
@@ -164,7 +194,6 @@ struct SplitParams {
   int32_t plan_W_guess, plan_np_guess;  // device plan when every L is the capacity
   int32_t t_from_len;   // static grid: T = max(64, ceil16(L / P)) per sequence
   int32_t hilo;         // 1: P enters the value product as FP16 high + residual
-  BlockScaled bs;       // block-scaled caches (bs.scales != null); `scales` is null then
 };
 
 // The combine kernel's parameters.
@@ -185,7 +214,6 @@ struct CombineParams {
   int32_t t_from_len;        // static grid, T from each sequence's length
   uint32_t *status;
   int32_t num_sms;           // SMs the grid is sized for
-  int32_t sparse;            // partitions per stream from plan_tab, possibly none
 };
 
 // The bridge kernel's parameters (paged FP8 -> dense FP16 K and V).

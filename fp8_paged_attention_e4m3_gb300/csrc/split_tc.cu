@@ -111,22 +111,6 @@ cudaError_t launch_split_tc(const SplitParams &p_in, long long wait_limit, cudaS
       encode_cache_map(&map_k, p.k_base, p.k_ps, p.k_ts, p.k_hs, p) &&
       encode_cache_map(&map_v, p.v_base, p.v_ps, p.v_ts, p.v_hs, p))
     p.kv_cpasync = 0;
-  if (p.bs.list) {
-    // a stream (sequence, KV head) is a sequence with one KV head to the plan;
-    // its record starts with the (length, queries) pair that the plan reads
-    p.bs.heads = p.Hkv;
-    p.B *= p.Hkv;
-    p.Hkv = 1;
-    p.seq = reinterpret_cast<const int32_t *>(p.bs.streams);
-    p.seq_sb = sizeof(BlockStream) / sizeof(int32_t);
-    p.seq_has_qlen = 1;
-    p.capacity = p.bs.list_cap * p.bs.blk;
-    return p.dev_plan ? launch_split_tc_listed_dev(p, a, n, map_k, map_v, stream)
-                      : launch_split_tc_listed_len(p, a, n, map_k, map_v, stream);
-  }
-  if (p.bs.scales)
-    return p.dev_plan ? launch_split_tc_dense_dev(p, a, n, map_k, map_v, stream)
-                      : launch_split_tc_dense_len(p, a, n, map_k, map_v, stream);
   if (p.dev_plan) return launch_split_tc_dev(p, a, n, map_k, map_v, stream);
   if (p.t_from_len) return launch_split_tc_len(p, a, n, map_k, map_v, stream);
   return p.hilo ? launch_tc_any<kPlanFixed, true>(p, a, n, map_k, map_v, stream)

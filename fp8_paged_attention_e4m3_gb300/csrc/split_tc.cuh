@@ -49,21 +49,6 @@
 // Add opt-in E4M3 grouped attention with FP32 partials", final status).  Keys are visited in ascending logical
 // order, so the result does not depend on where pages live.
 //
-// Block-scaled caches (BM): a key's block has its own s_K and s_V.  The
-// softmax threads own keys, so both cost one multiply-add per score: with
-// t = alpha (q . dec(K)) the score in log2 units (alpha holds s_K) and
-// g = log2 s_V, a key's weight is w = 2^(t + g - m), m the running maximum
-// of t + g.  P holds w, so O accumulates e^z s_V dec(V), and the row sums add
-// w / s_V in FP32 before the rounding to FP16, so O / l is the result for any
-// m, however far apart the blocks' scales are (within 2^-40 .. 2^40 no w or
-// sum overflows).  Each thread fetches its key's scales a tile ahead, and the
-// page id that leads to them two tiles ahead.
-//   kDense: the sequence's keys; kListed: sparse attention.  The CTA then
-// walks the blocks of a stream's visit list, one after another as if they
-// were a sequence (a stream is a sequence with one KV head to the plan); a
-// list entry gives the block's page, its first token for the causal mask, a
-// bit per query that attends to it, and its scales.
-//
 // Every mbarrier wait is bounded; on expiry the CTA raises an abort flag,
 // every role winds down, outstanding copies and MMAs are drained, TMEM is
 // freed and the partition is marked invalid (sum = -1, status TIMEOUT).
@@ -161,7 +146,7 @@ enum : int {
 // kDevPlanMaxB sequences from byte 0, the published plan at byte kPlanSh
 constexpr int kPlanSh = 12288;
 // offsets in the small region (the mbarriers occupy its first 512 bytes)
-constexpr int kSmTslot = 512, kSmAbort = 516, kSmBad = 520, kSmBadScale = 524, kSmCta = 544, kSmM = 576,
+constexpr int kSmTslot = 512, kSmAbort = 516, kSmBad = 520, kSmCta = 544, kSmM = 576,
               kSmPos = 832, kSmMNew = 1088, kSmBase = 1344, kSmThr = 1600,
               kSmRed = 1856;  // red: 8 warps x 32 floats, ends at 2880
 
@@ -188,33 +173,6 @@ static __device__ __noinline__ void zero_v_tail(uint8_t *raw, int kz, int dq, in
   __syncwarp();
 }
 
-// Which keys a split CTA walks and where their scales are.
-enum { kHeadScaled = 0, kDense = 1, kListed = 2 };
-
-// One batch of the block table (kListed: of the visit list) per lane: the
-// physical page and the first 16-token box of the entry in it.
-struct PageWin {
-  int page, box0;
-};
-template <int BM>
-__device__ __forceinline__ PageWin fetch_page(const SplitParams &p, const int32_t *btb,
-                                              const BlockEntry *list, int lp) {
-  if constexpr (BM == kListed) {
-    if (lp >= p.bs.list_cap) return PageWin{-1, 0};
-    const int2 e = __ldg(reinterpret_cast<const int2 *>(list + lp));
-    return PageWin{e.x, e.y};
-  } else {
-    return PageWin{lp < p.max_pages ? __ldg(btb + lp) : -1, 0};
-  }
-}
-
-// The softmax's view of one key of a block-scaled cache.
-struct KeyScale {
-  float alpha, lgv, inv_sv;  // softmax_scale s_K log2(e), log2 s_V, 1 / s_V
-  int pos;                   // position in the sequence
-  uint32_t mask;             // queries that attend to it (kListed)
-};
-
 // Producer of one ring (K or V) for caches whose strides are multiples of 8
 // bytes but not all of 16 (the pages' 264-byte token stride, PR #524
 // "[Kernel][SM70] Add opt-in E4M3 grouped attention with FP32 partials", AI
@@ -224,13 +182,13 @@ struct KeyScale {
 // on the slot's "full" barrier (32 arrivals per phase).  Keys past the
 // partition and pages with invalid ids are zero-filled.  Out of line: the
 // tensor-load producer is the hot path.  Returns the half-tiles issued.
-template <int D, int BM>
+template <int D>
 static __device__ __noinline__ int cpa_produce(const SplitParams &p, int h, int k0, int k1,
                                                int nhalf, bool isv, uint32_t ring, uint32_t full0,
                                                uint32_t empty0, int nslot, volatile int *abort_f,
-                                               long long lim, volatile int *bad_f, PageWin cur,
-                                               PageWin nxt, int lp_base, const int32_t *btb,
-                                               const BlockEntry *list, int lane) {
+                                               long long lim, volatile int *bad_f, int cur,
+                                               int nxt, int lp_base, const int32_t *btb,
+                                               int lane) {
   constexpr int IB = D < 128 ? D : 128, SMASK = IB == 128 ? 7 : 3;
   constexpr int CPK = D / 8, KPI = 32 / CPK;  // 8-byte chunks per key, keys per instruction
   constexpr int RSLOT = 64 * D;
@@ -239,7 +197,7 @@ static __device__ __noinline__ int cpa_produce(const SplitParams &p, int h, int 
   const uint64_t pol = tc::l2_evict_first_policy();
   const int c = lane % CPK, kk = lane / CPK;
   const int dh = (8 * c) / IB, cb = (8 * c) % IB;  // this lane's chunk: IB block, byte in it
-  const int ppb = (BM == kListed ? p.bs.blk : p.page) >> 4;
+  const int ppb = p.page >> 4;
   const int box0 = (k0 >> 4) + lane;  // lane g < 4: box g of the first half-tile
   int lpg = box0 / ppb, sbg = box0 - lpg * ppb;
   int st = 0, u = 0, n_issued = 0;
@@ -247,14 +205,8 @@ static __device__ __noinline__ int cpa_produce(const SplitParams &p, int h, int 
     if (u > 0 && !tc::mbar_wait(empty0 + 8u * st, (u - 1) & 1, abort_f, lim)) break;
     n_issued = t + 1;
     const int rel = lpg - lp_base;
-    const int pc = __shfl_sync(0xffffffffu, cur.page, rel & 31);
-    const int pn = __shfl_sync(0xffffffffu, nxt.page, rel & 31);
-    int sbp = sbg;  // box within the page
-    if constexpr (BM == kListed) {
-      const int bc = __shfl_sync(0xffffffffu, cur.box0, rel & 31);
-      const int bn = __shfl_sync(0xffffffffu, nxt.box0, rel & 31);
-      sbp += rel < 32 ? bc : bn;
-    }
+    const int pc = __shfl_sync(0xffffffffu, cur, rel & 31);
+    const int pn = __shfl_sync(0xffffffffu, nxt, rel & 31);
     int phys = -1;  // lanes 0-3: page of box `lane`, -1 = zero fill
     if (lane < 4 && k0 + 64 * t + 16 * lane < k1) {
       const int ph = rel < 32 ? pc : pn;
@@ -267,7 +219,7 @@ static __device__ __noinline__ int cpa_produce(const SplitParams &p, int h, int 
 #pragma unroll 1
     for (int g = 0; g < 4; ++g) {
       const int pg = __shfl_sync(0xffffffffu, phys, g);
-      const int sb = __shfl_sync(0xffffffffu, sbp, g);
+      const int sb = __shfl_sync(0xffffffffu, sbg, g);
       const int key0 = k0 + 64 * t + 16 * g;  // first key of box g
       const uint8_t *src = hbase + (int64_t)max(pg, 0) * ps + (int64_t)(16 * sb + kk) * ts + 8 * c;
 #pragma unroll
@@ -292,7 +244,8 @@ static __device__ __noinline__ int cpa_produce(const SplitParams &p, int h, int 
     if (__shfl_sync(0xffffffffu, lpg, 0) >= lp_base + 32) {  // slide the window
       cur = nxt;
       lp_base += 32;
-      nxt = fetch_page<BM>(p, btb, list, lp_base + 32 + lane);
+      const int lp = lp_base + 32 + lane;
+      nxt = lp < p.max_pages ? __ldg(btb + lp) : -1;
     }
     if (++st == nslot) {
       st = 0;
@@ -308,12 +261,11 @@ static __device__ __noinline__ int cpa_produce(const SplitParams &p, int h, int 
 // plan of one sequence); kPlanDevice: the device-side balanced plan
 // (grid.x = partition number, grid.y = row group).
 enum { kPlanFixed = 0, kPlanFromLen = 1, kPlanDevice = 2 };
-template <int D, int N, int MODE, bool HL, int BM>
+template <int D, int N, int MODE, bool HL>
 __global__ void __launch_bounds__(TcCfg<D, N, HL>::NTHREADS, 1)
     split_tc_kernel(const SplitParams p, const TcArgs a, const __grid_constant__ CUtensorMap tmap_k,
                     const __grid_constant__ CUtensorMap tmap_v) {
   using C = TcCfg<D, N, HL>;
-  static_assert(BM == kHeadScaled || !HL, "block scales: one FP16 P");
   constexpr int kKFull = C::B_KFULL, kKEmpty = C::B_KEMPTY, kVFull = C::B_VFULL,
                 kVEmpty = C::B_VEMPTY, kKReady = C::B_KREADY, kKFree = C::B_KFREE,
                 kVReady = C::B_VREADY, kVFree = C::B_VFREE, kSFull = C::B_SFULL,
@@ -349,12 +301,11 @@ __global__ void __launch_bounds__(TcCfg<D, N, HL>::NTHREADS, 1)
   auto bar = [&](int i) -> uint32_t { return sSm + 8u * (uint32_t)i; };
   volatile int *abort_f = reinterpret_cast<volatile int *>(gSm + kSmAbort);
   volatile int *bad_f = reinterpret_cast<volatile int *>(gSm + kSmBad);
-  volatile int *bads_f = reinterpret_cast<volatile int *>(gSm + kSmBadScale);
   float *m_s = reinterpret_cast<float *>(gSm + kSmM);      // running max (log2 units)
   int *pos_s = reinterpret_cast<int *>(gSm + kSmPos);      // last visible key per row
   float *mnew_s = reinterpret_cast<float *>(gSm + kSmMNew);
   float *base_s = reinterpret_cast<float *>(gSm + kSmBase);  // m, or 0 while m = -inf
-  float *thr_s = reinterpret_cast<float *>(gSm + kSmThr);    // (m + tau) / alpha; BM: m + tau
+  float *thr_s = reinterpret_cast<float *>(gSm + kSmThr);    // (m + tau) / alpha
   float *red = reinterpret_cast<float *>(gSm + kSmRed);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -383,7 +334,6 @@ __global__ void __launch_bounds__(TcCfg<D, N, HL>::NTHREADS, 1)
     }
     *abort_f = 0;
     *bad_f = 0;
-    *bads_f = 0;
   }
   if (producer && lane == 0 && !p.kv_cpasync)  // kernel parameters
     tc::prefetch_tensormap(warp == kWVProd ? &tmap_v : &tmap_k);
@@ -415,16 +365,13 @@ __global__ void __launch_bounds__(TcCfg<D, N, HL>::NTHREADS, 1)
   // entries past the row are -1, entries past the sequence are loaded but
   // never used.
   int part, b, h, T, L, ql;
-  PageWin cur{-1, 0}, nxt{-1, 0};
-  int lp_base = 0;
+  int cur = -1, nxt = -1, lp_base = 0;
   const int32_t *btb = p.bt;
-  const BlockEntry *list = nullptr;  // kListed: the stream's
-  auto fetch = [&](int lp) -> PageWin { return fetch_page<BM>(p, btb, list, lp); };
+  auto fetch = [&](int lp) -> int { return lp < p.max_pages ? __ldg(btb + lp) : -1; };
   auto fetch_bt = [&](int bb, int k0_) {
-    if constexpr (BM == kListed) list = p.bs.list + (int64_t)bb * p.bs.list_cap;
     if (producer) {
-      if constexpr (BM != kListed) btb = p.bt + (int64_t)bb * p.bt_sb;
-      lp_base = k0_ / (BM == kListed ? p.bs.blk : p.page);  // any multiple of 16
+      btb = p.bt + (int64_t)bb * p.bt_sb;
+      lp_base = k0_ / p.page;  // any page size that is a multiple of 16
       cur = fetch(lp_base + lane);
       nxt = fetch(lp_base + 32 + lane);
     }
@@ -437,15 +384,11 @@ __global__ void __launch_bounds__(TcCfg<D, N, HL>::NTHREADS, 1)
     // fetch again if not.
     // (at the capacity every sequence keeps the same row groups, so CTA c
     // serves partition c mod the plan's partition count)
-    int bg = -1, k0g = 0;
-    if constexpr (BM != kListed) {  // (the lists' lengths cannot be guessed)
-      const int npg = p.plan_np_guess;
-      const int xg = (int)(blockIdx.x % (unsigned)(p.B * p.Hkv * npg));
-      const int xs = xg / npg;  // stream of the guess
-      bg = xs / p.Hkv;
-      k0g = (xg - xs * npg) * p.plan_W_guess;
-      if (bg < p.B) fetch_bt(bg, k0g);
-    }
+    const int npg = p.plan_np_guess;
+    const int xg = (int)(blockIdx.x % (unsigned)(p.B * p.Hkv * npg));
+    const int xs = xg / npg;  // stream of the guess
+    const int bg = xs / p.Hkv, k0g = (xg - xs * npg) * p.plan_W_guess;
+    if (bg < p.B) fetch_bt(bg, k0g);
     // The K producer warp evaluates the plan and passes it on through the
     // P^T buffer, unused until the first tile: the (L, q_len) pairs of the
     // batch staged at its start, then b, h, p, W, L and q_len of sequence b
@@ -495,14 +438,8 @@ __global__ void __launch_bounds__(TcCfg<D, N, HL>::NTHREADS, 1)
       // read once the length is known (fetching the window of the plan at
       // the capacity first, with a second fetch on a miss, measured no
       // earlier first data and a slightly slower kernel)
-      // (block-scaled caches run explicit lengths here too)
-      if (L > 0 && L <= p.capacity && (BM == kHeadScaled || p.t_from_len))
-        T = max(64, plan_t_from_len(L, p.P));
+      if (L > 0 && L <= p.capacity) T = max(64, plan_t_from_len(L, p.P));
       fetch_bt(b, part * T);
-      if constexpr (BM == kListed) {  // the stream's partitions, for the combine
-        if (part == 0 && blockIdx.y == 0 && tid == 0)
-          p.plan_tab[b] = make_int2(b * p.P, L > 0 && L <= p.capacity ? (L + T - 1) / T : 0);
-      }
     }
   }
   // row group and workspace slot: from the CTA index (static grids) or
@@ -540,16 +477,7 @@ __global__ void __launch_bounds__(TcCfg<D, N, HL>::NTHREADS, 1)
     leave();
     return;
   }
-  // kListed: b is a stream and L the (rounded) length of its list so far
-  int bq = b, Lk = L;
-  if constexpr (BM == kListed) {
-    const BlockStream rec = p.bs.streams[b];
-    bq = b / p.bs.heads;
-    h = b - bq * p.bs.heads;
-    Lk = rec.n;
-    L = rec.L;
-  }
-  const int k1 = min(k0 + T, Lk);
+  const int k1 = min(k0 + T, L);
   const int ntiles = (k1 - k0 + 127) >> 7;
   const int nhalf = 2 * ntiles;  // half-tiles, the last may be all padding
 
@@ -561,7 +489,7 @@ __global__ void __launch_bounds__(TcCfg<D, N, HL>::NTHREADS, 1)
   constexpr int kSetup = C::NTHREADS - 64;  // every thread but the producers
   if (!producer) {
     const int st_id = tid < 32 * kWKProd ? tid : tid - 64;
-    const __half *qb = static_cast<const __half *>(p.q) + (int64_t)bq * p.q_sb;
+    const __half *qb = static_cast<const __half *>(p.q) + (int64_t)b * p.q_sb;
     constexpr int QCH = D / 8;  // 16-byte chunks per query row
     for (int c = st_id; c < N * QCH; c += kSetup) {
       const int r = c / QCH, cc = c - r * QCH;
@@ -600,14 +528,14 @@ __global__ void __launch_bounds__(TcCfg<D, N, HL>::NTHREADS, 1)
     // the KV stream is read once: keep it from pushing other data (the
     // partials the combine reads, the block table) out of L2
     const uint64_t pol = tc::l2_evict_first_policy();
-    const int ppb = (BM == kListed ? p.bs.blk : p.page) >> 4;  // 16-key boxes per page (block)
+    const int ppb = p.page >> 4;        // 16-key boxes per page
     const int box0 = (k0 >> 4) + lane;  // lane g < 4: box g of the first half-tile
     int lpg = box0 / ppb, sbg = box0 - lpg * ppb;
     const CUtensorMap *map = isv ? &tmap_v : &tmap_k;
     int st = 0, u = 0;  // ring slot and pass of half-tile t (t = u * nslot + st)
     if (p.kv_cpasync)
-      n_issued = cpa_produce<D, BM>(p, h, k0, k1, nhalf, isv, ring, bar(fullb), bar(emptyb), nslot,
-                                    abort_f, LIM, bad_f, cur, nxt, lp_base, btb, list, lane);
+      n_issued = cpa_produce<D>(p, h, k0, k1, nhalf, isv, ring, bar(fullb), bar(emptyb), nslot,
+                                abort_f, LIM, bad_f, cur, nxt, lp_base, btb, lane);
     // V, consumed a chain after K, starts ~0.6 us later (a fixed pause),
     // so K's first tile lands sooner (long step -0.2 us, ragged split -0.4)
     if (isv && !p.kv_cpasync) {
@@ -622,14 +550,8 @@ __global__ void __launch_bounds__(TcCfg<D, N, HL>::NTHREADS, 1)
       // block-table window: lane 0's page is in [lp_base, lp_base + 32) and
       // the others' at most 3 pages on, so every box finds its id in cur/nxt
       const int rel = lpg - lp_base;
-      const int pc = __shfl_sync(0xffffffffu, cur.page, rel & 31);
-      const int pn = __shfl_sync(0xffffffffu, nxt.page, rel & 31);
-      int sbp = sbg;  // box within the page
-      if constexpr (BM == kListed) {
-        const int bc = __shfl_sync(0xffffffffu, cur.box0, rel & 31);
-        const int bn = __shfl_sync(0xffffffffu, nxt.box0, rel & 31);
-        sbp += rel < 32 ? bc : bn;
-      }
+      const int pc = __shfl_sync(0xffffffffu, cur, rel & 31);
+      const int pn = __shfl_sync(0xffffffffu, nxt, rel & 31);
       if (lane < 4) {
         const int phys = rel < 32 ? pc : pn;
         int pgc = (int)p.n_pages;  // outside the tensor: zero fill
@@ -641,7 +563,7 @@ __global__ void __launch_bounds__(TcCfg<D, N, HL>::NTHREADS, 1)
         }
         // one box: 16 keys x D bytes of head h, as NDH blocks of 16 x IB
         // (swizzled); coordinates (byte, token in page, block, head, page)
-        tc::tma_load_5d_hint(ring + st * C::RSLOT + lane * (16 * D), map, 0, 16 * sbp, 0, h, pgc,
+        tc::tma_load_5d_hint(ring + st * C::RSLOT + lane * (16 * D), map, 0, 16 * sbg, 0, h, pgc,
                              bar(fullb + st), pol);
       }
       if (ppb == 1) {
@@ -867,8 +789,7 @@ __global__ void __launch_bounds__(TcCfg<D, N, HL>::NTHREADS, 1)
     const int col0 = cg * C::NC;
     const uint32_t lane_off = (uint32_t)(32 * q) << 16;
     // K holds dec(b) exactly; t = S * alpha is the score in log2 units
-    float alpha = 0.f;
-    if constexpr (BM == kHeadScaled) alpha = p.sm_scale * p.scales[h * p.scale_sh] * kLog2e;
+    const float alpha = p.sm_scale * p.scales[h * p.scale_sh] * kLog2e;
     // every real row sees keys 0 .. L - q_len; padding rows have zero
     // queries (finite, never output), so only tiles past that key or past
     // the partition end need the per-row mask
@@ -878,109 +799,9 @@ __global__ void __launch_bounds__(TcCfg<D, N, HL>::NTHREADS, 1)
 #pragma unroll
     for (int c = 0; c < C::NC; ++c) lpart[c] = 0.f;
     bool alive = true;
-    // block scales: this thread's key of the next tile to fetch, as (unit,
-    // token in the unit), a unit being a page (kDense) or a list entry, and
-    // for kDense its block in the sequence likewise; advanced by 128 keys
-    // without a division
-    KeyScale ks{0.f, 0.f, 1.f, 0, 0xFFFFu};
-    int f_unit = 0, f_off = 0, f_blk = 0, f_boff = 0, f_key = 0, page1 = -1;
-    const int f_size = BM == kListed ? p.bs.blk : p.page;
-    const uint32_t all_queries = (1u << ql) - 1u;
-    auto fetch_next = [&]() {  // the key 128 on
-      f_key += 128;
-      f_unit += 128 / f_size;
-      f_off += 128 % f_size;
-      if (f_off >= f_size) {
-        f_off -= f_size;
-        ++f_unit;
-      }
-      if constexpr (BM == kDense) {
-        f_blk += 128 / p.bs.blk;
-        f_boff += 128 % p.bs.blk;
-        if (f_boff >= p.bs.blk) {
-          f_boff -= p.bs.blk;
-          ++f_blk;
-        }
-      }
-    };
-    auto load_page = [&](int key, int unit) -> int {
-      if constexpr (BM == kDense)
-        return key < k1 ? __ldg(p.bt + (int64_t)b * p.bt_sb + unit) : -1;
-      else
-        return -1;
-    };
-    // raw scales (kDense: s_K, s_V) or the entry's (kListed) of one key
-    struct Raw {
-      float4 f;
-      int2 e;
-      bool ok;
-    };
-    const int nb_page = BM == kDense ? p.page / p.bs.blk : 1;
-    auto load_scales = [&](int key, int unit, int blk, int page) -> Raw {
-      Raw r{make_float4(0.f, 0.f, 1.f, 0.f), make_int2(0, 0), false};
-      if constexpr (BM == kDense) {
-        if (key < k1 && page >= 0 && page < p.n_pages) {
-          const float *sp = p.bs.scales + (int64_t)page * p.bs.s_page + (int64_t)h * p.bs.s_head +
-                            (blk - unit * nb_page);
-          r.f.x = __ldg(sp);
-          r.f.y = __ldg(sp + p.bs.s_kv);
-          r.ok = true;
-        }
-      } else if constexpr (BM == kListed) {
-        if (key < k1) {
-          const BlockEntry *e = list + unit;
-          r.e = __ldg(reinterpret_cast<const int2 *>(&e->tok0));
-          r.f = __ldg(reinterpret_cast<const float4 *>(&e->alpha));
-          r.ok = true;
-        }
-      }
-      return r;
-    };
-    auto key_scale = [&](const Raw &r, int key, int off) {
-      ks = KeyScale{0.f, 0.f, 1.f, key, 0xFFFFu};
-      if constexpr (BM == kDense) {
-        if (r.ok) {
-          const float sk = r.f.x, sv = r.f.y;
-          if (sk >= kMinScale && sk <= kMaxScale && sv >= kMinScale && sv <= kMaxScale) {
-            ks.alpha = p.sm_scale * kLog2e * sk;
-            ks.lgv = __log2f(sv);
-            ks.inv_sv = __fdividef(1.f, sv);
-          } else {
-            *bads_f = 1;
-          }
-        }
-      } else if constexpr (BM == kListed) {
-        if (r.ok) {
-          ks.alpha = r.f.x;
-          ks.lgv = r.f.y;
-          ks.inv_sv = r.f.z;
-          ks.pos = r.e.x + off;
-          ks.mask = (uint32_t)r.e.y;
-        }
-      }
-    };
-    Raw raw{};
-    if constexpr (BM != kHeadScaled) {
-      f_key = k0 + 32 * q + lane;
-      f_unit = f_key / f_size;
-      f_off = f_key - f_unit * f_size;
-      if constexpr (BM == kDense) {
-        f_blk = f_key / p.bs.blk;
-        f_boff = f_key - f_blk * p.bs.blk;
-      }
-      const int page0 = load_page(f_key, f_unit);
-      raw = load_scales(f_key, f_unit, f_blk, page0);
-      page1 = load_page(f_key + 128, f_unit + 128 / f_size + (f_off + 128 % f_size >= f_size));
-    }
     for (int j = 0; j < ntiles; ++j) {
       const int buf = j & 1;
       float s[C::NC];
-      if constexpr (BM != kHeadScaled) {
-        key_scale(raw, f_key, f_off);
-        fetch_next();
-        raw = load_scales(f_key, f_unit, f_blk, page1);
-        page1 = load_page(f_key + 128, f_unit + 128 / f_size + (f_off + 128 % f_size >= f_size));
-      }
       alive = alive && tc::mbar_wait(bar(kSFull + buf), (j >> 1) & 1, abort_f, LIM);
       if (alive) {
         tc::tc_fence_after();
@@ -1001,26 +822,7 @@ __global__ void __launch_bounds__(TcCfg<D, N, HL>::NTHREADS, 1)
 
       const int key = k0 + 128 * j + 32 * q + lane;
       bool exceed = false;
-      if constexpr (BM != kHeadScaled) {  // t + g in the place of the raw score
-        if (key < k1 && ks.pos <= min_pos &&
-            (BM == kDense || (ks.mask & all_queries) == all_queries)) {
-#pragma unroll
-          for (int c = 0; c < C::NC; ++c) {
-            s[c] = fmaf(s[c], ks.alpha, ks.lgv);
-            exceed |= s[c] > thr_s[col0 + c];
-          }
-        } else {
-          const bool kvalid = key < k1;
-#pragma unroll
-          for (int c = 0; c < C::NC; ++c) {
-            const int ps = pos_s[col0 + c];  // of query ps - min_pos (-1: no query)
-            bool see = kvalid && ks.pos <= ps;
-            if constexpr (BM == kListed) see = see && ((ks.mask >> ((ps - min_pos) & 31)) & 1u);
-            s[c] = see ? fmaf(s[c], ks.alpha, ks.lgv) : -kInf;
-            exceed |= s[c] > thr_s[col0 + c];
-          }
-        }
-      } else if (key < k1 && key <= min_pos) {
+      if (key < k1 && key <= min_pos) {
 #pragma unroll
         for (int c = 0; c < C::NC; ++c) exceed |= s[c] > thr_s[col0 + c];
       } else {
@@ -1040,8 +842,7 @@ __global__ void __launch_bounds__(TcCfg<D, N, HL>::NTHREADS, 1)
           float mx = s[c];
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          if (lane == 0)  // -inf stays -inf
-            red[warp * 32 + c] = BM == kHeadScaled ? mx * alpha : mx;
+          if (lane == 0) red[warp * 32 + c] = mx * alpha;  // -inf stays -inf
         }
         tc::named_bar(1, nsm);
         if (q == 0 && lane < C::NC) {  // one warp per column group combines the quadrants
@@ -1087,7 +888,7 @@ __global__ void __launch_bounds__(TcCfg<D, N, HL>::NTHREADS, 1)
           const float mn = mnew_s[col0 + lane];
           m_s[col0 + lane] = mn;
           base_s[col0 + lane] = mn == -kInf ? 0.f : mn;
-          thr_s[col0 + lane] = BM == kHeadScaled ? (mn + kTau) / alpha : mn + kTau;
+          thr_s[col0 + lane] = (mn + kTau) / alpha;
         }
         tc::named_bar(1, nsm);  // new maxima visible
       }
@@ -1107,8 +908,8 @@ __global__ void __launch_bounds__(TcCfg<D, N, HL>::NTHREADS, 1)
             b0 += kHiLoExp;
             b1 += kHiLoExp;
           }
-          const float e0 = fast_exp2(BM == kHeadScaled ? fmaf(s[c], alpha, b0) : s[c] + b0);
-          const float e1 = fast_exp2(BM == kHeadScaled ? fmaf(s[c + 1], alpha, b1) : s[c + 1] + b1);
+          const float e0 = fast_exp2(fmaf(s[c], alpha, b0));
+          const float e1 = fast_exp2(fmaf(s[c + 1], alpha, b1));
           const __half2 hh = __floats2half2_rn(e0, e1);
           const float2 fl = __half22float2(hh);
           if constexpr (HL) {
@@ -1118,9 +919,6 @@ __global__ void __launch_bounds__(TcCfg<D, N, HL>::NTHREADS, 1)
             lpart[c] += fl.x + fr.x;
             lpart[c + 1] += fl.y + fr.y;
             lw[e] = *reinterpret_cast<const uint32_t *>(&ll);
-          } else if constexpr (BM != kHeadScaled) {
-            lpart[c] = fmaf(e0, ks.inv_sv, lpart[c]);
-            lpart[c + 1] = fmaf(e1, ks.inv_sv, lpart[c + 1]);
           } else {
             lpart[c] += fl.x;
             lpart[c + 1] += fl.y;
@@ -1215,18 +1013,10 @@ __global__ void __launch_bounds__(TcCfg<D, N, HL>::NTHREADS, 1)
   __syncthreads();
   tc::tc_fence_after();
   if (warp == kWQk) tc::tmem_dealloc(tbase, 512);
-  const bool aborted = *abort_f != 0;
-  bool bad = *bad_f != 0;
+  const bool aborted = *abort_f != 0, bad = *bad_f != 0;
   if (tid == 0) {
     if (aborted) atomicOr(p.status, VAE4_STATUS_TIMEOUT);
-    // (the visit list's writer has reported its pages and scales)
-    if (bad && BM != kListed) atomicOr(p.status, VAE4_STATUS_BAD_BLOCK);
-  }
-  if constexpr (BM == kDense) {
-    if (*bads_f != 0) {
-      bad = true;
-      if (tid == 0) atomicOr(p.status, VAE4_STATUS_BAD_SCALE);
-    }
+    if (bad) atomicOr(p.status, VAE4_STATUS_BAD_BLOCK);
   }
   if (tid < N) {
     const int r = tid, cg = r / C::NC, c = r - cg * C::NC;
@@ -1242,7 +1032,7 @@ __global__ void __launch_bounds__(TcCfg<D, N, HL>::NTHREADS, 1)
 
 // ---------------------------------------------------------------------------
 // Host side: launch of one instantiation.
-template <int D, int N, int MODE, bool HL, int BM>
+template <int D, int N, int MODE, bool HL>
 cudaError_t launch_tc(const SplitParams &p, const TcArgs &a, const CUtensorMap &map_k,
                       const CUtensorMap &map_v, cudaStream_t stream) {
   using C = TcCfg<D, N, HL>;
@@ -1256,7 +1046,7 @@ cudaError_t launch_tc(const SplitParams &p, const TcArgs &a, const CUtensorMap &
   const unsigned long long ctx = current_context_id();
   if (dev < 0 || dev >= kDevs || ctx == 0 ||
       configured[dev].load(std::memory_order_acquire) != ctx) {
-    cudaError_t e = cudaFuncSetAttribute(split_tc_kernel<D, N, MODE, HL, BM>,
+    cudaError_t e = cudaFuncSetAttribute(split_tc_kernel<D, N, MODE, HL>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < kDevs) configured[dev].store(current_context_id(), std::memory_order_release);
@@ -1277,26 +1067,26 @@ cudaError_t launch_tc(const SplitParams &p, const TcArgs &a, const CUtensorMap &
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, split_tc_kernel<D, N, MODE, HL, BM>, p, a, map_k, map_v);
+  return cudaLaunchKernelEx(&cfg, split_tc_kernel<D, N, MODE, HL>, p, a, map_k, map_v);
 }
 
 // Every (head dim, padded rows) instantiation of one plan mode.
-template <int MODE, bool HL, int BM = kHeadScaled>
+template <int MODE, bool HL>
 cudaError_t launch_tc_any(const SplitParams &p, const TcArgs &a, int n, const CUtensorMap &map_k,
                           const CUtensorMap &map_v, cudaStream_t stream) {
   switch (p.D * 1000 + n) {
-    case 64016: return launch_tc<64, 16, MODE, HL, BM>(p, a, map_k, map_v, stream);
-    case 64032: return launch_tc<64, 32, MODE, HL, BM>(p, a, map_k, map_v, stream);
-    case 64048: return launch_tc<64, 48, MODE, HL, BM>(p, a, map_k, map_v, stream);
-    case 64064: return launch_tc<64, 64, MODE, HL, BM>(p, a, map_k, map_v, stream);
-    case 128016: return launch_tc<128, 16, MODE, HL, BM>(p, a, map_k, map_v, stream);
-    case 128032: return launch_tc<128, 32, MODE, HL, BM>(p, a, map_k, map_v, stream);
-    case 128048: return launch_tc<128, 48, MODE, HL, BM>(p, a, map_k, map_v, stream);
-    case 128064: return launch_tc<128, 64, MODE, HL, BM>(p, a, map_k, map_v, stream);
-    case 256016: return launch_tc<256, 16, MODE, HL, BM>(p, a, map_k, map_v, stream);
-    case 256032: return launch_tc<256, 32, MODE, HL, BM>(p, a, map_k, map_v, stream);
-    case 256048: return launch_tc<256, 48, MODE, HL, BM>(p, a, map_k, map_v, stream);
-    case 256064: return launch_tc<256, 64, MODE, HL, BM>(p, a, map_k, map_v, stream);
+    case 64016: return launch_tc<64, 16, MODE, HL>(p, a, map_k, map_v, stream);
+    case 64032: return launch_tc<64, 32, MODE, HL>(p, a, map_k, map_v, stream);
+    case 64048: return launch_tc<64, 48, MODE, HL>(p, a, map_k, map_v, stream);
+    case 64064: return launch_tc<64, 64, MODE, HL>(p, a, map_k, map_v, stream);
+    case 128016: return launch_tc<128, 16, MODE, HL>(p, a, map_k, map_v, stream);
+    case 128032: return launch_tc<128, 32, MODE, HL>(p, a, map_k, map_v, stream);
+    case 128048: return launch_tc<128, 48, MODE, HL>(p, a, map_k, map_v, stream);
+    case 128064: return launch_tc<128, 64, MODE, HL>(p, a, map_k, map_v, stream);
+    case 256016: return launch_tc<256, 16, MODE, HL>(p, a, map_k, map_v, stream);
+    case 256032: return launch_tc<256, 32, MODE, HL>(p, a, map_k, map_v, stream);
+    case 256048: return launch_tc<256, 48, MODE, HL>(p, a, map_k, map_v, stream);
+    case 256064: return launch_tc<256, 64, MODE, HL>(p, a, map_k, map_v, stream);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -1309,18 +1099,5 @@ cudaError_t launch_split_tc_dev(const SplitParams &p, const TcArgs &a, int n,
 cudaError_t launch_split_tc_len(const SplitParams &p, const TcArgs &a, int n,
                                 const CUtensorMap &map_k, const CUtensorMap &map_v,
                                 cudaStream_t stream);
-// Block-scaled caches: dense and over visit lists, by plan mode.
-cudaError_t launch_split_tc_dense_dev(const SplitParams &p, const TcArgs &a, int n,
-                                      const CUtensorMap &map_k, const CUtensorMap &map_v,
-                                      cudaStream_t stream);
-cudaError_t launch_split_tc_dense_len(const SplitParams &p, const TcArgs &a, int n,
-                                      const CUtensorMap &map_k, const CUtensorMap &map_v,
-                                      cudaStream_t stream);
-cudaError_t launch_split_tc_listed_dev(const SplitParams &p, const TcArgs &a, int n,
-                                       const CUtensorMap &map_k, const CUtensorMap &map_v,
-                                       cudaStream_t stream);
-cudaError_t launch_split_tc_listed_len(const SplitParams &p, const TcArgs &a, int n,
-                                       const CUtensorMap &map_k, const CUtensorMap &map_v,
-                                       cudaStream_t stream);
 
 }  // namespace vae4

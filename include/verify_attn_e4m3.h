@@ -506,10 +506,15 @@ int verify_attn_e4m3_append(const vae4_tensor *k_new, const vae4_tensor *v_new,
  *     z_t = softmax_scale * s_K[t / S] * q . dec(K_t)
  *     out = sum_t e^(z_t - max z) s_V[t / S] dec(V_t) / sum_t e^(z_t - max z)
  *
- * Arguments, workspace, plans, results and errors as verify_attn_e4m3_kv with
- * block_scales in the place of kv_scales.  A block with an invalid scale sets
- * BAD_SCALE and zeroes the rows of its sequence and KV head, as an invalid
- * page does.  hilo_pv and VAE4_FLAG_WARP_MMA: VAE4_ERR_UNSUPPORTED.
+ * Arguments, results and errors as verify_attn_e4m3_kv with block_scales in
+ * the place of kv_scales.  A block with an invalid scale sets BAD_SCALE and
+ * zeroes the rows of its sequence and KV head, as an invalid page does.
+ *  workspace   at least verify_attn_e4m3_block_scaled_workspace_bytes(...)
+ *              bytes.
+ * The batch's keys are divided evenly among the SMs on the device, from the
+ * lengths of the call (so a captured graph stays balanced as they change):
+ * opt->partition_tokens must be 0 (VAE4_ERR_PARTITION).  Repeated calls give
+ * the same bits.  hilo_pv and VAE4_FLAG_WARP_MMA: VAE4_ERR_UNSUPPORTED.
  */
 int verify_attn_e4m3_block_scaled(const vae4_tensor *q, const vae4_tensor *k_cache,
                                   const vae4_tensor *v_cache, const vae4_tensor *block_table,
@@ -572,8 +577,7 @@ int verify_attn_e4m3_select_blocks(const vae4_tensor *scores, const vae4_tensor 
  *  workspace   at least verify_attn_e4m3_sparse_workspace_bytes(...) bytes.
  * A block that several queries of a KV head list is read once.  A sequence
  * may have at most 98304 blocks (capacity / S; else VAE4_ERR_UNSUPPORTED).
- * opt->partition_tokens must be 0 (VAE4_ERR_PARTITION): the lists are divided
- * among the SMs on the device.  Pages and scales of blocks outside every list
+ * opt->partition_tokens must be 0 (VAE4_ERR_PARTITION), as above.  Pages and scales of blocks outside every list
  * are not looked at.
  */
 int verify_attn_e4m3_sparse(const vae4_tensor *q, const vae4_tensor *k_cache,
@@ -583,10 +587,19 @@ int verify_attn_e4m3_sparse(const vae4_tensor *q, const vae4_tensor *k_cache,
                             const vae4_tensor *workspace, vae4_stream stream,
                             const vae4_options *opt);
 
-/* Bytes of workspace of a verify_attn_e4m3_sparse call: the partials of the
- * split stage and a list of up to min(ceil(max_seq_len / block_tokens),
- * Qmax * blocks) 32-byte entries for every (sequence, KV head).  Arguments and
- * errors as verify_attn_e4m3_workspace_bytes; blocks = k. */
+/* Bytes of workspace of a verify_attn_e4m3_block_scaled call: the status word,
+ * FP32 partial states of two units per SM ((max, sum) [2 SMs][N][2] and
+ * unnormalised P.V [2 SMs][N][D], N the rows per unit: Qmax * Hq/Hkv in one or
+ * two groups, rounded up to 16) and 8 bytes per (sequence, KV head, row
+ * group).  Fewer SMs count if the longest batch has fewer 64-key pieces.
+ * Arguments and errors as verify_attn_e4m3_workspace_bytes. */
+int64_t verify_attn_e4m3_block_scaled_workspace_bytes(int B, int Hq, int Hkv, int Qmax, int D,
+                                                      int max_seq_len, int num_sms);
+
+/* Bytes of workspace of a verify_attn_e4m3_sparse call: that of
+ * verify_attn_e4m3_block_scaled, 16 bytes per (sequence, KV head) and a list
+ * of up to min(ceil(max_seq_len / block_tokens), Qmax * blocks) 32-byte
+ * entries for each; blocks = k. */
 int64_t verify_attn_e4m3_sparse_workspace_bytes(int B, int Hq, int Hkv, int Qmax, int D,
                                                 int max_seq_len, int block_tokens, int blocks,
                                                 int num_sms);

@@ -144,8 +144,9 @@ def test_options(lib):
         assert call(lib, name, base(), o(flags=16)) == OPT
         assert call(lib, name, base(), o(s=-1.0)) == OPT
         assert call(lib, name, base(), o(cap=MP * PAGE + 1)) == SHAPE
-    assert call(lib, "attend", base(), o(T=24)) == PART
-    assert call(lib, "sparse", base(), o(T=64)) == PART
+    for name in ("attend", "sparse"):  # the keys are divided on the device
+        for T in (24, 64):
+            assert call(lib, name, base(), o(T=T)) == PART
     for name in ("append", "scores"):
         assert call(lib, name, base(), flags=vae4.FLAG_WARP_MMA) == OPT
     assert call(lib, "scores", base(), scale=-1.0) == OPT
@@ -174,17 +175,31 @@ def test_empty_batch_is_no_error(lib):
         assert call(lib, name, a) == 0, name
 
 
-def test_sparse_workspace_bytes():
+def test_workspace_bytes():
+    """Status, partial states of two units per SM (fewer SMs if there are fewer
+    64-key pieces), the units' table; sparse: stream records and lists."""
     al = lambda x: (x + 255) // 256 * 256  # noqa: E731
-    # 2 sequences x 2 KV heads, 8 queries x 6 heads (48 rows), 5 blocks of 48 tokens each
-    streams, entries = 4, min(-(-1536 // 48), 8 * 5)
-    slots = max(152, 4 * (152 // 4))
-    o = al(al(256 + slots * 48 * 8) + slots * 48 * D * 4) + streams * 8
-    n = al(al(o) + streams * 16) + streams * entries * 32
+
+    def dense(streams, n_rg, N, D, pieces):
+        ctas = min(152, streams * n_rg * pieces)
+        o = al(al(256 + 2 * ctas * N * 8) + 2 * ctas * N * D * 4)
+        return o + streams * n_rg * 8
+
+    bs = vae4.block_scaled_workspace_bytes
+    assert bs(2, 12, 2, 8, D, 1536, 152) == dense(4, 1, 48, D, 24)    # 48 rows
+    assert bs(1, 6, 1, 16, 256, 262144, 152) == dense(1, 2, 48, 256, 4096)  # two row groups
+    assert bs(1, 2, 1, 1, 64, 100, 152) == dense(1, 1, 16, 64, 2)     # two pieces
+    # 2 sequences x 2 KV heads, 5 blocks of 48 tokens for each of 8 queries
+    entries = min(-(-1536 // 48), 8 * 5)
+    n = al(al(dense(4, 1, 48, D, 24)) + 4 * 16) + 4 * entries * 32
     assert vae4.sparse_workspace_bytes(2, 12, 2, 8, D, 1536, 48, 5, 152) == n
-    for bad in ((1, 7, 2, 8, D, 1536, 48, 5), (1, 12, 2, 8, 96, 1536, 48, 5),
-                (1, 12, 2, 8, D, 1536, 40, 5), (1, 12, 2, 17, D, 1536, 48, 5),
-                (1, 12, 2, 8, D, 0, 48, 5), (1, 12, 2, 8, D, 1536, 48, 0),
+    for bad in ((1, 7, 2, 8, D, 1536), (1, 12, 2, 8, 96, 1536), (1, 12, 2, 17, D, 1536),
+                (1, 12, 2, 8, D, 0), (0, 12, 2, 8, D, 1536), (1, 32, 1, 4, D, 1536)):
+        with pytest.raises(vae4.Vae4Error):
+            bs(*bad, 152)
+        with pytest.raises(vae4.Vae4Error):
+            vae4.sparse_workspace_bytes(*bad, 48, 5, 152)
+    for bad in ((1, 12, 2, 8, D, 1536, 40, 5), (1, 12, 2, 8, D, 1536, 48, 0),
                 (1, 12, 2, 8, D, 16 * 98305, 16, 5)):
         with pytest.raises(vae4.Vae4Error):
             vae4.sparse_workspace_bytes(*bad, 152)

@@ -142,8 +142,9 @@ def attend(c, q, layout="tokens", **kw):
     k, v = c.device(layout)
     qd, bt, seq, sc = dev(q, c.table, c.seq, c.scales)
     out = torch.full_like(qd, float("nan"))
-    ws = vae4.alloc_workspace(B, Hq, c.Hkv, Q, D, cap or c.table.shape[1] * c.page,
-                              kw.get("partition_tokens", 0))
+    top = cap or c.table.shape[1] * c.page
+    n = vae4.block_scaled_workspace_bytes(B, Hq, c.Hkv, Q, D, top, kw.get("num_sms", 0))
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
     vae4.verify_attn_e4m3_block_scaled(qd, k, v, bt, seq, sc, out, ws, max_seq_len=cap,
                                        flags=FMT[c.fmt][2], **kw)
     torch.cuda.synchronize()
@@ -158,30 +159,77 @@ def check(got, ref, tol):
 
 
 ATTEND = [
-    # lens, Q, G, Hkv, D, page, block, format, layout, T
-    ([(1, 1)], 1, 1, 1, 64, 16, 16, "e4m3", "tokens", 0),
-    ([(17, 8)], 8, 2, 1, 64, 16, 16, "e4m3", "pool", 0),
-    ([(1024, 8)], 8, 2, 1, 64, 16, 16, "e4m3", "tokens", 256),
-    ([(3297, 8), (1025, 5), (0, 0), (16, 16), (15, 1)], 16, 6, 1, 256, 16, 16, "e4m3", "tokens", 0),
-    ([(700, 16), (3000, 16)], 16, 6, 1, 256, 48, 48, "e4m3", "pool", 0),
-    ([(2500, 1), (95, 1), (96, 1), (97, 1)], 1, 8, 4, 128, 96, 32, "e4m3", "tokens", 0),
-    ([(2500, 3), (777, 2)], 5, 4, 3, 128, 64, 64, "e5m2", "pool", 0),
-    ([(5000, 8)], 8, 6, 1, 256, 848, 848, "e4m3", "padded", 0),
-    ([(1500, 8), (300, 8)], 8, 4, 2, 128, 32, 16, "e4m3", "padded", 512),
-    ([(4000, 4)], 4, 12, 2, 64, 128, 16, "e5m2", "padded", 0),
-    ([(300, 2)] * 40, 2, 3, 2, 64, 32, 32, "e4m3", "tokens", 0),
+    # lens, Q, G, Hkv, D, page, block, format, layout
+    ([(1, 1)], 1, 1, 1, 64, 16, 16, "e4m3", "tokens"),
+    ([(17, 8)], 8, 2, 1, 64, 16, 16, "e4m3", "pool"),
+    ([(1024, 8)], 8, 2, 1, 64, 16, 16, "e4m3", "tokens"),
+    ([(3297, 8), (1025, 5), (0, 0), (16, 16), (15, 1)], 16, 6, 1, 256, 16, 16, "e4m3", "tokens"),
+    ([(700, 16), (3000, 16)], 16, 6, 1, 256, 48, 48, "e4m3", "pool"),
+    ([(2500, 1), (95, 1), (96, 1), (97, 1)], 1, 8, 4, 128, 96, 32, "e4m3", "tokens"),
+    ([(2500, 3), (777, 2)], 5, 4, 3, 128, 64, 64, "e5m2", "pool"),
+    ([(5000, 8)], 8, 6, 1, 256, 848, 848, "e4m3", "padded"),
+    ([(1500, 8), (300, 8)], 8, 4, 2, 128, 32, 16, "e4m3", "padded"),
+    ([(4000, 4)], 4, 12, 2, 64, 128, 16, "e5m2", "padded"),
+    ([(300, 2)] * 40, 2, 3, 2, 64, 32, 32, "e4m3", "tokens"),
+    # several units per SM, in one and in several batches of segments
+    ([(200 + 37 * b, 1) for b in range(30)], 1, 16, 8, 128, 64, 32, "e4m3", "tokens"),
+    ([(70, 4)] * 33, 4, 12, 2, 256, 64, 64, "e4m3", "pool"),
+    ([(9000, 1)] + [(5, 1)] * 900, 1, 2, 2, 64, 16, 16, "e4m3", "tokens"),
+    ([(20, 1)] * 1500, 1, 1, 8, 64, 32, 32, "e4m3", "tokens"),
 ]
 
 
-@pytest.mark.parametrize("lens,Q,G,Hkv,D,page,blk,fmt,layout,T", ATTEND)
-def test_attention_matches_the_definition(lens, Q, G, Hkv, D, page, blk, fmt, layout, T):
+@pytest.mark.parametrize("lens,Q,G,Hkv,D,page,blk,fmt,layout", ATTEND,
+                         ids=[f"{len(c[0])}x{c[3]}-q{c[1]}x{c[2]}-{c[4]}-{c[5]}/{c[6]}-{c[7]}-{c[8]}"
+                              for c in ATTEND])
+def test_attention_matches_the_definition(lens, Q, G, Hkv, D, page, blk, fmt, layout):
     c = Cache(lens, Hkv, D, page, blk, fmt, seed=len(lens) + D)
     q = queries(c, Q, G)
-    got, status = attend(c, q, layout, partition_tokens=T)
+    got, status = attend(c, q, layout)
     assert status == 0
     check(got, *reference(c, q))
     for b, (L, n) in enumerate(lens):  # padding slots and dead sequences
         assert not got[b, n if L else 0:].any()
+
+
+@pytest.mark.parametrize("sms", [1, 3, 152, 400])
+def test_attention_divided_among_other_numbers_of_sms(sms):
+    """Fewer CTAs than units (one CTA walks them all) and more than the GPU's
+    SMs; the same call twice gives the same bits."""
+    c = Cache([(1000, 3), (130, 1), (64, 2), (2000, 3), (0, 0), (700, 2)], 2, 128, 32, 16, seed=12)
+    q = queries(c, 3, 4)
+    got, status = attend(c, q, num_sms=sms)
+    assert status == 0
+    check(got, *reference(c, q))
+    again, _ = attend(c, q, num_sms=sms)
+    assert torch.equal(got, again)
+
+
+def test_waits_that_run_out_mark_the_rows():
+    """The failure path: every pipeline wait gives up at once, the call reports
+    the timeout and writes zero rows, and the workspace serves the next call."""
+    c = Cache([(3000, 4), (100, 4), (50, 2)], 2, 128, 32, 16, seed=13)
+    q = queries(c, 4, 3)
+    k, v = c.device()
+    qd, bt, seq, sc = dev(q, c.table, c.seq, c.scales)
+    ids = torch.arange(6, dtype=torch.int32).expand(3, 4, 2, 6).contiguous().cuda()
+    cap = c.table.shape[1] * c.page
+    for sp in (False, True):
+        ws = (vae4.alloc_sparse_workspace(3, 6, 2, 4, 128, cap, 16, 6) if sp else
+              vae4.alloc_workspace(3, 6, 2, 4, 128, cap))
+        out = torch.full_like(qd, float("nan"))
+        for flags in (vae4.FLAG_TEST_SHORT_WAITS, 0):
+            if sp:
+                vae4.verify_attn_e4m3_sparse(qd, k, v, bt, seq, sc, ids, out, ws, flags=flags)
+            else:
+                vae4.verify_attn_e4m3_block_scaled(qd, k, v, bt, seq, sc, out, ws, flags=flags)
+            torch.cuda.synchronize()
+            assert vae4.read_status(ws) == (vae4.STATUS_TIMEOUT if flags else 0)
+            if flags:
+                assert not out.any()
+                vae4.clear_status(ws)
+        allowed = listed(c, ids.cpu()) if sp else None
+        check(out.cpu(), *reference(c, q, allowed=allowed))
 
 
 def test_attention_with_scales_far_apart():
