@@ -69,6 +69,8 @@ struct SegParams {
   int2 *tab;                   // (first CTA, parts) [B * Hkv][n_rg]
   uint32_t *status;
   int32_t B, Qmax, Hkv, G, D, page, e5m2;
+  int32_t page_blocks;         // page / blk
+  unsigned long long page_m, blk_m;  // reciprocals for the device's divisions (seg_tc.cuh)
   int32_t N, n_rg;             // rows per unit, row groups
   int32_t ctas;
   float sm_scale;

@@ -40,7 +40,7 @@
 //                     tensor memory, the A operand of O^T = V^T . P^T.
 //   score MMA, value MMA: one thread each issues the products of a tile.
 //   softmax (8)     : thread = key, half of the N rows each.  The reference m
-//                     of a row is raised only when a weight would pass 2^12
+//                     of a row is raised only when a weight would pass 2^15
 //                     (one vote per tile); then only the rows concerned, and
 //                     only the groups of 8 accumulator columns that hold them,
 //                     are rescaled.  At a segment's end they load the next
@@ -144,6 +144,13 @@ enum : int { kWSoftmax = 0, kWKDec = 8, kWVDec = 12, kWKProd = 16, kWVProd = 17,
 
 __device__ __forceinline__ uint32_t sw128(uint32_t off) { return off ^ (((off >> 7) & 7u) << 4); }
 
+// key / n for n a multiple of 16 up to 65536 and key < 2^30, m = ceil(2^38 /
+// (n / 16)): with x = key / 16 < 2^26, x m < 2^64, and the excess of x m / 2^38
+// over x / (n / 16) is below x / 2^38 < 2^-12 <= 1 / (n / 16).
+__device__ __forceinline__ int div16(int key, unsigned long long m) {
+  return (int)((unsigned long long)(unsigned)(key >> 4) * m >> 38);
+}
+
 // ---------------------------------------------------------------------------
 // The plan: which segments a CTA walks.
 
@@ -161,29 +168,37 @@ struct Line {
   int q;      // places per CTA
 };
 
-// `st`: the groups' lengths staged in shared memory, or null
-__device__ __forceinline__ int2 length_of(const SegParams &p, const int2 *st, int x) {
-  if (x >= p.groups) return make_int2(0, 0);
-  return st ? st[x] : group_len(p, x);
-}
+// Where the plan's lengths come from: staged in shared memory, read as they
+// are (st = null), or, for a dry run, one invented group.
+struct Lengths {
+  const int2 *st;
+  int groups;
+  bool dry;
+  __device__ __forceinline__ int2 of(const SegParams &p, int x) const {
+    if (x >= groups) return make_int2(0, 0);
+    if (dry) return make_int2(640, 1);
+    return st ? st[x] : group_len(p, x);
+  }
+};
 
-// cost of a group: its units (heads x row groups with a live query) and places
-__device__ __forceinline__ int group_units(const SegParams &p, int2 v, int N) {
-  return v.x > 0 ? p.unit_heads * ((v.y * p.G + N - 1) / N) : 0;
+// A group's row groups with a live query (its units are heads x row groups,
+// at most two: 96 rows in groups of 48) and a unit's places.
+__device__ __forceinline__ int row_groups(const SegParams &p, int2 v, int N) {
+  return v.x <= 0 ? 0 : v.y * p.G > N ? 2 : 1;
 }
 __device__ __forceinline__ int unit_places(int2 v) { return kUnitCost + (v.x + 63) / 64; }
 
 // One warp: the line's length (four groups per lane in flight).
-static __device__ __noinline__ Line plan_line(const SegParams &p, const int2 *st, int N, int lane) {
+static __device__ __noinline__ Line plan_line(const SegParams &p, Lengths len, int N, int lane) {
   int sum = 0;
-  for (int x0 = 0; x0 < p.groups; x0 += 128) {
+  for (int x0 = 0; x0 < len.groups; x0 += 128) {
     int2 v[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      v[e] = length_of(p, st, x0 + 32 * e + lane);
+      v[e] = len.of(p, x0 + 32 * e + lane);
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sum += group_units(p, v[e], N) * unit_places(v[e]);
+    for (int e = 0; e < 4; ++e) sum += p.unit_heads * row_groups(p, v[e], N) * unit_places(v[e]);
   }
   Line l;
   l.total = (int)__reduce_add_sync(0xffffffffu, (unsigned)sum);
@@ -196,17 +211,17 @@ static __device__ __noinline__ Line plan_line(const SegParams &p, const int2 *st
 // end: the CTA's last place).  The CTA where a unit starts records its first
 // CTA and its parts for the combine (parts = -1: finished in one CTA).
 template <bool LISTED>
-static __device__ __noinline__ int plan_segments(const SegParams &p, const int2 *st, int N, Line l,
+static __device__ __noinline__ int plan_segments(const SegParams &p, Lengths len, int N, Line l,
                                                  int cta, int from, int *next, Segment *seg,
                                                  int *bad, int lane) {
   const int end = min((cta + 1) * l.q, l.total);
   int n = 0;
   int base = 0;  // place where group x0 starts
-  for (int x0 = 0; x0 < p.groups && base < end; x0 += 32) {
+  for (int x0 = 0; x0 < len.groups && base < end; x0 += 32) {
     const int x = x0 + lane;
-    const int2 v = length_of(p, st, x);
-    const int units = group_units(p, v, N), pl = unit_places(v);
-    const int cost = units * pl;
+    const int2 v = len.of(p, x);
+    const int rgs = row_groups(p, v, N), pl = unit_places(v);
+    const int cost = p.unit_heads * rgs * pl;
     int incl = cost;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -220,9 +235,9 @@ static __device__ __noinline__ int plan_segments(const SegParams &p, const int2 
       const int src = __ffs(hit) - 1;
       hit &= hit - 1;
       const int gs = __shfl_sync(0xffffffffu, start, src);
-      const int gu = __shfl_sync(0xffffffffu, units, src), gp = __shfl_sync(0xffffffffu, pl, src);
+      const int n_rg = __shfl_sync(0xffffffffu, rgs, src), gp = __shfl_sync(0xffffffffu, pl, src);
       const int gl = __shfl_sync(0xffffffffu, v.x, src), gq = __shfl_sync(0xffffffffu, v.y, src);
-      const int n_rg = gu / p.unit_heads, nh = gp - kUnitCost;
+      const int gu = p.unit_heads * n_rg, nh = gp - kUnitCost;
       const int u0 = from > gs ? (from - gs) / gp : 0;
       for (int ub = u0; ub < gu && gs + ub * gp < end; ub += 32) {
         const int u = min(ub + lane, gu);
@@ -233,7 +248,7 @@ static __device__ __noinline__ int plan_segments(const SegParams &p, const int2 
         const unsigned m = __ballot_sync(0xffffffffu, mine);
         const int at = n + __popc(m & ((1u << lane) - 1u));
         if (mine && at < kMaxSeg) {
-          const int h = u / n_rg, rg = u - h * n_rg;
+          const int h = u >> (n_rg - 1), rg = u - h * n_rg;
           Segment s;
           s.b = x0 + src;
           s.h_rg = h | rg << 16;
@@ -241,10 +256,10 @@ static __device__ __noinline__ int plan_segments(const SegParams &p, const int2 
           s.k1 = min((z - us) * 64, gl);
           s.L = gl;
           s.ql = gq;
-          const int c0 = us / l.q, c1 = (us + nh - 1) / l.q;
-          s.slot = c0 == c1 ? -1 : cta == c0 ? cta : p.ctas + cta;
+          const bool starts = a == us, ends = z == us + nh;
+          s.slot = !starts ? p.ctas + cta : ends ? -1 : cta;
           s.pad = 0;
-          if constexpr (LISTED) {
+          if (LISTED && !len.dry) {
             const BlockStream rec = p.streams[s.b];
             s.h_rg = s.b % p.Hkv | rg << 16;
             s.k1 = min(s.k1, rec.n);
@@ -252,9 +267,10 @@ static __device__ __noinline__ int plan_segments(const SegParams &p, const int2 
           }
           seg[at] = s;
           bad[at] = 0;
-          if (a == us) {
+          if (starts && !len.dry) {
             const int str = LISTED ? s.b : s.b * p.Hkv + h;
-            p.tab[(int64_t)str * p.n_rg + rg] = make_int2(c0, c0 == c1 ? -1 : c1 - c0 + 1);
+            const int parts = ends ? -1 : (us + nh - 1) / l.q - cta + 1;
+            p.tab[(int64_t)str * p.n_rg + rg] = make_int2(cta, parts);
           }
         }
         n += __popc(m);
@@ -343,8 +359,8 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   const float kInf = __int_as_float(0x7f800000);
   constexpr float kLog2e = 1.4426950408889634f;
-  // lazy-rescale threshold (log2 units): P <= 4096, far inside FP16
-  constexpr float kTau = 12.0f;
+  // lazy-rescale threshold (log2 units): P <= 2^15, inside FP16
+  constexpr float kTau = 15.0f;
 
   const uint32_t raw_addr = smem_u32(smem_raw);
   const uint32_t sbase = (raw_addr + 1023u) & ~1023u;
@@ -364,8 +380,9 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
 
   // ---- set-up that touches only this CTA's shared memory and TMEM, done
   // before the grid dependency wait so it overlaps the previous kernel's tail
-  if (tid == 0) {
-    for (int i = 0; i < C::NBARS; ++i) {
+  static_assert(C::NBARS <= 96, "one thread per barrier");
+  if (tid < 96) {
+    if (const int i = tid; i < C::NBARS) {
       uint32_t cnt = 1;
       if (i >= kKEmpty && i < kKEmpty + C::NKR)
         cnt = 64;
@@ -382,10 +399,22 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
         cnt = 32;  // one arrival per producer lane (8-byte copies)
       tc::mbar_init(bar(i), cnt);
     }
-    *abort_f = 0;
+    if (tid == 0) *abort_f = 0;
   }
   if (producer && lane == 0 && !p.cpasync)  // kernel parameters
     tc::prefetch_tensormap(warp == kWVProd ? &tmap_v : &tmap_k);
+  if (warp == kWKProd) {
+    // The plan's code runs once on an invented batch, while the previous kernel
+    // ends and the barriers and TMEM are set up: its instructions are then at
+    // hand when the lengths arrive (6000 cycles for the first run, 400 for the
+    // next).
+    Segment *seg = reinterpret_cast<Segment *>(gSm + C::S_SEG);
+    int next;
+    const Lengths dry{nullptr, 1, true};
+    const Line l = plan_line(p, dry, N, lane);
+    plan_segments<LISTED>(p, dry, N, l, 0, 0, &next, seg,
+                          reinterpret_cast<int *>(gSm + C::S_BAD), lane);
+  }
   if (warp == kWQk) {
     tc::tmem_alloc(sSm + C::S_SCAL + 4, 512);
     tc::tmem_relinquish();
@@ -422,13 +451,13 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
       __syncthreads();
     }
     if (warp == kWKProd) {
-      const int2 *st = staged ? st_len : nullptr;
-      const Line line = first ? plan_line(p, st, N, lane) : *line_s;
+      const Lengths len{staged ? st_len : nullptr, p.groups, false};
+      const Line line = first ? plan_line(p, len, N, lane) : *line_s;
       const int place = first ? cta * line.q : *place_s;
       int next = place, n = 0;
       const int end = min((cta + 1) * line.q, line.total);
       if (place < end)
-        n = plan_segments<LISTED>(p, st, N, line, cta, place, &next, seg_s, bad_s, lane);
+        n = plan_segments<LISTED>(p, len, N, line, cta, place, &next, seg_s, bad_s, lane);
       __syncwarp();
       if (lane == 0) {
         *line_s = line;
@@ -458,7 +487,12 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
       const CUtensorMap *map = isv ? &tmap_v : &tmap_k;
       const int unit = LISTED ? p.blk : p.page;  // tokens per table (list) entry
       const int nbox = 64 >> lb;                 // copies per half-tile
-      int st = count % nslot, u = count / nslot;
+      const unsigned long long unit_m = LISTED ? p.blk_m : p.page_m;
+      int st = 0, u = 0;  // ring slot and its pass
+      if (count > 0) {
+        u = count / nslot;
+        st = count - u * nslot;
+      }
       // Copies are prepared 32 at a time, one per lane (its page, and its
       // token in the page), from table entries requested a group ahead: the
       // loop over half-tiles is one warp's serial code and its length is what
@@ -480,15 +514,15 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
         if (key >= 0) {
           if constexpr (LISTED)
             raw = __ldg(reinterpret_cast<const int2 *>(
-                p.list + (int64_t)seg_s[it.x].b * p.list_cap + key / unit));
+                p.list + (int64_t)seg_s[it.x].b * p.list_cap + div16(key, unit_m)));
           else
-            raw.x = __ldg(p.bt + (int64_t)seg_s[it.x].b * p.bt_sb + key / unit);
+            raw.x = __ldg(p.bt + (int64_t)seg_s[it.x].b * p.bt_sb + div16(key, unit_m));
         }
       };
       int page = 0, tok = 0;  // of the lane's copy; the page past the last one reads as zeros
       auto prepare = [&](int2 it) {
         const int key = copy_key(it);
-        tok = key >= 0 ? key % unit + 16 * raw.y : 0;
+        tok = key >= 0 ? key - div16(key, unit_m) * unit + 16 * raw.y : 0;
         page = raw.x;
         if (key >= 0 && (page < 0 || page >= p.n_pages)) atomicOr(&bad_s[it.x], 1);
         if (page < 0 || page >= p.n_pages) page = (int)p.n_pages;
@@ -500,7 +534,6 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
       // requested a group ahead of its use, the page ids that lead to it two.
       float4 *box_s = reinterpret_cast<float4 *>(gSm + C::S_BOX);
       uint32_t *mask_s = reinterpret_cast<uint32_t *>(gSm + C::S_MASK);
-      const int nb_page = p.page / p.blk;
       auto step = [&](int2 it) -> int2 {  // (segment, group) after it
         if (it.x >= nseg) return it;
         return 4 * (it.y + 1) < tiles_of(it.x) ? make_int2(it.x, it.y + 1) : make_int2(it.x + 1, 0);
@@ -513,7 +546,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
       auto load_page = [&](int2 it) -> int {
         if constexpr (LISTED) return 0;
         const int key = key_of(it);
-        return key >= 0 ? __ldg(p.bt + (int64_t)seg_s[it.x].b * p.bt_sb + key / p.page) : -1;
+        return key >= 0 ? __ldg(p.bt + (int64_t)seg_s[it.x].b * p.bt_sb + div16(key, p.page_m)) : -1;
       };
       float4 f = make_float4(0.f, 0.f, 1.f, 0.f);  // (s_K, s_V); listed: the entry's
       int2 e = make_int2(0, 0);                    // listed: first token, mask
@@ -523,7 +556,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
         live = key >= 0;
         if constexpr (LISTED) {
           if (live) {
-            const int x = key / p.blk;
+            const int x = div16(key, p.blk_m);
             const BlockEntry *en = p.list + (int64_t)seg_s[it.x].b * p.list_cap + x;
             e = __ldg(reinterpret_cast<const int2 *>(&en->tok0));
             e.x += key - x * p.blk;
@@ -534,7 +567,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
           if (live) {
             const float *sp = p.scales + (int64_t)page * p.s_page +
                               (int64_t)(seg_s[it.x].h_rg & 0xFFFF) * p.s_head +
-                              (key / p.blk - key / p.page * nb_page);
+                              (div16(key, p.blk_m) - div16(key, p.page_m) * p.page_blocks);
             f.x = __ldg(sp);
             f.y = __ldg(sp + p.s_kv);
           }
@@ -580,8 +613,6 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
           const int h = seg_s[s].h_rg & 0xFFFF;
           const int nhalf = 2 * tiles_of(s);
           for (int t = 0; t < nhalf; ++t) {
-            // (before the wait for a slot, which the keys of this group may need)
-            if (!isv && (t & 7) == 0 && !(ok = pass_scales())) break;
             if (t % (32 / NB) == 0) {  // (a half-tile past the segment's end may start a group)
               if (itc.x == s) {
                 prepare(itc);
@@ -618,6 +649,9 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
                            seg_s[s].k1 - seg_s[s].k0 - 64 * t, mine < p.n_pages ? mine : -1, box, slot,
                            full, lane);
             }
+            // a group's scales follow its first copy (their loads may still be
+            // on the way, and the softmax needs them later than the keys)
+            if (!isv && (t & 7) == 0 && !(ok = pass_scales())) break;
             ++count;
             if (++st == nslot) {
               st = 0;
