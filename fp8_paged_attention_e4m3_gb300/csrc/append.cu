@@ -68,7 +68,7 @@ __device__ __forceinline__ uint32_t fp8x2_of_f16x2(uint32_t h) {
 __device__ __forceinline__ bool scale_ok(float s) { return s >= kMinScale && s <= kMaxScale; }
 
 template <int D, bool BF16, bool E5M2>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 6) append_kernel(const AppendParams p) {
   constexpr int CH = D / 8;                    // 8-element chunks per row
   constexpr int RG = kAppendThreads / CH;      // rows per pass
   constexpr int LEAD = E5M2 ? 15 : 8;          // FPMAX = 1.75 * 2^LEAD

@@ -193,7 +193,7 @@ cudaError_t launch_t(const ScoreParams &p, cudaStream_t stream) {
   const int64_t need = std::max<int64_t>(1, (p.cols + per - 1) / per);
   const int64_t res = std::max<int64_t>(1, std::min<int64_t>(8, 220 * 1024 / (smem + 1024)));
   const int64_t want = std::max<int64_t>(1, (2 * res * p.num_sms + rows - 1) / rows);
-  const int64_t steps = (need + want - 1) / want;
+  const int64_t steps = std::min<int64_t>((need + want - 1) / want, (NT + 1) / 2);
   const dim3 grid((unsigned)std::min<int64_t>((need + steps - 1) / steps, 0x7fffffff),
                   (unsigned)p.Hkv, (unsigned)p.B);
   block_scores_kernel<D, NT, E5M2><<<grid, kScoreThreads, smem, stream>>>(p);

@@ -33,8 +33,8 @@ __device__ __forceinline__ uint32_t score_key(float x) {
 }
 
 // kKeys > 0: rows of up to kThreads * kKeys blocks, in registers; 0: any row
-template <int kThreads, int kKeys>
-__global__ void __launch_bounds__(kThreads) select_blocks_kernel(const SelectParams p) {
+template <int kThreads, int kKeys, int kCtas>
+__global__ void __launch_bounds__(kThreads, kCtas) select_blocks_kernel(const SelectParams p) {
   constexpr int kWarps = kThreads / 32;
   constexpr int kOwn = kBins / kThreads;  // bins per thread
   __shared__ uint32_t hist[kBins];
@@ -158,13 +158,13 @@ cudaError_t launch_select_blocks(const SelectParams &p, cudaStream_t stream) {
   const dim3 grid((unsigned)p.Qmax, (unsigned)p.Hkv, (unsigned)p.B);
   // a row has at most `cols` blocks: the smallest CTA that holds it in registers
   if (p.cols <= 256 * 8)
-    select_blocks_kernel<256, 8><<<grid, 256, 0, stream>>>(p);
+    select_blocks_kernel<256, 8, 4><<<grid, 256, 0, stream>>>(p);
   else if (p.cols <= 1024 * 8)
-    select_blocks_kernel<1024, 8><<<grid, 1024, 0, stream>>>(p);
-  else if (p.cols <= 1024 * 16)
-    select_blocks_kernel<1024, 16><<<grid, 1024, 0, stream>>>(p);
+    select_blocks_kernel<1024, 8, 1><<<grid, 1024, 0, stream>>>(p);
+  else if (p.cols <= 512 * 32)
+    select_blocks_kernel<512, 32, 2><<<grid, 512, 0, stream>>>(p);
   else
-    select_blocks_kernel<1024, 0><<<grid, 1024, 0, stream>>>(p);
+    select_blocks_kernel<1024, 0, 2><<<grid, 1024, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
