@@ -14,7 +14,11 @@
 // to the fragments with one 16-byte load per 16 channels and no shared memory,
 // and the matching share of B is 4 consecutive halves of a query's row.  The
 // bytes of the bounds bound it (2 D per block and head, read once); the tensor
-// products of up to 96 rows stay below them.
+// products of up to 96 rows stay below them.  16 sequences of up to
+// 131072 tokens, 8 heads of 128, blocks of 32: 91 MB in 24.5 us, 3.7 TB/s; what keeps it from
+// the memory's rate is the chain page -> bounds -> products of each warp's step.
+// Eight queries over 262144 tokens are that chain alone, 8.4 us with the queries'
+// staging.
 #include <algorithm>
 
 #include "common.cuh"
@@ -58,7 +62,7 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Score
   const int nblk = L > 0 && n > 0 ? (L - 1) / p.blk + 1 : 0;
   const int step = gridDim.x * kScoreWarps * 16;
   int j0 = (blockIdx.x * kScoreWarps + warp) * 16;
-  if (blockIdx.x * kScoreWarps * 16 >= nblk) return;
+  if (blockIdx.x * kScoreWarps * 16 >= nblk) return;  // (a warp past the end stores nothing)
   // the page and scale of block j0 + lane (lanes 0 .. 15)
   auto page_of = [&](int jj) -> int {
     const int j = jj + lane;
@@ -92,41 +96,48 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Score
   }
   __syncthreads();
   const float ninf = -__int_as_float(0x7f800000);
-  for (; j0 < nblk; j0 += step) {
-    // ---- this lane's block: address and scale
-    const int j = j0 + lane;
-    bool ok = lane < 16 && j < nblk && phys >= 0 && phys < p.n_pages;
+  // ---- A: rows g and g + 8 of 16 blocks, 16 bytes per 64 channels; with them
+  // this lane's block's scale and the mask of valid blocks
+  struct Tile {
+    uint4 a[2][2][NC];  // [hi, lo][row][chunk]
+    float s;
+    unsigned okm;
+  };
+  auto load = [&](Tile &x, int jj) {
+    const int j = jj + lane;
+    const bool ok = lane < 16 && j < nblk && phys >= 0 && phys < p.n_pages;
     if (lane < 16 && j < nblk && !ok && p.status) atomicOr(p.status, VAE4_STATUS_BAD_BLOCK);
     int64_t off = 0;
-    float s = 0.f;
+    x.s = 0.f;
     if (ok) {
       const int sub = j % p.nb;
       off = (int64_t)phys * p.b_page + (int64_t)h * p.b_head + (int64_t)sub * p.b_blk;
-      s = __ldg(p.scales + (int64_t)phys * p.s_page + (int64_t)h * p.s_head + sub) * p.sm_scale;
+      x.s = __ldg(p.scales + (int64_t)phys * p.s_page + (int64_t)h * p.s_head + sub) * p.sm_scale;
     }
-    phys = page_of(j0 + step);  // in flight with this step's bounds
-    const unsigned okm = __ballot_sync(0xffffffffu, ok);
-    // ---- A: rows g and g + 8 of the 16 blocks, 16 bytes per 64 channels
-    uint4 a[2][2][NC];  // [hi, lo][row][chunk]
+    phys = page_of(jj + step);  // in flight with this step's bounds
+    x.okm = __ballot_sync(0xffffffffu, ok);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int src = g + 8 * r;
       const int64_t o = __shfl_sync(0xffffffffu, off, src);
-      const bool live = (okm >> src) & 1u;
+      const bool live = (x.okm >> src) & 1u;
       const uint8_t *base = p.bounds + o + 16 * t;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        a[0][r][c] = live ? __ldg(reinterpret_cast<const uint4 *>(base + p.b_mm + 64 * c))
-                          : make_uint4(0u, 0u, 0u, 0u);
-        a[1][r][c] = live ? __ldg(reinterpret_cast<const uint4 *>(base + 64 * c))
-                          : make_uint4(0u, 0u, 0u, 0u);
+        x.a[0][r][c] = live ? __ldg(reinterpret_cast<const uint4 *>(base + p.b_mm + 64 * c))
+                            : make_uint4(0u, 0u, 0u, 0u);
+        x.a[1][r][c] = live ? __ldg(reinterpret_cast<const uint4 *>(base + 64 * c))
+                            : make_uint4(0u, 0u, 0u, 0u);
       }
     }
+  };
+  auto use = [&](const Tile &x, int jj) {
+    const auto &a = x.a;
     float acc[NT][4];
 #pragma unroll
-    for (int x = 0; x < NT; ++x)
+    for (int k = 0; k < NT; ++k)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[x][e] = 0.f;
+      for (int e = 0; e < 4; ++e) acc[k][e] = 0.f;
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
 #pragma unroll
@@ -145,10 +156,10 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Score
             fa[e][3] = fp8x2_to_f16x2<E5M2>(w1[2 * hf + e] >> 16);
           }
 #pragma unroll
-          for (int x = 0; x < NT; ++x) {
-            const uint4 bq = *reinterpret_cast<const uint4 *>(qb + x * 8 * BS + 8 * hf);
-            mma16816(acc[x], fa[0], bq.x, bq.y);
-            mma16816(acc[x], fa[1], bq.z, bq.w);
+          for (int k = 0; k < NT; ++k) {
+            const uint4 bq = *reinterpret_cast<const uint4 *>(qb + k * 8 * BS + 8 * hf);
+            mma16816(acc[k], fa[0], bq.x, bq.y);
+            mma16816(acc[k], fa[1], bq.z, bq.w);
           }
         }
       }
@@ -156,25 +167,32 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Score
     // ---- the maximum over each query's heads, through shared memory
     __syncwarp();
 #pragma unroll
-    for (int x = 0; x < NT; ++x) {
-      us[g * RS + 8 * x + 2 * t] = acc[x][0];
-      us[g * RS + 8 * x + 2 * t + 1] = acc[x][1];
-      us[(g + 8) * RS + 8 * x + 2 * t] = acc[x][2];
-      us[(g + 8) * RS + 8 * x + 2 * t + 1] = acc[x][3];
+    for (int k = 0; k < NT; ++k) {
+      us[g * RS + 8 * k + 2 * t] = acc[k][0];
+      us[g * RS + 8 * k + 2 * t + 1] = acc[k][1];
+      us[(g + 8) * RS + 8 * k + 2 * t] = acc[k][2];
+      us[(g + 8) * RS + 8 * k + 2 * t + 1] = acc[k][3];
     }
     __syncwarp();
-    const float sj = __shfl_sync(0xffffffffu, s, lane & 15);
-    const bool live = (okm >> (lane & 15)) & 1u;
-    const int jo = j0 + (lane & 15);
+    const float sj = __shfl_sync(0xffffffffu, x.s, lane & 15);
+    const bool live = (x.okm >> (lane & 15)) & 1u;
+    const int jo = jj + (lane & 15);
     for (int i = lane >> 4; i < n; i += 2) {  // 16 blocks of two queries at a time
       float best = ninf;
-      for (int x = 0; x < p.G; ++x) best = fmaxf(best, us[(lane & 15) * RS + i * p.G + x]);
+      for (int k = 0; k < p.G; ++k) best = fmaxf(best, us[(lane & 15) * RS + i * p.G + k]);
       if (jo < nblk) {
         const bool seen = (int64_t)jo * p.blk <= L - n + i;
         p.scores[(int64_t)b * p.o_sb + (int64_t)i * p.o_si + (int64_t)h * p.o_sh + jo] =
             live && seen ? best * sj : ninf;
       }
     }
+  };
+  Tile x;
+  load(x, j0);
+  for (;;) {
+    use(x, j0);
+    if ((j0 += step) >= nblk) break;
+    load(x, j0);
   }
 }
 
@@ -186,14 +204,15 @@ cudaError_t launch_t(const ScoreParams &p, cudaStream_t stream) {
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  // enough CTAs for a full load of every SM (16 warps each, as far as shared
-  // memory allows); beyond that the warps take several steps, so that fewer
-  // CTAs read the queries
+  // CTAs for one full load of every SM (as far as shared memory allows), whose
+  // warps then take several steps: each CTA reads and splits the queries.  24.5 us
+  // for the batch above, 26.2 with twice the CTAs; the next step's bounds on
+  // their way during one's products cost more registers than they gain (25.8)
   const int64_t per = kScoreWarps * 16, rows = (int64_t)p.Hkv * p.B;
   const int64_t need = std::max<int64_t>(1, (p.cols + per - 1) / per);
   const int64_t res = std::max<int64_t>(1, std::min<int64_t>(8, 220 * 1024 / (smem + 1024)));
-  const int64_t want = std::max<int64_t>(1, (2 * res * p.num_sms + rows - 1) / rows);
-  const int64_t steps = std::min<int64_t>((need + want - 1) / want, (NT + 1) / 2);
+  const int64_t want = std::max<int64_t>(1, (res * p.num_sms + rows - 1) / rows);
+  const int64_t steps = (need + want - 1) / want;
   const dim3 grid((unsigned)std::min<int64_t>((need + steps - 1) / steps, 0x7fffffff),
                   (unsigned)p.Hkv, (unsigned)p.B);
   block_scores_kernel<D, NT, E5M2><<<grid, kScoreThreads, smem, stream>>>(p);
