@@ -15,10 +15,10 @@
 // and the matching share of B is 4 consecutive halves of a query's row.  The
 // bytes of the bounds bound it (2 D per block and head, read once); the tensor
 // products of up to 96 rows stay below them.  16 sequences of up to
-// 131072 tokens, 8 heads of 128, blocks of 32: 91 MB in 24.5 us, 3.7 TB/s; what keeps it from
-// the memory's rate is the chain page -> bounds -> products of each warp's step.
-// Eight queries over 262144 tokens are that chain alone, 8.4 us with the queries'
-// staging.
+// 131072 tokens, 8 heads of 128, blocks of 32: 91 MB in 22.4 us, 4.1 TB/s; what
+// keeps it from the memory's rate is the chain lengths -> page -> bounds ->
+// products of each warp.  Eight queries of 6 heads of 256 over 262144 tokens, in
+// blocks of 64, are that chain alone, 6.2 us.
 #include <algorithm>
 
 #include "common.cuh"
@@ -49,13 +49,14 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Score
   float *us = reinterpret_cast<float *>(smem + 2 * NT * 8 * BS * 2) + (threadIdx.x >> 5) * 16 * RS;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const int h = blockIdx.y, b = blockIdx.z;
+  const int h = blockIdx.y / p.parts, b = blockIdx.z;
+  const int i0 = (blockIdx.y - h * p.parts) * p.qn;  // first of the CTA's queries
   const int L = p.seq[(int64_t)b * p.seq_sb];
   const int n = p.seq_has_qlen ? p.seq[(int64_t)b * p.seq_sb + 1] : p.Qmax;
   const bool long_l = L > 0 && (L - 1) / p.blk >= p.cols;  // more blocks than columns
   const bool bad_l = L < 0 || (int64_t)L > (int64_t)p.max_pages * p.nb * p.blk || long_l;
   if (bad_l || n < 0 || n > p.Qmax || (L > 0 && n > L)) {
-    if (blockIdx.x == 0 && h == 0 && tid == 0 && p.status)
+    if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0 && p.status)
       atomicOr(p.status, bad_l ? VAE4_STATUS_BAD_LENGTH : VAE4_STATUS_BAD_QLEN);
     return;
   }
@@ -69,32 +70,8 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Score
     return lane < 16 && j < nblk ? __ldg(p.bt + (int64_t)b * p.bt_sb + j / p.nb) : 0;
   };
   int phys = page_of(j0);
-  // ---- B: the group's rows, split by sign
-  const int rows = n * p.G;
-  for (int x = tid; x < NT * 8 * (D / 8); x += kScoreThreads) {
-    const int r = x / (D / 8), c = x - r * (D / 8), i = r / p.G;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (r < rows)
-      v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __half *>(p.q) + (int64_t)b * p.q_sb +
-                                                (int64_t)i * p.q_si +
-                                                (int64_t)(h * p.G + r - i * p.G) * p.q_sh + 8 * c));
-    uint4 lo, hi;
-    const __half2 z = __float2half2_rn(0.f);
-    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-    uint32_t ph[4], nl[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const __half2 w = *reinterpret_cast<const __half2 *>(&in[e]);
-      const __half2 a = __hmax2_nan(w, z), m = __hmin2_nan(w, z);
-      ph[e] = *reinterpret_cast<const uint32_t *>(&a);
-      nl[e] = *reinterpret_cast<const uint32_t *>(&m);
-    }
-    hi = make_uint4(ph[0], ph[1], ph[2], ph[3]);
-    lo = make_uint4(nl[0], nl[1], nl[2], nl[3]);
-    *reinterpret_cast<uint4 *>(qs + r * BS + 8 * c) = hi;
-    *reinterpret_cast<uint4 *>(qs + (NT * 8 + r) * BS + 8 * c) = lo;
-  }
-  __syncthreads();
+  const int ni = min(n - i0, p.qn);
+  if (ni <= 0) return;
   const float ninf = -__int_as_float(0x7f800000);
   // ---- A: rows g and g + 8 of 16 blocks, 16 bytes per 64 channels; with them
   // this lane's block's scale and the mask of valid blocks
@@ -177,18 +154,44 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Score
     const float sj = __shfl_sync(0xffffffffu, x.s, lane & 15);
     const bool live = (x.okm >> (lane & 15)) & 1u;
     const int jo = jj + (lane & 15);
-    for (int i = lane >> 4; i < n; i += 2) {  // 16 blocks of two queries at a time
+    for (int i = lane >> 4; i < ni; i += 2) {  // 16 blocks of two queries at a time
       float best = ninf;
       for (int k = 0; k < p.G; ++k) best = fmaxf(best, us[(lane & 15) * RS + i * p.G + k]);
       if (jo < nblk) {
-        const bool seen = (int64_t)jo * p.blk <= L - n + i;
-        p.scores[(int64_t)b * p.o_sb + (int64_t)i * p.o_si + (int64_t)h * p.o_sh + jo] =
+        const bool seen = (int64_t)jo * p.blk <= L - n + i0 + i;
+        p.scores[(int64_t)b * p.o_sb + (int64_t)(i0 + i) * p.o_si + (int64_t)h * p.o_sh + jo] =
             live && seen ? best * sj : ninf;
       }
     }
   };
   Tile x;
-  load(x, j0);
+  load(x, j0);  // (on its way while the queries are staged)
+  // ---- B: the group's rows, split by sign
+  const int rows = ni * p.G;
+  for (int x = tid; x < NT * 8 * (D / 8); x += kScoreThreads) {
+    const int r = x / (D / 8), c = x - r * (D / 8), i = r / p.G;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (r < rows)
+      v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __half *>(p.q) + (int64_t)b * p.q_sb +
+                                                (int64_t)(i0 + i) * p.q_si +
+                                                (int64_t)(h * p.G + r - i * p.G) * p.q_sh + 8 * c));
+    uint4 lo, hi;
+    const __half2 z = __float2half2_rn(0.f);
+    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+    uint32_t ph[4], nl[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const __half2 w = *reinterpret_cast<const __half2 *>(&in[e]);
+      const __half2 a = __hmax2_nan(w, z), m = __hmin2_nan(w, z);
+      ph[e] = *reinterpret_cast<const uint32_t *>(&a);
+      nl[e] = *reinterpret_cast<const uint32_t *>(&m);
+    }
+    hi = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+    lo = make_uint4(nl[0], nl[1], nl[2], nl[3]);
+    *reinterpret_cast<uint4 *>(qs + r * BS + 8 * c) = hi;
+    *reinterpret_cast<uint4 *>(qs + (NT * 8 + r) * BS + 8 * c) = lo;
+  }
+  __syncthreads();
   for (;;) {
     use(x, j0);
     if ((j0 += step) >= nblk) break;
@@ -204,24 +207,35 @@ cudaError_t launch_t(const ScoreParams &p, cudaStream_t stream) {
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  // CTAs for one full load of every SM (as far as shared memory allows), whose
-  // warps then take several steps: each CTA reads and splits the queries.  24.5 us
-  // for the batch above, 26.2 with twice the CTAs; the next step's bounds on
-  // their way during one's products cost more registers than they gain (25.8)
-  const int64_t per = kScoreWarps * 16, rows = (int64_t)p.Hkv * p.B;
+  // CTAs for one and a half loads of every SM (as far as shared memory allows),
+  // whose warps then take several steps: each CTA reads and splits the queries,
+  // and those of short sequences leave room early.  22.4 us for the batch above,
+  // 22.9 with one load, 22.8 with two; the next step's bounds on their way during
+  // one's products cost more registers than they gain (1 us)
+  const int64_t per = kScoreWarps * 16, rows = (int64_t)p.Hkv * p.parts * p.B;
   const int64_t need = std::max<int64_t>(1, (p.cols + per - 1) / per);
   const int64_t res = std::max<int64_t>(1, std::min<int64_t>(8, 220 * 1024 / (smem + 1024)));
-  const int64_t want = std::max<int64_t>(1, (res * p.num_sms + rows - 1) / rows);
+  const int64_t want = std::max<int64_t>(1, (3 * res * p.num_sms / 2 + rows - 1) / rows);
   const int64_t steps = (need + want - 1) / want;
   const dim3 grid((unsigned)std::min<int64_t>((need + steps - 1) / steps, 0x7fffffff),
-                  (unsigned)p.Hkv, (unsigned)p.B);
+                  (unsigned)(p.Hkv * p.parts), (unsigned)p.B);
   block_scores_kernel<D, NT, E5M2><<<grid, kScoreThreads, smem, stream>>>(p);
   return cudaGetLastError();
 }
 
 template <int D, bool E5M2>
-cudaError_t launch_n(const ScoreParams &p, cudaStream_t stream) {
-  const int nt = (p.Qmax * p.G + 7) / 8;
+cudaError_t launch_n(ScoreParams p, cudaStream_t stream) {
+  // Few blocks: the queries are split over CTAs until there are two per SM.  The
+  // eight queries above take 6.2 us by twos, 6.4 by fours, 8.8 one by one; all by
+  // one CTA 8.4
+  const int64_t ctas = (p.cols + 16 * kScoreWarps - 1) / (16 * kScoreWarps) * (int64_t)p.Hkv * p.B;
+  p.parts = 1;
+  p.qn = p.Qmax;
+  while (p.qn > 1 && ctas * p.parts < 2ll * p.num_sms) {
+    p.qn = (p.Qmax + 2 * p.parts - 1) / (2 * p.parts);
+    p.parts = (p.Qmax + p.qn - 1) / p.qn;
+  }
+  const int nt = (p.qn * p.G + 7) / 8;
   if (nt <= 1) return launch_t<D, 1, E5M2>(p, stream);
   if (nt <= 2) return launch_t<D, 2, E5M2>(p, stream);
   if (nt <= 3) return launch_t<D, 3, E5M2>(p, stream);

@@ -141,6 +141,7 @@ struct ScoreParams {
   uint32_t *status;              // may be null
   int32_t B, Qmax, Hkv, G, D, nb, blk;  // nb: blocks per page
   int32_t num_sms;               // SMs the grid is sized for
+  int32_t qn, parts;             // queries per CTA, CTAs that share them (set at the launch)
   float sm_scale;
 };
 

@@ -458,6 +458,41 @@ def test_scores_report_pages_and_columns():
     assert torch.isfinite(got[0, 0, 0, [0, 1, 2, 3, 5, 6, 7, 8, 9]]).all()
 
 
+@pytest.mark.parametrize("B,Q,G,Hkv,D,nblk", [
+    (2, 3, 2, 8, 64, 1400), (1, 16, 6, 2, 128, 6000), (40, 1, 8, 8, 128, 520), (1, 7, 12, 1, 256, 700),
+    (1, 5, 3, 4, 64, 2600),
+])
+def test_scores_of_many_blocks(B, Q, G, Hkv, D, nblk):
+    """Grids in which queries share CTAs or not, and warps take several steps."""
+    g = torch.Generator(device="cuda").manual_seed(nblk)
+    blk = 16
+    lens = [(max(1, nblk * blk - 1 - 977 * b % (nblk * blk)), 1 + (Q - 1) * (b + 1) // B) for b in range(B)]
+    lens = [(L, min(n, L)) for L, n in lens]
+    seq = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    table = torch.randperm(B * nblk, generator=g, device="cuda").int().view(B, nblk)
+    x = torch.randn(B * nblk, Hkv, 1, 2, D, generator=g, device="cuda").sort(3).values
+    bd = x.to(torch.float8_e4m3fn).view(torch.uint8)
+    sc = torch.exp2(torch.randint(-3, 4, (B * nblk, 2, Hkv, 1), generator=g, device="cuda").float())
+    q = torch.randn(B, Q, G * Hkv, D, generator=g, device="cuda").half()
+    got = torch.full((B, Q, Hkv, nblk), 7.0, device="cuda")
+    vae4.verify_attn_e4m3_block_scores(q, bd, table, seq, sc, got, block_tokens=blk)
+    for b, (L, n) in enumerate(lens):
+        v = (L - 1) // blk + 1
+        pg = table[b, :v].long()
+        lohi = bd[pg, :, 0].view(torch.float8_e4m3fn).double()  # [v][H][2][D]
+        s = sc[pg, 0, :, 0].double() / math.sqrt(D)
+        assert (got[b, n:] == 7).all() and (got[b, :, :, v:] == 7).all()  # left as they were
+        for i in range(n):
+            qq = q[b, i].double().view(Hkv, G, D)
+            want = (torch.einsum("hgd,vhd->vhg", qq.clamp(min=0), lohi[:, :, 1]) +
+                    torch.einsum("hgd,vhd->vhg", qq.clamp(max=0), lohi[:, :, 0])).amax(-1) * s
+            mags = torch.einsum("hgd,vhd->vhg", qq.abs(), lohi.abs().amax(2)).amax(-1) * s
+            hidden = torch.arange(v, device="cuda") * blk > L - n + i
+            r = got[b, i, :, :v].T.double()
+            assert (r[hidden] == -math.inf).all()
+            assert ((r - want).abs() <= (2 * D + 4) * 2.0 ** -24 * mags)[~hidden].all()
+
+
 # ------------------------------------------------------------------ choice of blocks
 def choose(row, v, k, sink, local):
     if v <= k:
