@@ -23,8 +23,9 @@
 // Within 2^-40 .. 2^40 no scale makes a weight or a sum overflow.
 //
 // Warp roles (20 warps; a 21st would leave a sixth warp on one scheduler and 80
-// instead of 96 registers per thread: 1.2 times as long), each running through all segments so that the copies
-// and decodes of a segment overlap the end of the previous one:
+// instead of 96 registers per thread: 1.2 times as long), each running through
+// all segments so that the copies and decodes of a segment overlap the end of
+// the previous one:
 //   K / V producer  : walk the block table (or the visit list) and issue TMA
 //                     loads (128-byte swizzle) of 16, 32 or 64 keys, whatever
 //                     the page (block) is a multiple of, into rings of raw
@@ -43,7 +44,10 @@
 //                     of a row is raised only when a weight would pass 2^15
 //                     (one vote per tile); then only the rows concerned, and
 //                     only the groups of 8 accumulator columns that hold them,
-//                     are rescaled.  At a segment's end they load the next
+//                     are rescaled.  (The first tile raises every row: its
+//                     maxima by one warp reduction per row instead of shuffles
+//                     took 262144 tokens of 48 rows of 256 from 43.0 to 37.3
+//                     us.)  At a segment's end they load the next
 //                     segment's queries while the value product runs, then
 //                     write the rows out.
 //
@@ -151,6 +155,13 @@ __device__ __forceinline__ int div16(int key, unsigned long long m) {
   return (int)((unsigned long long)(unsigned)(key >> 4) * m >> 38);
 }
 
+// maximum over the warp (a NaN does not count)
+__device__ __forceinline__ float warp_max(float x) {
+  float d;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;\n" : "=f"(d) : "f"(x));
+  return d;
+}
+
 // ---------------------------------------------------------------------------
 // The plan: which segments a CTA walks.
 
@@ -162,11 +173,6 @@ __device__ __forceinline__ int2 group_len(const SegParams &p, int x) {
   const bool live = L > 0 && L <= p.capacity && ql > 0 && ql <= p.Qmax && ql <= L;
   return make_int2(live ? L : 0, ql);
 }
-
-struct Line {
-  int total;  // places of the line (below 2^30)
-  int q;      // places per CTA
-};
 
 // Where the plan's lengths come from: staged in shared memory, read as they
 // are (st = null), or, for a dry run, one invented group.
@@ -188,48 +194,79 @@ __device__ __forceinline__ int row_groups(const SegParams &p, int2 v, int N) {
 }
 __device__ __forceinline__ int unit_places(int2 v) { return kUnitCost + (v.x + 63) / 64; }
 
-// One warp: the line's length (four groups per lane in flight).
-static __device__ __noinline__ Line plan_line(const SegParams &p, Lengths len, int N, int lane) {
-  int sum = 0;
-  for (int x0 = 0; x0 < len.groups; x0 += 128) {
-    int2 v[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[e] = len.of(p, x0 + 32 * e + lane);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) sum += p.unit_heads * row_groups(p, v[e], N) * unit_places(v[e]);
-  }
-  Line l;
-  l.total = (int)__reduce_add_sync(0xffffffffu, (unsigned)sum);
-  l.q = l.total > 0 ? (l.total + p.ctas - 1) / p.ctas : 1;
-  return l;
-}
-
-// One warp: the segments of CTA `cta` from place `from` on into seg[], at
-// most kMaxSeg; returns how many, and in *next the place to go on from (its
-// end: the CTA's last place).  The CTA where a unit starts records its first
-// CTA and its parts for the combine (parts = -1: finished in one CTA).
+// One warp: the segments of CTA `cta` into seg[], at most kMaxSeg, from place
+// state[2] on (first: from the CTA's first, after the line's length has been
+// counted); leaves the line and the place to go on from (its end: the CTA's
+// last place) in state[0 .. 2] and (segments, 1 if more follow) in state[-2],
+// state[-1].  The CTA where a unit starts records its first CTA and its parts
+// for the combine (parts = -1: finished in one CTA).
+// A batch of up to 32 groups is read by the warp itself and scanned once.
 template <bool LISTED>
-static __device__ __noinline__ int plan_segments(const SegParams &p, Lengths len, int N, Line l,
-                                                 int cta, int from, int *next, Segment *seg,
-                                                 int *bad, int lane) {
-  const int end = min((cta + 1) * l.q, l.total);
-  int n = 0;
-  int base = 0;  // place where group x0 starts
-  for (int x0 = 0; x0 < len.groups && base < end; x0 += 32) {
-    const int x = x0 + lane;
-    const int2 v = len.of(p, x);
-    const int rgs = row_groups(p, v, N), pl = unit_places(v);
-    const int cost = p.unit_heads * rgs * pl;
-    int incl = cost;
+static __device__ __noinline__ void plan_segments(const SegParams &p, Lengths len, int N, int cta,
+                                                  bool first, volatile int *state, Segment *seg,
+                                                  int *bad, int lane) {
+  int2 v = make_int2(0, 0);
+  int2 vis = make_int2(0, 0);  // LISTED: tokens to walk and length of the stream
+  const bool known = LISTED && len.groups <= 32 && !len.dry;
+  if (known) {
+    if (lane < len.groups) {
+      const BlockStream r = p.streams[lane];
+      v = make_int2(r.ql > 0 ? r.n16 : 0, r.ql);  // (the list's writer has checked them)
+      vis = make_int2(r.n, r.L);
+    }
+  } else {
+    v = len.of(p, lane);
+  }
+  int rgs, pl, cost, incl;
+  auto scan = [&]() {  // the lane's places, and those up to its end in the chunk
+    rgs = row_groups(p, v, N);
+    pl = unit_places(v);
+    cost = p.unit_heads * rgs * pl;
+    incl = cost;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int t = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += t;
     }
+  };
+  scan();
+  int total, q, from;
+  if (first) {
+    total = __shfl_sync(0xffffffffu, incl, 31);
+    if (len.groups > 32) {
+      int sum = 0;
+      for (int x0 = 32; x0 < len.groups; x0 += 128) {
+        int2 w[4];  // four groups per lane in flight
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = len.of(p, x0 + 32 * e + lane);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          sum += p.unit_heads * row_groups(p, w[e], N) * unit_places(w[e]);
+      }
+      total += (int)__reduce_add_sync(0xffffffffu, (unsigned)sum);
+    }
+    q = total > 0 ? (total + p.ctas - 1) / p.ctas : 1;
+    from = cta * q;
+  } else {
+    total = state[0];
+    q = state[1];
+    from = state[2];
+  }
+  const int end = min((cta + 1) * q, total);
+  int n = 0, next = end;
+  int base = 0;  // place where group x0 starts
+  for (int x0 = 0; x0 < len.groups && base < end; x0 += 32) {
+    if (x0 > 0) {
+      v = len.of(p, x0 + lane);
+      scan();
+    }
     const int start = base + incl - cost;
-    unsigned hit = __ballot_sync(0xffffffffu, cost > 0 && start < end && start + cost > from);
+    const bool is_hit = cost > 0 && start < end && start + cost > from;
+    if (LISTED && is_hit && !known && !len.dry) {
+      const BlockStream rec = p.streams[x0 + lane];
+      vis = make_int2(rec.n, rec.L);
+    }
+    unsigned hit = __ballot_sync(0xffffffffu, is_hit);
     base += __shfl_sync(0xffffffffu, incl, 31);
     while (hit) {
       const int src = __ffs(hit) - 1;
@@ -237,13 +274,14 @@ static __device__ __noinline__ int plan_segments(const SegParams &p, Lengths len
       const int gs = __shfl_sync(0xffffffffu, start, src);
       const int n_rg = __shfl_sync(0xffffffffu, rgs, src), gp = __shfl_sync(0xffffffffu, pl, src);
       const int gl = __shfl_sync(0xffffffffu, v.x, src), gq = __shfl_sync(0xffffffffu, v.y, src);
+      const int vn = __shfl_sync(0xffffffffu, vis.x, src), vl = __shfl_sync(0xffffffffu, vis.y, src);
       const int gu = p.unit_heads * n_rg, nh = gp - kUnitCost;
-      const int u0 = from > gs ? (from - gs) / gp : 0;
+      const int u0 = from > gs + gp ? (from - gs) / gp : 0;
       for (int ub = u0; ub < gu && gs + ub * gp < end; ub += 32) {
         const int u = min(ub + lane, gu);
         const int us = gs + u * gp + kUnitCost;  // place of its first half-tile
         // half-tiles in this CTA (at most once per CTA: `from` is a unit's start later on)
-        const int a = max(us, cta * l.q), z = min(us + nh, end);
+        const int a = max(us, cta * q), z = min(us + nh, end);
         const bool mine = u < gu && z > a && us - kUnitCost + gp > from;
         const unsigned m = __ballot_sync(0xffffffffu, mine);
         const int at = n + __popc(m & ((1u << lane) - 1u));
@@ -260,16 +298,15 @@ static __device__ __noinline__ int plan_segments(const SegParams &p, Lengths len
           s.slot = !starts ? p.ctas + cta : ends ? -1 : cta;
           s.pad = 0;
           if (LISTED && !len.dry) {
-            const BlockStream rec = p.streams[s.b];
             s.h_rg = s.b % p.Hkv | rg << 16;
-            s.k1 = min(s.k1, rec.n);
-            s.L = rec.L;
+            s.k1 = min(s.k1, vn);
+            s.L = vl;
           }
           seg[at] = s;
           bad[at] = 0;
           if (starts && !len.dry) {
             const int str = LISTED ? s.b : s.b * p.Hkv + h;
-            const int parts = ends ? -1 : (us + nh - 1) / l.q - cta + 1;
+            const int parts = ends ? -1 : (us + nh - 1) / q - cta + 1;
             p.tab[(int64_t)str * p.n_rg + rg] = make_int2(cta, parts);
           }
         }
@@ -278,16 +315,22 @@ static __device__ __noinline__ int plan_segments(const SegParams &p, Lengths len
           const int left = __popc(m) - (n - kMaxSeg);  // of this round's that fit
           unsigned mm = m;
           for (int k = 0; k < left; ++k) mm &= mm - 1;
-          *next = gs + (ub + __ffs(mm) - 1) * gp;
-          __syncwarp();
-          return kMaxSeg;
+          next = gs + (ub + __ffs(mm) - 1) * gp;
+          n = kMaxSeg;
+          goto done;
         }
       }
     }
   }
-  *next = end;
+done:
   __syncwarp();
-  return n;
+  if (lane == 0) {
+    state[0] = total;
+    state[1] = q;
+    state[2] = next;
+    state[-2] = n;
+    state[-1] = n > 0 && next < end;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -370,7 +413,8 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
   uint8_t *gP = gbase + C::OFF_P, *gKR = gbase + C::OFF_KR, *gSm = gbase + C::OFF_SMALL;
   auto bar = [&](int i) -> uint32_t { return sSm + 8u * (uint32_t)i; };
   volatile int *abort_f = reinterpret_cast<volatile int *>(gSm + C::S_SCAL);
-  int *nseg_s = reinterpret_cast<int *>(gSm + C::S_SCAL + 8);   // segments, 1 if more follow
+  // segments, 1 if more follow; the line's places, those per CTA, the next place
+  int *nseg_s = reinterpret_cast<int *>(gSm + C::S_SCAL + 8);
   Segment *seg_s = reinterpret_cast<Segment *>(gSm + C::S_SEG);
   int *bad_s = reinterpret_cast<int *>(gSm + C::S_BAD);         // per segment
 
@@ -408,12 +452,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
     // ends and the barriers and TMEM are set up: its instructions are then at
     // hand when the lengths arrive (6000 cycles for the first run, 400 for the
     // next).
-    Segment *seg = reinterpret_cast<Segment *>(gSm + C::S_SEG);
-    int next;
-    const Lengths dry{nullptr, 1, true};
-    const Line l = plan_line(p, dry, N, lane);
-    plan_segments<LISTED>(p, dry, N, l, 0, 0, &next, seg,
-                          reinterpret_cast<int *>(gSm + C::S_BAD), lane);
+    plan_segments<LISTED>(p, Lengths{nullptr, 1, true}, N, 0, true, nseg_s + 2, seg_s, bad_s, lane);
   }
   if (warp == kWQk) {
     tc::tmem_alloc(sSm + C::S_SCAL + 4, 512);
@@ -437,35 +476,21 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
   // and segments (score MMA) or groups of scales (softmax, K producer)
   int count = 0, count2 = 0;
   bool mma_issued = false;
-  Line *line_s = reinterpret_cast<Line *>(gSm + C::S_SCAL + 16);
-  int *place_s = reinterpret_cast<int *>(gSm + C::S_SCAL + 24);
   bool first = true;
 
   for (;;) {  // up to kMaxSeg segments at a time
-    // ---- the plan, by the K producer, from lengths that all threads stage in
-    // the K ring (idle here); a batch that does not fit is read as it is
-    const bool staged = p.groups <= C::NKR * C::RSLOT / 8;
+    // ---- the plan, by the K producer; the lengths of more than 32 groups are
+    // staged by all threads in the K ring (idle here), but read as they are if
+    // they do not fit
+    const bool staged = p.groups > 32 && p.groups <= C::NKR * C::RSLOT / 8;
     int2 *st_len = reinterpret_cast<int2 *>(gKR);
     if (staged) {
       for (int x = tid; x < p.groups; x += C::NTHREADS) st_len[x] = group_len(p, x);
       __syncthreads();
     }
-    if (warp == kWKProd) {
-      const Lengths len{staged ? st_len : nullptr, p.groups, false};
-      const Line line = first ? plan_line(p, len, N, lane) : *line_s;
-      const int place = first ? cta * line.q : *place_s;
-      int next = place, n = 0;
-      const int end = min((cta + 1) * line.q, line.total);
-      if (place < end)
-        n = plan_segments<LISTED>(p, len, N, line, cta, place, &next, seg_s, bad_s, lane);
-      __syncwarp();
-      if (lane == 0) {
-        *line_s = line;
-        *place_s = next;
-        nseg_s[0] = n;
-        nseg_s[1] = n > 0 && next < end;
-      }
-    }
+    if (warp == kWKProd)
+      plan_segments<LISTED>(p, Lengths{staged ? st_len : nullptr, p.groups, false}, N, cta, first,
+                            nseg_s + 2, seg_s, bad_s, lane);
     if (staged) tc::fence_proxy_async_smem();  // the ring is next written by tensor copies
     __syncthreads();
     const int nseg = nseg_s[0];
@@ -1008,23 +1033,21 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
           // did any score of the tile exceed its row's threshold (the four warps
           // of the column group; the other group's rows are its own affair)
           if (tc::named_bar_or(2 + cg, 128, exceed)) {
-            // tile maxima over the 128 keys of the rows concerned
+            // maxima over the tile's 128 keys; a row is raised if its own passes
+            // its threshold
+            float mine = -kInf;
 #pragma unroll
             for (int c = 0; c < C::NC; ++c) {
-              float mx = -kInf;
-              if (__any_sync(0xffffffffu, t[c] > thr[c])) {
-                mx = t[c];
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-              }
-              if (lane == 0) red[warp * 32 + c] = mx;
+              const float mx = warp_max(t[c]);
+              if (lane == c) mine = mx;
             }
+            if (lane < C::NC) red[warp * 32 + lane] = mine;
             tc::named_bar(2 + cg, 128);
             if (q == 0 && lane < C::NC) {  // one warp per column group combines the quadrants
               float mt = red[(cg * 4) * 32 + lane];
 #pragma unroll
               for (int qq = 1; qq < 4; ++qq) mt = fmaxf(mt, red[(cg * 4 + qq) * 32 + lane]);
-              const float mn = fmaxf(m_s[mb * 64 + col0 + lane], mt);
+              const float mn = mt > thr[lane] ? mt : m_s[mb * 64 + col0 + lane];
               const int o = (mb ^ 1) * 64 + col0 + lane;
               m_s[o] = mn;
               base_s[o] = mn == -kInf ? 0.f : mn;
@@ -1032,11 +1055,11 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
             }
             tc::named_bar(2 + cg, 128);
             const float *mo = m_s + mb * 64 + col0, *mn = m_s + (mb ^ 1) * 64 + col0;
-            // factors 2^(m_old - m_new) for the running sums ...
-#pragma unroll
-            for (int c = 0; c < C::NC; ++c)
-              if (mn[c] != mo[c]) lpart[c] *= fast_exp2(mo[c] - mn[c]);
             if (jl > 0) {
+              // factors 2^(m_old - m_new) for the running sums ...
+#pragma unroll
+              for (int c = 0; c < C::NC; ++c)
+                lpart[c] *= mn[c] == mo[c] ? 1.f : fast_exp2(mo[c] - mn[c]);
               // ... and for the O^T columns, once P.V of the previous tile is done
               alive = alive && tc::mbar_wait_brief(bar(kPvDone + (j - 1) % C::NPT),
                                              ((j - 1) / C::NPT) & 1, abort_f, LIM);
@@ -1104,11 +1127,22 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
 
         // ---- the segment's end: row sums, then the rows out of TMEM
 #pragma unroll
-        for (int c = 0; c < C::NC; ++c) {
-          float sm = lpart[c];
+        for (int c8 = 0; c8 < C::NC; c8 += 8) {  // eight rows at a time, halved at each exchange
+          float v8[8];
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) sm += __shfl_xor_sync(0xffffffffu, sm, o);
-          if (lane == 0) red[warp * 32 + c] = sm;
+          for (int e = 0; e < 8; ++e) v8[e] = lpart[c8 + e];
+#pragma unroll
+          for (int o = 16, k = 4; k > 0; o >>= 1, k >>= 1) {
+            const bool up = lane & o;
+#pragma unroll
+            for (int e = 0; e < k; ++e)
+              v8[e] = (up ? v8[e + k] : v8[e]) +
+                      __shfl_xor_sync(0xffffffffu, up ? v8[e] : v8[e + k], o);
+          }
+          float sm = v8[0];
+          sm += __shfl_xor_sync(0xffffffffu, sm, 2);
+          sm += __shfl_xor_sync(0xffffffffu, sm, 1);
+          if ((lane & 3) == 0) red[warp * 32 + c8 + (lane >> 2)] = sm;
         }
         if (q == 0 && lane == 0) mb_s[cg] = mb;
         const int jz = count - 1;  // the segment's last tile
