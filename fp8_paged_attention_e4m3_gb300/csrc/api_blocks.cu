@@ -242,6 +242,7 @@ int verify_attn_e4m3_block_scores(const vae4_tensor *q, const vae4_tensor *k_bou
   const int64_t n_pages = k_bounds->shape[0], Hkv = k_bounds->shape[1], nb = k_bounds->shape[2];
   rc = check_bounds(k_bounds, n_pages, Hkv, nb, D);
   if (rc) return rc;
+  if (Hkv > kMaxBlockedHeads) return VAE4_ERR_SHAPE;
   if (Hq % Hkv != 0) return VAE4_ERR_GQA;
   if (align_up(Qmax * (Hq / Hkv), 16) > kMaxRowsPad) return VAE4_ERR_UNSUPPORTED;
   if (block_tokens < 16 || block_tokens % 16 != 0 || nb * block_tokens > 65536)

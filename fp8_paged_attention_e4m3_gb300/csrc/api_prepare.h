@@ -266,6 +266,8 @@ inline int check_ids(const vae4_tensor *ids, int64_t B, int64_t Qmax, int64_t Hk
 // (max, sum) [2 CTAs][N][2] | unnormalised O [2 CTAs][N][D] | (first CTA,
 // parts) [streams][row groups] | sparse attention (k > 0): stream records |
 // visit lists [streams][list_cap].
+constexpr int kMaxSegCtas = 4096;            // the combine holds two floats of each part
+constexpr int64_t kMaxBlockedHeads = 65535;  // a segment's KV head is held in 16 bits
 struct BlockPlan {
   int64_t streams, list_cap;
   int n_rg, N, ctas;
@@ -276,7 +278,7 @@ inline int plan_blocks(int64_t B, int64_t Hkv, int64_t Qmax, int64_t rows, int64
                        int64_t blk, int64_t k, int sms, BlockPlan *o) {
   memset(o, 0, sizeof(*o));
   o->streams = B * Hkv;
-  if (o->streams > INT32_MAX / 64 || sms < 1) return VAE4_ERR_SHAPE;
+  if (o->streams > INT32_MAX / 64 || Hkv > kMaxBlockedHeads || sms < 1) return VAE4_ERR_SHAPE;
   int64_t tokens = cap;  // most that a stream walks
   if (k > 0) {
     const int64_t nblk = (cap + blk - 1) / blk;
@@ -285,7 +287,8 @@ inline int plan_blocks(int64_t B, int64_t Hkv, int64_t Qmax, int64_t rows, int64
     tokens = o->list_cap * blk;
   }
   tc_row_groups((int)rows, &o->n_rg, &o->N);
-  o->ctas = (int)std::min<int64_t>(sms, o->streams * o->n_rg * ((tokens + 63) / 64));
+  o->ctas = (int)std::min<int64_t>(std::min(sms, kMaxSegCtas),
+                                   o->streams * o->n_rg * ((tokens + 63) / 64));
   // places of the plan's line (see seg_tc.cuh), in 32 bits on the device
   if (o->streams * o->n_rg * ((tokens + 63) / 64 + 3) >= (1ll << 30)) return VAE4_ERR_SHAPE;
   o->ml_off = kStatusBytes;
@@ -390,7 +393,7 @@ inline int prepare(const vae4_tensor *q, const vae4_tensor *kv, const vae4_tenso
     if (rc) return rc;
   }
   int T = 0, P = 0;
-  if (B > 0) {
+  if (B > 0 && !blocked) {
     rc = do_plan((int)B, (int)Hkv, (int)cap, o.partition_tokens, sms, &T, &P);
     if (rc) return rc;
   }

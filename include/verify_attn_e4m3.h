@@ -513,8 +513,8 @@ int verify_attn_e4m3_append(const vae4_tensor *k_new, const vae4_tensor *v_new,
  *              bytes.
  * The batch's keys are divided evenly among the SMs on the device, from the
  * lengths of the call (so a captured graph stays balanced as they change):
- * opt->partition_tokens must be 0 (VAE4_ERR_PARTITION).  Repeated calls give
- * the same bits.  hilo_pv and VAE4_FLAG_WARP_MMA: VAE4_ERR_UNSUPPORTED.
+ * opt->partition_tokens must be 0 (VAE4_ERR_PARTITION).  At most 65535 KV
+ * heads; num_sms counts up to 4096.  Repeated calls give the same bits.  hilo_pv and VAE4_FLAG_WARP_MMA: VAE4_ERR_UNSUPPORTED.
  */
 int verify_attn_e4m3_block_scaled(const vae4_tensor *q, const vae4_tensor *k_cache,
                                   const vae4_tensor *v_cache, const vae4_tensor *block_table,
@@ -577,8 +577,8 @@ int verify_attn_e4m3_select_blocks(const vae4_tensor *scores, const vae4_tensor 
  *  workspace   at least verify_attn_e4m3_sparse_workspace_bytes(...) bytes.
  * A block that several queries of a KV head list is read once.  A sequence
  * may have at most 98304 blocks (capacity / S; else VAE4_ERR_UNSUPPORTED).
- * opt->partition_tokens must be 0 (VAE4_ERR_PARTITION), as above.  Pages and scales of blocks outside every list
- * are not looked at.
+ * opt->partition_tokens must be 0 (VAE4_ERR_PARTITION), as above.  Pages and
+ * scales of blocks outside every list are not looked at.
  */
 int verify_attn_e4m3_sparse(const vae4_tensor *q, const vae4_tensor *k_cache,
                             const vae4_tensor *v_cache, const vae4_tensor *block_table,

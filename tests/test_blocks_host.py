@@ -89,6 +89,12 @@ NULL, DTYPE, SHAPE, STRIDE, ALIGN, UNSUP, GQA, WS, PART, OPT = (-1, -2, -3, -4, 
     (ALL, dict(seq=_t(I32, [B, 3])), SHAPE),
     (("scores",), dict(scores=_t(F32, [B, Q, 1, 40])), SHAPE),
     (("append",), dict(bt=_t(I32, [B, 1 << 24])), SHAPE),                 # past 2^30 tokens
+    # more KV heads than a segment's record holds
+    (("attend",), dict(q=_t(F16, [B, Q, 65536, D]), out=_t(F16, [B, Q, 65536, D]),
+                       k=_t(U8, [NPG, PAGE, 65536, D]), v=_t(U8, [NPG, PAGE, 65536, D]),
+                       sc=_t(F32, [NPG, 2, 65536, NB])), SHAPE),
+    (("scores",), dict(q=_t(F16, [B, Q, 65536, D]), bd=_t(U8, [NPG, 65536, NB, 2, D]),
+                       sc=_t(F32, [NPG, 2, 65536, NB]), scores=_t(F32, [B, Q, 65536, 40])), SHAPE),
     # blocks: 24 tokens, 32 tokens of a page of 96 are no multiple / divisor
     (("append", "attend", "sparse"), dict(sc=_t(F32, [NPG, 2, HKV, 4])), UNSUP),
     (("append", "attend", "sparse"), dict(sc=_t(F32, [NPG, 2, HKV, 5])), UNSUP),
@@ -189,6 +195,8 @@ def test_workspace_bytes():
     assert bs(2, 12, 2, 8, D, 1536, 152) == dense(4, 1, 48, D, 24)    # 48 rows
     assert bs(1, 6, 1, 16, 256, 262144, 152) == dense(1, 2, 48, 256, 4096)  # two row groups
     assert bs(1, 2, 1, 1, 64, 100, 152) == dense(1, 1, 16, 64, 2)     # two pieces
+    # beyond 4096 CTAs the combine would not hold a unit's parts
+    assert bs(1, 2, 1, 1, 64, 1 << 20, 4096) == bs(1, 2, 1, 1, 64, 1 << 20, 10000)
     # 2 sequences x 2 KV heads, 5 blocks of 48 tokens for each of 8 queries
     entries = min(-(-1536 // 48), 8 * 5)
     n = al(al(dense(4, 1, 48, D, 24)) + 4 * 16) + 4 * entries * 32

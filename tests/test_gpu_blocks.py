@@ -176,6 +176,8 @@ ATTEND = [
     ([(70, 4)] * 33, 4, 12, 2, 256, 64, 64, "e4m3", "pool"),
     ([(9000, 1)] + [(5, 1)] * 900, 1, 2, 2, 64, 16, 16, "e4m3", "tokens"),
     ([(20, 1)] * 1500, 1, 1, 8, 64, 32, 32, "e4m3", "tokens"),
+    # more sequences than the plan stages
+    ([(1 + b % 40, 1) for b in range(4500)], 1, 2, 1, 64, 16, 16, "e4m3", "tokens"),
 ]
 
 
@@ -203,6 +205,50 @@ def test_attention_divided_among_other_numbers_of_sms(sms):
     check(got, *reference(c, q))
     again, _ = attend(c, q, num_sms=sms)
     assert torch.equal(got, again)
+
+
+def test_attention_over_more_parts_than_the_combine_holds():
+    """num_sms beyond 4096 counts as 4096."""
+    c = Cache([(420000, 1)], 1, 64, 64, 64, seed=14)
+    q = queries(c, 1, 2)
+    got, status = attend(c, q, num_sms=10000)
+    assert status == 0
+    check(got, *reference(c, q))
+    again, _ = attend(c, q, num_sms=4096)
+    assert torch.equal(got, again)
+
+
+def test_calls_at_once_on_two_streams():
+    """Calls on two streams, each with its own workspace and outputs, give what
+    they give alone."""
+    c = Cache([(6000, 2), (900, 3), (3100, 1)], 2, 128, 32, 16, seed=15)
+    q = queries(c, 3, 4)
+    k, v = c.device()
+    qd, bt, seq, sc = dev(q, c.table, c.seq, c.scales)
+    ids = random_ids(c, 3, 40).cuda()
+    cap = c.table.shape[1] * c.page
+    outs = [torch.empty(12, *qd.shape, dtype=torch.float16, device="cuda") for _ in range(4)]
+    ws = [vae4.alloc_workspace(3, 8, 2, 3, 128, cap), vae4.alloc_sparse_workspace(3, 8, 2, 3, 128, cap, 16, 40)]
+    ws += [w.clone() for w in ws]
+
+    def both(o, w, n, stream):
+        for x in range(n):
+            vae4.verify_attn_e4m3_block_scaled(qd, k, v, bt, seq, sc, o[0][x], w[0], stream=stream)
+            vae4.verify_attn_e4m3_sparse(qd, k, v, bt, seq, sc, ids, o[1][x], w[1], stream=stream)
+
+    both(outs[:2], ws[:2], 1, None)
+    torch.cuda.synchronize()
+    want = [outs[0][0].clone(), outs[1][0].clone()]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for o in outs:
+        o.fill_(float("nan"))
+    torch.cuda.synchronize()
+    both(outs[:2], ws[:2], 12, streams[0])
+    both(outs[2:], ws[2:], 12, streams[1])
+    torch.cuda.synchronize()
+    for e, o in enumerate(outs):
+        assert (o == want[e % 2]).all()
+    assert all(vae4.read_status(w) == 0 for w in ws)
 
 
 def test_waits_that_run_out_mark_the_rows():
@@ -328,6 +374,7 @@ SPARSE = [
     ([(1200, 4), (800, 4)], 4, 3, 2, 64, 48, 16, 10, "e4m3", "padded"),
     ([(600, 2)] * 50, 2, 2, 3, 64, 32, 32, 4, "e4m3", "tokens"),
     ([(40, 1)] * 520, 1, 1, 2, 64, 16, 16, 2, "e4m3", "tokens"),   # more than 1024 streams
+    ([(1 + b % 70, 1) for b in range(2100)], 1, 1, 2, 64, 16, 16, 2, "e4m3", "tokens"),  # 4200
     ([(5000, 2)], 2, 4, 1, 128, 848, 848, 3, "e4m3", "tokens"),
     ([(5000, 2)], 2, 4, 1, 128, 848, 848, 3, "e4m3", "padded"),
     ([(4000, 3)], 3, 4, 1, 256, 32, 16, 200, "e4m3", "pool"),      # one stream over many SMs
@@ -717,6 +764,43 @@ def test_append_refuses_pages_scales_and_lengths():
 
 
 # ------------------------------------------------------------------ together
+def test_caches_past_32_bit_offsets():
+    """Pages, scales and bounds a GB apart: the same bits as when they lie
+    together."""
+    gb = 1 << 30
+    c = Cache([(250, 3), (60, 2)], 2, 128, 64, 32, seed=16, extra=1)
+    q, bd = queries(c, 3, 4), bounds_of(c)
+    k_new = torch.randn(2, 3, 2, 128, generator=torch.Generator().manual_seed(1)).half()
+    assert c.n_pages == 6
+    buf = torch.zeros(6 * gb, dtype=torch.uint8, device="cuda")
+    near = dict(k=c.codes[0].cuda(), v=c.codes[1].cuda(), sc=c.scales.cuda(), bd=bd.cuda())
+    far = dict(k=buf.as_strided((6, 64, 2, 128), (gb, 256, 128, 1)),
+               v=buf.as_strided((6, 64, 2, 128), (gb, 256, 128, 1), gb // 4),
+               sc=buf.view(torch.float32).as_strided((6, 2, 2, 2), (gb // 4, 4, 2, 1), gb // 8),
+               bd=buf.as_strided((6, 2, 2, 2, 128), (gb, 1024, 512, 128, 1), 3 * gb // 4))
+    for name, t in near.items():
+        far[name].copy_(t)
+    qd, bt, seq, kd = dev(q, c.table, c.seq, k_new)
+    got = []
+    for d in (near, far):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        outs = [torch.zeros_like(qd), torch.zeros_like(qd)]
+        scores = torch.zeros(2, 3, 2, 8, device="cuda")
+        ids = torch.zeros(2, 3, 2, 4, dtype=torch.int32, device="cuda")
+        ws = vae4.alloc_sparse_workspace(2, 8, 2, 3, 128, 64 * c.table.shape[1], 32, 4)
+        wd = vae4.alloc_workspace(2, 8, 2, 3, 128, 64 * c.table.shape[1])
+        vae4.verify_attn_e4m3_append(kd, kd, d["k"], d["v"], bt, seq, d["sc"], k_bounds=d["bd"], status=status)
+        vae4.verify_attn_e4m3_block_scaled(qd, d["k"], d["v"], bt, seq, d["sc"], outs[0], wd)
+        vae4.verify_attn_e4m3_block_scores(qd, d["bd"], bt, seq, d["sc"], scores, block_tokens=32, status=status)
+        vae4.verify_attn_e4m3_select_blocks(scores, seq, ids, block_tokens=32, local_blocks=1, status=status)
+        vae4.verify_attn_e4m3_sparse(qd, d["k"], d["v"], bt, seq, d["sc"], ids, outs[1], ws)
+        assert int(status) == 0 and vae4.read_status(ws) == 0 and vae4.read_status(wd) == 0
+        assert outs[0].any() and torch.isfinite(outs[0]).all()
+        got.append([d["k"], d["v"], d["sc"].contiguous().view(torch.int32), d["bd"], scores, ids] + outs)
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("graph", [False, True])
 @pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
 def test_decoding_steps_together(graph, fmt):
