@@ -15,9 +15,9 @@
 // and the matching share of B is 4 consecutive halves of a query's row.  The
 // bytes of the bounds bound it (2 D per block and head, read once); the tensor
 // products of up to 96 rows stay below them.  16 sequences of up to
-// 131072 tokens, 8 heads of 128, blocks of 32: 91 MB in 22.4 us, 4.1 TB/s; what
-// keeps it from the memory's rate is the chain lengths -> page -> bounds ->
-// products of each warp.  Eight queries of 6 heads of 256 over 262144 tokens, in
+// 131072 tokens, 8 heads of 128, blocks of 32: 91 MB in 21.9 us, 4.2 TB/s; what
+// keeps it from the memory's rate is the start of the chain (page, queries and
+// lengths, asked for together -> bounds -> products) and the ragged end.  Eight queries of 6 heads of 256 over 262144 tokens, in
 // blocks of 64, are that chain alone, 6.2 us.
 #include <algorithm>
 
@@ -51,6 +51,24 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Score
   const int g = lane >> 2, t = lane & 3;
   const int h = blockIdx.y / p.parts, b = blockIdx.z;
   const int i0 = (blockIdx.y - h * p.parts) * p.qn;  // first of the CTA's queries
+  // requested together: the lengths, the thread's first chunks of the queries
+  // (padding rows are part of the tensor) and the page of its first block
+  constexpr int kChunks = NT * 8 * (D / 8);
+  auto query = [&](int x) -> uint4 {
+    const int r = x / (D / 8), c = x - r * (D / 8), i = r / p.G;
+    if (x >= kChunks || r >= p.qn * p.G || i0 + i >= p.Qmax) return make_uint4(0u, 0u, 0u, 0u);
+    return __ldg(reinterpret_cast<const uint4 *>(static_cast<const __half *>(p.q) + (int64_t)b * p.q_sb +
+                                                 (int64_t)(i0 + i) * p.q_si +
+                                                 (int64_t)(h * p.G + r - i * p.G) * p.q_sh + 8 * c));
+  };
+  constexpr int kQ = kChunks < 4 * kScoreThreads ? (kChunks + kScoreThreads - 1) / kScoreThreads : 4;
+  uint4 qv[kQ];
+#pragma unroll
+  for (int e = 0; e < kQ; ++e) qv[e] = query(tid + e * kScoreThreads);
+  int j0 = (blockIdx.x * kScoreWarps + warp) * 16;
+  int phys = 0;
+  if (const int lp = (j0 + lane) / p.nb; lane < 16 && lp < p.max_pages)
+    phys = __ldg(p.bt + (int64_t)b * p.bt_sb + lp);
   const int L = p.seq[(int64_t)b * p.seq_sb];
   const int n = p.seq_has_qlen ? p.seq[(int64_t)b * p.seq_sb + 1] : p.Qmax;
   const bool long_l = L > 0 && (L - 1) / p.blk >= p.cols;  // more blocks than columns
@@ -62,14 +80,12 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Score
   }
   const int nblk = L > 0 && n > 0 ? (L - 1) / p.blk + 1 : 0;
   const int step = gridDim.x * kScoreWarps * 16;
-  int j0 = (blockIdx.x * kScoreWarps + warp) * 16;
   if (blockIdx.x * kScoreWarps * 16 >= nblk) return;  // (a warp past the end stores nothing)
   // the page and scale of block j0 + lane (lanes 0 .. 15)
   auto page_of = [&](int jj) -> int {
     const int j = jj + lane;
     return lane < 16 && j < nblk ? __ldg(p.bt + (int64_t)b * p.bt_sb + j / p.nb) : 0;
   };
-  int phys = page_of(j0);
   const int ni = min(n - i0, p.qn);
   if (ni <= 0) return;
   const float ninf = -__int_as_float(0x7f800000);
@@ -168,13 +184,9 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Score
   load(x, j0);  // (on its way while the queries are staged)
   // ---- B: the group's rows, split by sign
   const int rows = ni * p.G;
-  for (int x = tid; x < NT * 8 * (D / 8); x += kScoreThreads) {
-    const int r = x / (D / 8), c = x - r * (D / 8), i = r / p.G;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (r < rows)
-      v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __half *>(p.q) + (int64_t)b * p.q_sb +
-                                                (int64_t)(i0 + i) * p.q_si +
-                                                (int64_t)(h * p.G + r - i * p.G) * p.q_sh + 8 * c));
+  auto stage = [&](int x, uint4 v) {
+    const int r = x / (D / 8), c = x - r * (D / 8);
+    if (r >= rows) v = make_uint4(0u, 0u, 0u, 0u);
     uint4 lo, hi;
     const __half2 z = __float2half2_rn(0.f);
     const uint32_t in[4] = {v.x, v.y, v.z, v.w};
@@ -190,7 +202,11 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Score
     lo = make_uint4(nl[0], nl[1], nl[2], nl[3]);
     *reinterpret_cast<uint4 *>(qs + r * BS + 8 * c) = hi;
     *reinterpret_cast<uint4 *>(qs + (NT * 8 + r) * BS + 8 * c) = lo;
-  }
+  };
+#pragma unroll
+  for (int e = 0; e < kQ; ++e)
+    if (tid + e * kScoreThreads < kChunks) stage(tid + e * kScoreThreads, qv[e]);
+  for (int x = tid + kQ * kScoreThreads; x < kChunks; x += kScoreThreads) stage(x, query(x));
   __syncthreads();
   for (;;) {
     use(x, j0);
