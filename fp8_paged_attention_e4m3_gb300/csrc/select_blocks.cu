@@ -20,8 +20,8 @@
 //
 // The steps of the search bound it, not the bytes (4 per score): histogram,
 // scan over the bins, next digit, each behind a barrier.  16 rows of 4096
-// blocks take 5.9 us, 256 rows of up to 16384 blocks 18.7 us (22.9 with the
-// longer rows' writer).
+// blocks take 5.7 us, 256 rows of up to 16384 blocks 16.0 us (of which reading
+// the row is a third).
 #include "common.cuh"
 #include "kernels.h"
 #include "verify_attn_e4m3.h"
@@ -67,13 +67,16 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_blocks_kernel(const Se
   const int x0 = min(warp * seg, v), x1 = min(x0 + seg, v);
   // key of a candidate; all ones for a forced place, 0 past the row's end (no
   // score maps to either)
-  auto read_key = [&](int x) -> uint32_t {
-    return x >= x1 ? 0u : x >= c0 && x < c1 ? score_key(__ldg(sc + x)) : 0xFFFFFFFFu;
+  auto key_of = [&](int x, float score) -> uint32_t {
+    return x >= x1 ? 0u : x >= c0 && x < c1 ? score_key(score) : 0xFFFFFFFFu;
   };
   uint32_t key[kKeys > 0 ? kKeys : 1];
   if constexpr (kKeys > 0) {
 #pragma unroll
-    for (int e = 0; e < kKeys; ++e) key[e] = read_key(x0 + 32 * e + lane);
+    for (int e = 0; e < kKeys; ++e)  // all under way together
+      key[e] = __float_as_uint(__ldg(sc + min(x0 + 32 * e + lane, v - 1)));
+#pragma unroll
+    for (int e = 0; e < kKeys; ++e) key[e] = key_of(x0 + 32 * e + lane, __uint_as_float(key[e]));
   }
   auto each_key = [&](auto &&f) {
     if constexpr (kKeys > 0) {
@@ -84,7 +87,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_blocks_kernel(const Se
         for (int k = 0; k < 4; ++k) f(x0 + 32 * (e + k) + lane, key[e + k]);
       }
     } else {
-      for (int x = x0; x < x1; x += 32) f(x + lane, read_key(x + lane));
+      for (int x = x0; x < x1; x += 32) f(x + lane, key_of(x + lane, __ldg(sc + min(x + lane, v - 1))));
     }
   };
   uint32_t m = (uint32_t)(p.k - p.sink - p.local);  // how many of them (fewer than there are)
