@@ -176,6 +176,9 @@ int verify_attn_e4m3_append(const vae4_tensor *k_new, const vae4_tensor *v_new,
   p.page = (int32_t)src.page;
   p.blk = (int32_t)blk;
   p.touched = (int32_t)((Q + blk - 2) / blk + 1);
+  p.nb = (int32_t)nb;
+  p.page_m = reciprocal16(p.page);
+  p.blk_m = reciprocal16(p.blk);
   if (launch_append(p, k_new->dtype == VAE4_BF16, (flags & VAE4_FLAG_KV_E5M2) != 0, cu(stream)) !=
       cudaSuccess)
     return VAE4_ERR_CUDA;

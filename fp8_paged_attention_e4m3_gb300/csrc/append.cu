@@ -20,10 +20,11 @@
 // memory once each (a row's 16 bits in, 8 out): a thread asks for its rows before
 // it knows the page and keeps them in registers between the maximum and the
 // rounding, and tracks the bounds as 16-bit values, since rounding to a code is
-// monotonic.  2 x 16384 new tokens, 8 heads of 128: 202 MB in 48 us, 4.2 TB/s;
-// the instructions per row (rounding 8 values of a thread takes most) and the
-// chain of a CTA (lengths, page, rows, maximum, store) bound it, not the bytes.
-// A step of few rows is the launch and that chain: 2.8 to 3.5 us.
+// monotonic.  2 x 16384 new tokens, 8 heads of 128: 202 MB in 43.6 us, 4.6 TB/s.
+// The instructions bound it, not the bytes: 72 percent of the issue slots, before
+// products with the inverse scale stayed in 16 bits and divisions by the page and
+// the block became products (48 us).  A step of few rows is the launch and the
+// chain lengths -> rows -> maximum -> store: 2.3 to 3.5 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -38,7 +39,7 @@ namespace vae4 {
 namespace {
 
 constexpr int kAppendThreads = 256;
-constexpr int kCtas = 4;  // per SM; 5 leave 48 registers and spill, for the same time
+constexpr int kCtas = 4;  // per SM; 5 gain a percent for prompts and cost ten for few rows
 constexpr int kHold = 4;  // rows a thread keeps: a block of 64 tokens at D = 128 is read once
 
 template <bool BF16>
@@ -67,12 +68,17 @@ __device__ __forceinline__ uint32_t fp8x2(float a, float b) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(d) : "f"(b), "f"(a));
   return d;
 }
+// two FP16 values -> two E4M3 codes, to nearest even, saturating
+__device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t h) {
+  unsigned short d;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;\n" : "=h"(d) : "r"(h));
+  return d;
+}
 // f16x2 that holds two FP8 values -> their codes (exact)
 template <bool E5M2>
 __device__ __forceinline__ uint32_t fp8x2_of_f16x2(uint32_t h) {
   if constexpr (E5M2) return __byte_perm(h, 0u, 0x4431) & 0xFFFFu;
-  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-  return fp8x2<false>(f.x, f.y);
+  return e4m3x2_of_f16x2(h);
 }
 
 // 8 codes -> their values
@@ -84,21 +90,14 @@ __device__ __forceinline__ void values8(uint2 codes, __half2 (&v)[4]) {
   for (int e = 0; e < 4; ++e) v[e] = *reinterpret_cast<const __half2 *>(&h[e]);
 }
 
-// maximum and minimum of two pairs of 16-bit values (NAN: a NaN stays)
-template <bool BF16, bool NAN_STAYS>
+// maximum and minimum of two pairs of 16-bit values (not a NaN if one is a number)
+template <bool BF16>
 __device__ __forceinline__ uint32_t max16(uint32_t a, uint32_t b) {
   uint32_t d;
-  if constexpr (BF16) {
-    if constexpr (NAN_STAYS)
-      asm("max.NaN.bf16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
-    else
-      asm("max.bf16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
-  } else {
-    if constexpr (NAN_STAYS)
-      asm("max.NaN.f16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
-    else
-      asm("max.f16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
-  }
+  if constexpr (BF16)
+    asm("max.bf16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
+  else
+    asm("max.f16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 template <bool BF16>
@@ -108,6 +107,25 @@ __device__ __forceinline__ uint32_t min16(uint32_t a, uint32_t b) {
     asm("min.bf16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
   else
     asm("min.f16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// the larger magnitude of two pairs, of either sign; a NaN stays
+template <bool BF16>
+__device__ __forceinline__ uint32_t maxabs16(uint32_t a, uint32_t b) {
+  uint32_t d;
+  if constexpr (BF16)
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
+  else
+    asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t mul16(uint32_t a, uint32_t b) {
+  uint32_t d;
+  if constexpr (BF16)
+    asm("mul.rn.bf16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
+  else
+    asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 template <bool BF16>
@@ -140,9 +158,9 @@ __global__ void __launch_bounds__(kAppendThreads, kCtas) append_kernel(const App
   if (L == 0 || n == 0) return;
   const int new0 = L - n;                              // first new token
   const bool bounds = w == 0 && p.bounds != nullptr;
-  const int64_t first = (new0 / p.blk + (int64_t)blockIdx.x) * p.blk;  // token of the block
-  if (first >= L) return;
-  const int t0 = (int)first;
+  const int64_t blk0 = div16(new0, p.blk_m) + (int64_t)blockIdx.x;  // the CTA's block
+  if (blk0 * p.blk >= L) return;
+  const int t0 = (int)blk0 * p.blk;
   const int a = max(new0 - t0, 0);                     // rows the block holds already
   const int z = min(p.blk, L - t0);                    // rows it holds afterwards
   // the first kHold rows of a thread are requested before the page is known;
@@ -150,20 +168,22 @@ __global__ void __launch_bounds__(kAppendThreads, kCtas) append_kernel(const App
   const int64_t x_row = p.x_si[w];
   const uint16_t *x = static_cast<const uint16_t *>(p.x[w]) + (int64_t)b * p.x_sb[w] +
                       (int64_t)h * p.x_sh[w] + (int64_t)(t0 - new0) * x_row + 8 * c;
+  const uint16_t *xk = x + (a + g) * x_row;
   auto load = [&](int r) { return __ldcs(reinterpret_cast<const uint4 *>(x + r * x_row)); };
   uint4 held[kHold];
 #pragma unroll
   for (int k = 0; k < kHold; ++k) {
-    const int r = a + g + k * RG;
-    held[k] = r < z ? load(r) : make_uint4(0u, 0u, 0u, 0u);
+    held[k] = a + g + k * RG < z ? __ldcs(reinterpret_cast<const uint4 *>(xk)) : make_uint4(0u, 0u, 0u, 0u);
+    xk += RG * x_row;
   }
-  const int lp = t0 / p.page, slot = t0 - lp * p.page;
+  const int lp = div16(t0, p.page_m), slot = t0 - lp * p.page;
+  const int sub = (int)blk0 - lp * p.nb;  // the block in its page
   const int phys = p.bt[(int64_t)b * p.bt_sb + lp];
   if (phys < 0 || phys >= p.n_pages) {
     if (tid == 0 && p.status) atomicOr(p.status, VAE4_STATUS_BAD_BLOCK);
     return;
   }
-  float *sp = p.scales + (int64_t)phys * p.s_page + w * p.s_kv + (int64_t)h * p.s_head + slot / p.blk;
+  float *sp = p.scales + (int64_t)phys * p.s_page + w * p.s_kv + (int64_t)h * p.s_head + sub;
   float s_old = 0.f;
   if (a > 0) {
     s_old = *sp;
@@ -188,12 +208,12 @@ __global__ void __launch_bounds__(kAppendThreads, kCtas) append_kernel(const App
   auto look = [&](const uint4 &v, bool live) {
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) am2 = max16<BF16, true>(am2, u[e] & 0x7FFF7FFFu);
+    for (int e = 0; e < 4; ++e) am2 = maxabs16<BF16>(am2, u[e]);
     if (bounds && live) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         lo[e] = min16<BF16>(lo[e], u[e]);
-        hi[e] = max16<BF16, false>(hi[e], u[e]);
+        hi[e] = max16<BF16>(hi[e], u[e]);
       }
     }
   };
@@ -208,7 +228,7 @@ __global__ void __launch_bounds__(kAppendThreads, kCtas) append_kernel(const App
     for (int k = 0; k < kAppendThreads / 32; ++k) v = max(v, red[k]);
     return v;
   };
-  uint32_t am = block_max(max(am2 & 0xFFFFu, am2 >> 16));
+  uint32_t am = block_max(max(am2 & 0x7FFFu, am2 >> 16 & 0x7FFFu));
   bool odd = false;  // a NaN, an infinity or a value beyond the largest scale
   if (am >= (BF16 ? 0x7F80u : 0x7C00u)) {  // rare, the same for every thread: the finite values'
     odd = true;
@@ -224,7 +244,7 @@ __global__ void __launch_bounds__(kAppendThreads, kCtas) append_kernel(const App
         if (bounds) {  // a NaN is stored as zero
           const uint32_t f = nan_to_zero<BF16>(u[e]);
           lo[e] = min16<BF16>(lo[e], f);
-          hi[e] = max16<BF16, false>(hi[e], f);
+          hi[e] = max16<BF16>(hi[e], f);
         }
       }
     }
@@ -240,16 +260,67 @@ __global__ void __launch_bounds__(kAppendThreads, kCtas) append_kernel(const App
   odd |= e_need > 30;
   const float need = __uint_as_float((uint32_t)(min(max(e_need, -30), 30) + 127) << 23);
   const float s = a > 0 ? fmaxf(s_old, need) : need;
+  // s a power of two: x / s is a product with its inverse, in FP32 exact, in
+  // BF16 too, and in FP16 (if it holds the inverse) but for quotients below
+  // 2^-14, which round to an E4M3 zero like their exact values
   const bool pow2 = (__float_as_uint(s) & 0x7FFFFFu) == 0u;
-  const float inv = 1.f / s;  // exact for a power of two
+  const bool direct = pow2 && (BF16 || E5M2 || (s >= 0x1p-15f && s <= 0x1p14f));
+  // (s lies within 2^-40 .. 2^40: the inverse of a power of two by its exponent)
+  const float inv = pow2 ? __uint_as_float(0x7F000000u - __float_as_uint(s)) : 0.f;
+  const uint32_t inv16 = BF16 ? (__float_as_uint(inv) >> 16) * 0x10001u
+                              : __half_as_ushort(__float2half_rn(inv)) * 0x10001u;
   if (odd && tid == 0 && p.status) atomicOr(p.status, VAE4_STATUS_BAD_VALUE);
   auto encode = [&](uint4 v, auto exact) -> uint2 {
-    float f[8];
-    unpack8<BF16>(v, f);
+    constexpr bool EX = decltype(exact)::value;
+    if constexpr (EX && (BF16 || !E5M2)) {
+      uint32_t u[4] = {v.x, v.y, v.z, v.w}, d[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = decltype(exact)::value ? f[e] * inv : __fdiv_rn(f[e], s);
-    return make_uint2(fp8x2<E5M2>(f[0], f[1]) | fp8x2<E5M2>(f[2], f[3]) << 16,
-                      fp8x2<E5M2>(f[4], f[5]) | fp8x2<E5M2>(f[6], f[7]) << 16);
+      for (int e = 0; e < 4; ++e) {
+        u[e] = mul16<BF16>(u[e], inv16);
+        if constexpr (BF16)
+          d[e] = fp8x2<E5M2>(__uint_as_float(u[e] << 16), __uint_as_float(u[e] & 0xFFFF0000u));
+        else
+          d[e] = e4m3x2_of_f16x2(u[e]);
+      }
+      return make_uint2(d[0] | d[1] << 16, d[2] | d[3] << 16);
+    } else {
+      float f[8];
+      unpack8<BF16>(v, f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = EX ? f[e] * inv : __fdiv_rn(f[e], s);
+      return make_uint2(fp8x2<E5M2>(f[0], f[1]) | fp8x2<E5M2>(f[2], f[3]) << 16,
+                        fp8x2<E5M2>(f[4], f[5]) | fp8x2<E5M2>(f[6], f[7]) << 16);
+    }
+  };
+  // minimum and maximum over the threads of a channel chunk, first those of a
+  // warp; valid in the first 2 CH threads: thread (mm, c) has chunk c's
+  auto over_rows = [&](uint4 l4, uint4 h4, auto mn, auto mx) -> uint4 {
+    uint32_t l[4] = {l4.x, l4.y, l4.z, l4.w}, u[4] = {h4.x, h4.y, h4.z, h4.w};
+#pragma unroll
+    for (int o = 16; o >= CH; o >>= 1) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        l[e] = mn(l[e], __shfl_xor_sync(0xffffffffu, l[e], o));
+        u[e] = mx(u[e], __shfl_xor_sync(0xffffffffu, u[e], o));
+      }
+    }
+    constexpr int WG = CH < 32 ? kAppendThreads / 32 : RG;  // what is left, CH chunks each
+    if (CH >= 32 || (tid & 31) < CH) {
+      const int x = CH < 32 ? (tid >> 5) * CH + c : tid;
+      lohi[0][x] = make_uint4(l[0], l[1], l[2], l[3]);
+      lohi[1][x] = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+    __syncthreads();
+    if (tid >= 2 * CH) return make_uint4(0u, 0u, 0u, 0u);
+    const int mm = tid / CH, cc = tid % CH;
+    uint4 t = lohi[mm][cc];
+#pragma unroll
+    for (int k = 1; k < WG; ++k) {
+      const uint4 q = lohi[mm][cc + k * CH];
+      t = mm ? make_uint4(mx(t.x, q.x), mx(t.y, q.y), mx(t.z, q.z), mx(t.w, q.w))
+             : make_uint4(mn(t.x, q.x), mn(t.y, q.y), mn(t.z, q.z), mn(t.w, q.w));
+    }
+    return t;
   };
   // ---- new rows
   const int64_t row = p.c_ts[w];
@@ -271,34 +342,23 @@ __global__ void __launch_bounds__(kAppendThreads, kCtas) append_kernel(const App
                      nan_to_zero<BF16>(v.w));
       *reinterpret_cast<uint2 *>(d) = encode(v, std::false_type{});
     }
-  } else if (pow2) {
+  } else if (direct) {
     store(std::true_type{});
   } else {
     store(std::false_type{});
   }
-  // the bounds of the new rows, as the values of their codes
-  __half2 lo2[4], hi2[4];
-  if (bounds) {
-    if (a + g < z) {
-      const uint4 vl = make_uint4(lo[0], lo[1], lo[2], lo[3]), vh = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      const uint2 cl = pow2 ? encode(vl, std::true_type{}) : encode(vl, std::false_type{});
-      const uint2 ch = pow2 ? encode(vh, std::true_type{}) : encode(vh, std::false_type{});
-      values8<E5M2>(cl, lo2);
-      values8<E5M2>(ch, hi2);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        lo2[e] = __halves2half2(__ushort_as_half(0x7C00), __ushort_as_half(0x7C00));
-        hi2[e] = __halves2half2(__ushort_as_half(0xFC00), __ushort_as_half(0xFC00));
-      }
-    }
-  }
   // ---- rows the block holds already: under a larger scale, and in the bounds
   const bool grow = a > 0 && s > s_old;
-  if (grow || bounds) {
+  alignas(16) __half2 lo2[4], hi2[4];  // bounds of their codes' values
+  if (grow || (bounds && a > 0)) {
     const float f = s_old / s;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      lo2[e] = __halves2half2(__ushort_as_half(0x7C00), __ushort_as_half(0x7C00));
+      hi2[e] = __halves2half2(__ushort_as_half(0xFC00), __ushort_as_half(0xFC00));
+    }
     for (int r = g; r < a; r += RG) {
-      uint2 codes = *reinterpret_cast<const uint2 *>(dst + r * p.c_ts[w]);
+      uint2 codes = *reinterpret_cast<const uint2 *>(dst + r * row);
       if (grow) {
         const uint32_t in[4] = {codes.x, codes.x >> 16, codes.y, codes.y >> 16};
         uint32_t o[4];
@@ -309,7 +369,7 @@ __global__ void __launch_bounds__(kAppendThreads, kCtas) append_kernel(const App
           o[e] = fp8x2<E5M2>(v.x * f, v.y * f);
         }
         codes = make_uint2(o[0] | o[1] << 16, o[2] | o[3] << 16);
-        *reinterpret_cast<uint2 *>(dst + r * p.c_ts[w]) = codes;
+        *reinterpret_cast<uint2 *>(dst + r * row) = codes;
       }
       if (bounds) {
         __half2 v[4];
@@ -323,39 +383,35 @@ __global__ void __launch_bounds__(kAppendThreads, kCtas) append_kernel(const App
     }
   }
   if (tid == 0) *sp = s;
-  // ---- bounds: over the row groups, first those of a warp
+  // ---- bounds, over the row groups: of the new values, rounded at the end
+  // (rounding is monotonic), or, with earlier rows, of the codes' values
   if (bounds) {
+    auto rounded = [&](uint4 v) {
+      return direct ? encode(v, std::true_type{}) : encode(v, std::false_type{});
+    };
+    const uint4 ln = make_uint4(lo[0], lo[1], lo[2], lo[3]), hn = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    uint2 d;
+    if (a == 0) {
+      d = rounded(over_rows(ln, hn, [](uint32_t x, uint32_t y) { return min16<BF16>(x, y); },
+                            [](uint32_t x, uint32_t y) { return max16<BF16>(x, y); }));
+    } else {  // (a thread without new rows: the infinities round to the largest codes)
+      __half2 v[4];
+      values8<E5M2>(rounded(ln), v);
 #pragma unroll
-    for (int o = 16; o >= CH; o >>= 1) {
+      for (int e = 0; e < 4; ++e) lo2[e] = __hmin2(lo2[e], v[e]);
+      values8<E5M2>(rounded(hn), v);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        lo2[e] = __hmin2(lo2[e], __shfl_xor_sync(0xffffffffu, lo2[e], o));
-        hi2[e] = __hmax2(hi2[e], __shfl_xor_sync(0xffffffffu, hi2[e], o));
-      }
+      for (int e = 0; e < 4; ++e) hi2[e] = __hmax2(hi2[e], v[e]);
+      const uint4 m = over_rows(*reinterpret_cast<const uint4 *>(lo2), *reinterpret_cast<const uint4 *>(hi2),
+                                [](uint32_t x, uint32_t y) { return min16<false>(x, y); },
+                                [](uint32_t x, uint32_t y) { return max16<false>(x, y); });
+      d = make_uint2(fp8x2_of_f16x2<E5M2>(m.x) | fp8x2_of_f16x2<E5M2>(m.y) << 16,
+                     fp8x2_of_f16x2<E5M2>(m.z) | fp8x2_of_f16x2<E5M2>(m.w) << 16);
     }
-    constexpr int WG = CH < 32 ? kAppendThreads / 32 : RG;  // what is left, CH chunks each
-    if (CH >= 32 || (tid & 31) < CH) {
-      const int x = CH < 32 ? (tid >> 5) * CH + c : tid;
-      lohi[0][x] = *reinterpret_cast<const uint4 *>(lo2);
-      lohi[1][x] = *reinterpret_cast<const uint4 *>(hi2);
-    }
-    __syncthreads();
     if (tid < 2 * CH) {
       const int mm = tid / CH, cc = tid % CH;
-      const __half2 *v = reinterpret_cast<const __half2 *>(&lohi[mm][cc]);
-      __half2 t[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-      for (int k = 1; k < WG; ++k) {
-        const uint4 q = lohi[mm][cc + k * CH];
-        const __half2 *u = reinterpret_cast<const __half2 *>(&q);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) t[e] = mm ? __hmax2(t[e], u[e]) : __hmin2(t[e], u[e]);
-      }
-      const uint32_t *u = reinterpret_cast<const uint32_t *>(t);
       *reinterpret_cast<uint2 *>(p.bounds + (int64_t)phys * p.b_page + (int64_t)h * p.b_head +
-                                 (int64_t)(slot / p.blk) * p.b_blk + mm * p.b_mm + 8 * cc) =
-          make_uint2(fp8x2_of_f16x2<E5M2>(u[0]) | fp8x2_of_f16x2<E5M2>(u[1]) << 16,
-                     fp8x2_of_f16x2<E5M2>(u[2]) | fp8x2_of_f16x2<E5M2>(u[3]) << 16);
+                                 (int64_t)sub * p.b_blk + mm * p.b_mm + 8 * cc) = d;
     }
   }
 }

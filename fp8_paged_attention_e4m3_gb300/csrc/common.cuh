@@ -153,4 +153,11 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return *reinterpret_cast<uint32_t *>(&h);
 }
 
+// key / n for n a multiple of 16 up to 65536 and key < 2^30, m = ceil(2^38 /
+// (n / 16)): with x = key / 16 < 2^26, x m < 2^64, and the excess of x m / 2^38
+// over x / (n / 16) is below x / 2^38 < 2^-12 <= 1 / (n / 16).
+__device__ __forceinline__ int div16(int key, unsigned long long m) {
+  return (int)((unsigned long long)(unsigned)(key >> 4) * m >> 38);
+}
+
 }  // namespace vae4

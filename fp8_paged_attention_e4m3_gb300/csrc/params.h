@@ -27,6 +27,12 @@ struct alignas(16) BlockEntry {
   int32_t pad;
 };
 
+// n a multiple of 16 up to 65536 -> the multiplier of div16
+inline unsigned long long reciprocal16(int n) {
+  const unsigned long long d = (unsigned long long)n / 16;
+  return ((1ull << 38) + d - 1) / d;
+}
+
 // The stream record of one (sequence, KV head) under sparse attention.
 struct alignas(16) BlockStream {
   int32_t n16;  // tokens of the listed blocks, rounded up to 16 (0: nothing to visit)
@@ -119,6 +125,8 @@ struct AppendParams {
   uint32_t *status;              // may be null
   int32_t B, Qmax, Hkv, D, page, blk;
   int32_t touched;               // most blocks a sequence's new tokens can touch
+  int32_t nb;                    // blocks per page
+  unsigned long long page_m, blk_m;  // reciprocals of page and blk (div16)
 };
 
 // The block scores' parameters.

@@ -68,13 +68,9 @@ cudaError_t launch_seg(const SegParams &p_in, cudaStream_t stream) {
   // start at multiples of 64 keys, so it never crosses one
   const int unit = p.list ? p.blk : p.page;
   p.box_log2 = unit % 64 == 0 ? 6 : unit % 32 == 0 ? 5 : 4;
-  auto reciprocal = [](int n) -> unsigned long long {
-    const unsigned long long d = (unsigned long long)n / 16;
-    return ((1ull << 38) + d - 1) / d;
-  };
   p.page_blocks = p.page / p.blk;
-  p.page_m = reciprocal(p.page);
-  p.blk_m = reciprocal(p.blk);
+  p.page_m = reciprocal16(p.page);
+  p.blk_m = reciprocal16(p.blk);
   CUtensorMap map_k, map_v;
   memset(&map_k, 0, sizeof(map_k));
   memset(&map_v, 0, sizeof(map_v));

@@ -148,13 +148,6 @@ enum : int { kWSoftmax = 0, kWKDec = 8, kWVDec = 12, kWKProd = 16, kWVProd = 17,
 
 __device__ __forceinline__ uint32_t sw128(uint32_t off) { return off ^ (((off >> 7) & 7u) << 4); }
 
-// key / n for n a multiple of 16 up to 65536 and key < 2^30, m = ceil(2^38 /
-// (n / 16)): with x = key / 16 < 2^26, x m < 2^64, and the excess of x m / 2^38
-// over x / (n / 16) is below x / 2^38 < 2^-12 <= 1 / (n / 16).
-__device__ __forceinline__ int div16(int key, unsigned long long m) {
-  return (int)((unsigned long long)(unsigned)(key >> 4) * m >> 38);
-}
-
 // maximum over the warp (a NaN does not count)
 __device__ __forceinline__ float warp_max(float x) {
   float d;
