@@ -8,7 +8,9 @@
 //
 // A unit's parts lie in slots first, ctas + first + 1, ctas + first + 2, ...
 // Few streams (many parts each): one CTA per (row, 64 channels), 16 groups of
-// 16 lanes over the parts.  Many streams: one warp per (row, 32 channels).
+// 16 lanes over the parts.  Many streams: one warp per (row, 32 channels).  The
+// latency of table -> parts -> sums bounds both: 152 parts of 48 rows of 256
+// (7.5 MB, in L2) take 4 us after the split kernel.
 #include <algorithm>
 
 #include "common.cuh"
