@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
       };
       int2 it0 = make_int2(0, 0), it1 = step(it0);
       int page1 = -1;
-      if (!isv) {
+      if (isv) {
         load_scales(it0, load_page(it0));
         page1 = load_page(it1);
       }
@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
             }
             // a group's scales follow its first copy (their loads may still be
             // on the way, and the softmax needs them later than the keys)
-            if (!isv && (t & 7) == 0 && !(ok = pass_scales())) break;
+            if (isv && (t & 7) == 0 && !(ok = pass_scales())) break;
             ++count;
             if (++st == nslot) {
               st = 0;
