@@ -8,9 +8,9 @@ library cannot be built or loaded, every call raises.
 """
 from __future__ import annotations
 
-import array
 import ctypes
 import os
+import struct
 import threading
 
 ABI_VERSION = 3
@@ -428,30 +428,33 @@ def alloc_k_bounds(n_pages, Hkv, page, block_tokens, D, device=None):
 _torch = None
 _CODES = {}      # torch dtype -> vae4_dtype
 _raw_stream = None
-_PAD = [(0,) * (5 - n) for n in range(6)]
+_device = None
+# a vae4_tensor of n dimensions: data, dtype | ndim << 32, shape[5], stride[5]
+_PACK = [struct.Struct(f"=2q{n}q{40 - 8 * n}x{n}q{40 - 8 * n}x").pack for n in range(6)]
 
 
 def _setup():
-    global _torch, _raw_stream
+    global _torch, _raw_stream, _device
     import torch
     _CODES.update({torch.uint8: VAE4_U8, torch.int32: VAE4_I32, torch.float16: VAE4_F16,
                    torch.float32: VAE4_F32, torch.bfloat16: VAE4_BF16,
                    torch.float8_e4m3fn: VAE4_U8, torch.float8_e5m2: VAE4_U8})
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _torch = torch
 
 
 def _call(name, tensors, rest, stream, opt=None):
     """lib.verify_attn_e4m3_<name>(tensors..., rest..., stream[, opt]), the
-    tensors (None: a null pointer) as vae4_tensor structures of 12 64-bit
-    words each in one array.  Every tensor has to be on the current device."""
+    tensors (None: a null pointer) as packed vae4_tensor structures.  Every
+    tensor has to be on the current device."""
     if _torch is None:
         _setup()
-    words, ptrs, dev = [], [], -1
+    args, dev = [], -1
     for t in tensors:
         if t is None:
-            ptrs.append(-1)
+            args.append(None)
             continue
         d = t.get_device()
         if d < 0 or (d != dev and dev >= 0):
@@ -464,14 +467,10 @@ def _call(name, tensors, rest, stream, opt=None):
         n = len(shape)
         if n > 5:
             raise ValueError("at most 5 dimensions")
-        ptrs.append(8 * len(words))
-        words += (t.data_ptr(), code | n << 32, *shape, *_PAD[n], *t.stride(), *_PAD[n])
-    if dev != _torch.cuda.current_device():
+        args.append(_PACK[n](t.data_ptr(), code | n << 32, *shape, *t.stride()))
+    if dev != _device():
         raise ValueError("tensors have to be on the current device")
-    buf = array.array("q", words)
-    base = buf.buffer_info()[0]
     st = _raw_stream(dev) if stream is None else _stream_handle(stream)
-    args = [base + p if p >= 0 else None for p in ptrs]
     fn = getattr(_lib or load(), name)
     rc = fn(*args, *rest, st) if opt is None else fn(*args, *rest, st, ctypes.byref(opt))
     if rc != 0:

@@ -16,10 +16,10 @@
 // CTAs + c + 1, CTAs + c + 2, ...
 //
 // What bounds it.  The keys' bytes, read once: 32 sequences of up to 32749
-// tokens, 8 heads of 128 (1.42 GB), take 263 us with the combine, 0.80 of the
+// tokens, 8 heads of 128 (1.42 GB), take 265 us with the combine, 0.79 of the
 // copy peak, the softmax and the decoders beside the copies using 54 % of the
 // issue slots.  One sequence of 262144 tokens, 48 rows of 256 (134 MB), takes
-// 36.5 us (0.54): 4 us to the first copy (lengths, plan, page), 3 to the first
+// 36.1 us (0.55): 4 us to the first copy (lengths, plan, page), 3 to the first
 // scores, 20 at the memory's rate, up to 4 for the SMs whose rows are raised
 // most often, 4 for the combine.
 //
@@ -40,9 +40,9 @@
 //                     half-tiles.  (Boxes of 16 keys of 128 bytes held the
 //                     copies to 0.71 of the copy peak with all other work
 //                     taken out, boxes of 64 to 0.88.)  The K producer also
-//                     plans the segments and passes on the scales (positions,
-//                     masks) of 512 keys at a time, one 16-key box per lane,
-//                     requested 512 keys ahead.
+//                     plans the segments, the V producer passes on the scales
+//                     (positions, masks) of 512 keys at a time, one 16-key box
+//                     per lane, requested 512 keys ahead.
 //   K decoders (4)  : thread = key; exact FP8 -> FP16 into tensor memory, the
 //                     A operand of S^T = K . Q^T.
 //   V decoders (4)  : transposing 8-bit ldmatrix, the same conversion, into
@@ -115,7 +115,7 @@ struct Cfg {
   static constexpr int PB = 128 * 128;          // P^T, MN-major SW128 (N <= 64)
   static constexpr int RSLOT = 64 * D;          // one raw K or V half-tile
   static constexpr int LIMIT = 232448 - 1024;   // opt-in maximum minus alignment slack
-  // groups of 512 keys whose scales are held: the K producer runs up to eight
+  // groups of 512 keys whose scales are held: the V producer runs some
   // tiles ahead of the softmax and must not wait for it here
   static constexpr int NSG = 4;
   // small region: barriers, scalars, row state, scale boxes, segments
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
   const long long LIM = p.wait_limit;
   const int lb = p.box_log2;  // keys per tensor copy
   // counters of the role that run through all segments: half-tiles or tiles,
-  // and segments (score MMA) or groups of scales (softmax, K producer)
+  // and segments (score MMA) or groups of scales (softmax, V producer)
   int count = 0, count2 = 0;
   bool mma_issued = false;
   bool first = true;
@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
       };
       int2 itc = make_int2(0, 0);
       request(itc);
-      // ---- scales, by the K producer, four tiles at a time: lane = one 16-key
+      // ---- scales, by the V producer, four tiles at a time: lane = one 16-key
       // box of a group of 512 keys (a box lies in one block).  A group is
       // requested a group ahead of its use, the page ids that lead to it two.
       float4 *box_s = reinterpret_cast<float4 *>(gSm + C::S_BOX);
