@@ -20,14 +20,18 @@
 // memory once each (a row's 16 bits in, 8 out): a thread asks for its rows before
 // it knows the page and keeps them in registers between the maximum and the
 // rounding, and tracks the bounds as 16-bit values, since rounding to a code is
-// monotonic.  2 x 16384 new tokens, 8 heads of 128: 202 MB in 43.6 us, 4.6 TB/s.
-// The instructions bound it, not the bytes: 72 percent of the issue slots, before
-// products with the inverse scale stayed in 16 bits and divisions by the page and
-// the block became products (48 us).  A step of few rows is the launch and the
-// chain lengths -> rows -> maximum -> store: 2.3 to 3.5 us.
+// monotonic.  2 x 16384 new tokens, 8 heads of 128: 202 MB in 34.4 us, 5.9 TB/s,
+// 0.87 of the copy peak.  What had kept it from that were instructions, not bytes:
+// 256 threads of four rows each took 43.6 us with 69 percent of the issue slots in
+// use, since what a warp does once per block (lengths, page, scale, bounds) then
+// costs as much as its rows; and 48 us before products with the inverse scale
+// stayed in 16 bits and divisions by the page and the block became products.  A
+// step of few rows is the launch and the chain lengths -> rows -> maximum ->
+// store: 2.3 to 3.5 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "common.cuh"
@@ -38,9 +42,7 @@ namespace vae4 {
 
 namespace {
 
-constexpr int kAppendThreads = 256;
-constexpr int kCtas = 4;  // per SM; 5 gain a percent for prompts and cost ten for few rows
-constexpr int kHold = 4;  // rows a thread keeps: a block of 64 tokens at D = 128 is read once
+constexpr int kAppendThreads = 128;
 
 template <bool BF16>
 __device__ __forceinline__ void unpack8(const uint4 &w, float (&f)[8]) {
@@ -138,8 +140,9 @@ __device__ __forceinline__ uint32_t nan_to_zero(uint32_t v) {
 
 __device__ __forceinline__ bool scale_ok(float s) { return s >= kMinScale && s <= kMaxScale; }
 
-template <int D, bool BF16, bool E5M2>
-__global__ void __launch_bounds__(kAppendThreads, kCtas) append_kernel(const AppendParams p) {
+// kHold: rows a thread keeps
+template <int D, bool BF16, bool E5M2, int kHold>
+__global__ void __launch_bounds__(kAppendThreads, kHold > 4 ? 7 : 8) append_kernel(const AppendParams p) {
   constexpr int CH = D / 8;                    // 8-element chunks per row
   constexpr int RG = kAppendThreads / CH;      // rows per pass
   constexpr int LEAD = E5M2 ? 15 : 8;          // FPMAX = 1.75 * 2^LEAD
@@ -416,16 +419,26 @@ __global__ void __launch_bounds__(kAppendThreads, kCtas) append_kernel(const App
   }
 }
 
-template <int D>
-cudaError_t launch_d(const AppendParams &p, bool bf16, bool e5m2, dim3 grid, cudaStream_t st) {
+template <int D, int kHold>
+cudaError_t launch_h(const AppendParams &p, bool bf16, bool e5m2, dim3 grid, cudaStream_t st) {
   if (bf16) {
-    if (e5m2) append_kernel<D, true, true><<<grid, kAppendThreads, 0, st>>>(p);
-    else append_kernel<D, true, false><<<grid, kAppendThreads, 0, st>>>(p);
+    if (e5m2) append_kernel<D, true, true, kHold><<<grid, kAppendThreads, 0, st>>>(p);
+    else append_kernel<D, true, false, kHold><<<grid, kAppendThreads, 0, st>>>(p);
   } else {
-    if (e5m2) append_kernel<D, false, true><<<grid, kAppendThreads, 0, st>>>(p);
-    else append_kernel<D, false, false><<<grid, kAppendThreads, 0, st>>>(p);
+    if (e5m2) append_kernel<D, false, true, kHold><<<grid, kAppendThreads, 0, st>>>(p);
+    else append_kernel<D, false, false, kHold><<<grid, kAppendThreads, 0, st>>>(p);
   }
   return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_d(const AppendParams &p, bool bf16, bool e5m2, dim3 grid, cudaStream_t st) {
+  // Four rows per thread where they hold a block's new rows, else eight (a block
+  // of 64 tokens at D = 128 is then read once): 34.4 us for the prompts above,
+  // 46 with four; eight cost a step of few rows 0.2 us (2.3 and 3.4)
+  constexpr int rows = kAppendThreads / (D / 8);  // per pass
+  return std::min(p.blk, p.Qmax) <= 4 * rows ? launch_h<D, 4>(p, bf16, e5m2, grid, st)
+                                             : launch_h<D, 8>(p, bf16, e5m2, grid, st);
 }
 
 }  // namespace
