@@ -150,6 +150,7 @@ __global__ void __launch_bounds__(kAppendThreads, kHold > 4 ? 7 : 8) append_kern
   __shared__ uint4 lohi[2][kAppendThreads];
   const int tid = threadIdx.x, c = tid % CH, g = tid / CH;
   const int b = blockIdx.z, h = blockIdx.y >> 1, w = blockIdx.y & 1;
+  await_previous();
   const int L = p.seq[(int64_t)b * p.seq_sb];
   const int n = p.seq_has_qlen ? p.seq[(int64_t)b * p.seq_sb + 1] : p.Qmax;
   const bool bad_l = L < 0 || (int64_t)L > (int64_t)p.max_pages * p.page;
@@ -421,14 +422,9 @@ __global__ void __launch_bounds__(kAppendThreads, kHold > 4 ? 7 : 8) append_kern
 
 template <int D, int kHold>
 cudaError_t launch_h(const AppendParams &p, bool bf16, bool e5m2, dim3 grid, cudaStream_t st) {
-  if (bf16) {
-    if (e5m2) append_kernel<D, true, true, kHold><<<grid, kAppendThreads, 0, st>>>(p);
-    else append_kernel<D, true, false, kHold><<<grid, kAppendThreads, 0, st>>>(p);
-  } else {
-    if (e5m2) append_kernel<D, false, true, kHold><<<grid, kAppendThreads, 0, st>>>(p);
-    else append_kernel<D, false, false, kHold><<<grid, kAppendThreads, 0, st>>>(p);
-  }
-  return cudaGetLastError();
+  auto *kernel = bf16 ? (e5m2 ? append_kernel<D, true, true, kHold> : append_kernel<D, true, false, kHold>)
+                      : (e5m2 ? append_kernel<D, false, true, kHold> : append_kernel<D, false, false, kHold>);
+  return launch_dependent(kernel, grid, kAppendThreads, 0, st, p);
 }
 
 template <int D>

@@ -30,8 +30,7 @@ __global__ void __launch_bounds__(kListThreads) block_list_kernel(const ListPara
   const int h = blockIdx.x, b = blockIdx.y, stream = b * p.Hkv + h;
   // the split kernel may be placed already (it waits for this grid), and this
   // grid for the previous call's kernels, which read the lists
-  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  await_previous();
   const int L = p.seq[(int64_t)b * p.seq_sb];
   const int n = p.seq_has_qlen ? p.seq[(int64_t)b * p.seq_sb + 1] : p.Qmax;
   const bool bad_l = L < 0 || L > p.capacity;
@@ -135,17 +134,8 @@ cudaError_t launch_block_list(const ListParams &p, cudaStream_t stream) {
         cudaFuncSetAttribute(block_list_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.Hkv, (unsigned)p.B);
-  cfg.blockDim = dim3(kListThreads);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, block_list_kernel, p);
+  return launch_dependent(block_list_kernel, dim3((unsigned)p.Hkv, (unsigned)p.B), kListThreads,
+                          (size_t)smem, stream, p);
 }
 
 }  // namespace vae4

@@ -51,6 +51,7 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Score
   const int g = lane >> 2, t = lane & 3;
   const int h = blockIdx.y / p.parts, b = blockIdx.z;
   const int i0 = (blockIdx.y - h * p.parts) * p.qn;  // first of the CTA's queries
+  await_previous();
   // requested together: the lengths, the thread's first chunks of the queries
   // (padding rows are part of the tensor) and the page of its first block
   constexpr int kChunks = NT * 8 * (D / 8);
@@ -235,8 +236,7 @@ cudaError_t launch_t(const ScoreParams &p, cudaStream_t stream) {
   const int64_t steps = (need + want - 1) / want;
   const dim3 grid((unsigned)std::min<int64_t>((need + steps - 1) / steps, 0x7fffffff),
                   (unsigned)(p.Hkv * p.parts), (unsigned)p.B);
-  block_scores_kernel<D, NT, E5M2><<<grid, kScoreThreads, smem, stream>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(block_scores_kernel<D, NT, E5M2>, grid, kScoreThreads, smem, stream, p);
 }
 
 template <int D, bool E5M2>

@@ -160,4 +160,28 @@ __device__ __forceinline__ int div16(int key, unsigned long long m) {
   return (int)((unsigned long long)(unsigned)(key >> 4) * m >> 38);
 }
 
+// Programmatic dependent launch.  A kernel launched so may be placed while the
+// one before it on the stream still runs: it touches global memory only after
+// await_previous(), which every thread calls and which returns when that kernel
+// has ended; the one after it may then be placed early in the same way.
+__device__ __forceinline__ void await_previous() {
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+}
+template <class P>
+cudaError_t launch_dependent(void (*kernel)(P), dim3 grid, int threads, size_t smem,
+                             cudaStream_t stream, const P &p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 }  // namespace vae4

@@ -237,26 +237,16 @@ __global__ void __launch_bounds__(kWarpThreads) seg_combine_warps(const SegParam
 }  // namespace
 
 cudaError_t launch_seg_combine(const SegParams &p, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   const int R = p.Qmax * p.G;
   if ((int64_t)p.B * p.Hkv < 8) {
-    cfg.gridDim = dim3((unsigned)(R * (p.D / 64)), (unsigned)p.Hkv, (unsigned)p.B);
-    cfg.blockDim = dim3(kRowThreads);
-    cfg.dynamicSmemBytes = (size_t)p.ctas * 2 * sizeof(float);
-    return cudaLaunchKernelEx(&cfg, seg_combine_rows, p);
+    const dim3 grid((unsigned)(R * (p.D / 64)), (unsigned)p.Hkv, (unsigned)p.B);
+    return launch_dependent(seg_combine_rows, grid, kRowThreads, (size_t)p.ctas * 2 * sizeof(float),
+                            stream, p);
   }
   const int64_t warps = (int64_t)p.B * p.Hkv * R * (p.D / 32);
   const int64_t blocks = (warps + kWarpThreads / 32 - 1) / (kWarpThreads / 32);
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3(kWarpThreads);
-  return cudaLaunchKernelEx(&cfg, seg_combine_warps, p);
+  return launch_dependent(seg_combine_warps, dim3((unsigned)blocks), kWarpThreads, 0, stream, p);
 }
 
 }  // namespace vae4

@@ -50,6 +50,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_blocks_kernel(const Se
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int i = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   int32_t *ids = p.ids + (int64_t)b * p.i_sb + (int64_t)i * p.i_si + (int64_t)h * p.i_sh;
+  await_previous();
   const int L = p.seq[(int64_t)b * p.seq_sb];
   const int n = p.seq_has_qlen ? p.seq[(int64_t)b * p.seq_sb + 1] : p.Qmax;
   const bool bad_l = L < 0 || (L > 0 && (L - 1) / p.blk >= p.cols);
@@ -230,14 +231,12 @@ cudaError_t launch_select_blocks(const SelectParams &p, cudaStream_t stream) {
   const dim3 grid((unsigned)p.Qmax, (unsigned)p.Hkv, (unsigned)p.B);
   // a row has at most `cols` blocks: the smallest CTA that holds it in registers
   if (p.cols <= 256 * 8)
-    select_blocks_kernel<256, 8, 4><<<grid, 256, 0, stream>>>(p);
-  else if (p.cols <= 1024 * 8)
-    select_blocks_kernel<1024, 8, 1><<<grid, 1024, 0, stream>>>(p);
-  else if (p.cols <= 512 * 32)
-    select_blocks_kernel<512, 32, 2><<<grid, 512, 0, stream>>>(p);
-  else
-    select_blocks_kernel<1024, 0, 2><<<grid, 1024, 0, stream>>>(p);
-  return cudaGetLastError();
+    return launch_dependent(select_blocks_kernel<256, 8, 4>, grid, 256, 0, stream, p);
+  if (p.cols <= 1024 * 8)
+    return launch_dependent(select_blocks_kernel<1024, 8, 1>, grid, 1024, 0, stream, p);
+  if (p.cols <= 512 * 32)
+    return launch_dependent(select_blocks_kernel<512, 32, 2>, grid, 512, 0, stream, p);
+  return launch_dependent(select_blocks_kernel<1024, 0, 2>, grid, 1024, 0, stream, p);
 }
 
 }  // namespace vae4

@@ -801,6 +801,53 @@ def test_caches_past_32_bit_offsets():
         assert torch.equal(a, b)
 
 
+def test_steps_in_a_row_wait_for_one_another():
+    """Twenty steps enqueued without a pause, each kernel's input the one
+    before's output, give the bits of the steps run one by one."""
+    B, Q, G, H, D, page, blk, k, steps = 3, 4, 4, 2, 128, 64, 16, 6, 20
+    g = torch.Generator(device="cuda").manual_seed(17)
+    new = [torch.randn(steps, B, Q, H, D, generator=g, device="cuda").half() for _ in (0, 1)]
+    q = torch.randn(steps, B, Q, G * H, D, generator=g, device="cuda").half()
+    pages = 12
+    table = torch.randperm(B * pages, generator=g, device="cuda").int().view(B, pages)
+    seqs = [torch.tensor([[Q * (t + 1) + 100 * b, Q] for b in range(B)], dtype=torch.int32, device="cuda")
+            for t in range(steps)]
+    first = torch.tensor([[100 * b, 100 * b] for b in range(B)], dtype=torch.int32, device="cuda")
+    prompt = torch.randn(2, B, 200, H, D, generator=g, device="cuda").half()
+    runs = []
+    for pause in (True, False):
+        kv = torch.zeros(B * pages, 2, H, page, D, dtype=torch.uint8, device="cuda")
+        kc, vc = vae4.cache_views(kv)
+        sc = vae4.alloc_block_scales(B * pages, H, page, blk)
+        bd = vae4.alloc_k_bounds(B * pages, H, page, blk, D)
+        scores = torch.zeros(steps, B, Q, H, pages * page // blk, device="cuda")
+        ids = torch.zeros(steps, B, Q, H, k, dtype=torch.int32, device="cuda")
+        outs = torch.zeros(2, steps, B, Q, G * H, D, dtype=torch.float16, device="cuda")
+        ws = vae4.alloc_workspace(B, G * H, H, Q, D, pages * page)
+        wl = vae4.alloc_sparse_workspace(B, G * H, H, Q, D, pages * page, blk, k)
+        torch.cuda.synchronize()
+        wait = torch.cuda.synchronize if pause else (lambda: None)
+        vae4.verify_attn_e4m3_append(prompt[0], prompt[1], kc, vc, table, first, sc, k_bounds=bd)
+        wait()
+        for t in range(steps):
+            vae4.verify_attn_e4m3_append(new[0][t], new[1][t], kc, vc, table, seqs[t], sc, k_bounds=bd)
+            wait()
+            vae4.verify_attn_e4m3_block_scaled(q[t], kc, vc, table, seqs[t], sc, outs[0, t], ws)
+            wait()
+            vae4.verify_attn_e4m3_block_scores(q[t], bd, table, seqs[t], sc, scores[t], block_tokens=blk)
+            wait()
+            vae4.verify_attn_e4m3_select_blocks(scores[t], seqs[t], ids[t], block_tokens=blk)
+            wait()
+            vae4.verify_attn_e4m3_sparse(q[t], kc, vc, table, seqs[t], sc, ids[t], outs[1, t], wl)
+            wait()
+        torch.cuda.synchronize()
+        assert vae4.read_status(ws) == 0 and vae4.read_status(wl) == 0
+        assert outs[0].any() and outs[1].any() and torch.isfinite(outs).all()
+        runs.append((kv, sc.view(torch.int32), bd, scores.view(torch.int32), ids, outs))
+    for a, b in zip(*runs):
+        assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("graph", [False, True])
 @pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
 def test_decoding_steps_together(graph, fmt):
