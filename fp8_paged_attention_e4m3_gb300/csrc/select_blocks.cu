@@ -20,7 +20,7 @@
 //
 // The steps of the search bound it, not the bytes (4 per score): histogram,
 // scan over the bins, next digit, each behind a barrier.  16 rows of 4096
-// blocks take 5.7 us, 256 rows of up to 16384 blocks 16.0 us (of which reading
+// blocks take 4.7 us, 256 rows of up to 16384 blocks 14.5 us (of which reading
 // the row is a third).
 #include "common.cuh"
 #include "kernels.h"
@@ -35,8 +35,8 @@ constexpr int kBins = 2048;
 // unsigned keys in the order of the scores; -0 and 0 are equal, NaN = -inf
 __device__ __forceinline__ uint32_t score_key(float x) {
   x = x == x ? x + 0.f : -__int_as_float(0x7f800000);
-  const uint32_t u = __float_as_uint(x);
-  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+  const int u = __float_as_int(x);
+  return (uint32_t)(u ^ (u >> 31 | (int)0x80000000));
 }
 
 // kKeys > 0: rows of up to kThreads * kKeys blocks, in registers; 0: any row
@@ -76,8 +76,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_blocks_kernel(const Se
 #pragma unroll
     for (int e = 0; e < kKeys; ++e)  // all under way together
       key[e] = __float_as_uint(__ldg(sc + min(x0 + 32 * e + lane, v - 1)));
+    if (x0 >= c0 && x0 + 32 * kKeys <= min(x1, c1)) {  // candidates alone
 #pragma unroll
-    for (int e = 0; e < kKeys; ++e) key[e] = key_of(x0 + 32 * e + lane, __uint_as_float(key[e]));
+      for (int e = 0; e < kKeys; ++e) key[e] = score_key(__uint_as_float(key[e]));
+    } else {
+#pragma unroll
+      for (int e = 0; e < kKeys; ++e) key[e] = key_of(x0 + 32 * e + lane, __uint_as_float(key[e]));
+    }
   }
   auto each_key = [&](auto &&f) {
     if constexpr (kKeys > 0) {
@@ -156,14 +161,23 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_blocks_kernel(const Se
     static_assert(kWords <= kThreads && 2 * kWords <= kBins, "a thread per word");
     uint32_t *wg = hist, *we = hist + kWords;
     const int nw = (v + 31) / 32;
-    each_key([&](int x, uint32_t u) {
-      const unsigned any = __ballot_sync(0xffffffffu, (u & mask) >= prefix);
-      const unsigned e = __ballot_sync(0xffffffffu, (u & mask) == prefix);
-      if (lane == 0 && x < x1) {
-        wg[x >> 5] = any ^ e;
-        we[x >> 5] = e;
+    // (lane e keeps word e of the segment)
+    uint32_t bits_g = 0u, bits_e = 0u;
+#pragma unroll
+    for (int e = 0; e < kKeys; ++e) {
+      if (e % 4 == 0 && 32 * e >= x1 - x0) break;
+      const uint32_t u = key[e] & mask;
+      const unsigned any = __ballot_sync(0xffffffffu, u >= prefix);
+      const unsigned eq = __ballot_sync(0xffffffffu, u == prefix);
+      if (lane == e) {
+        bits_g = any ^ eq;
+        bits_e = eq;
       }
-    });
+    }
+    if (lane < kKeys && x0 + 32 * lane < x1) {
+      wg[x0 / 32 + lane] = bits_g;
+      we[x0 / 32 + lane] = bits_e;
+    }
     __syncthreads();
     uint32_t bg = tid < nw ? wg[tid] : 0u, be = tid < nw ? we[tid] : 0u;
     const uint32_t ng = __popc(bg), ne = __popc(be);
@@ -229,9 +243,14 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_blocks_kernel(const Se
 
 cudaError_t launch_select_blocks(const SelectParams &p, cudaStream_t stream) {
   const dim3 grid((unsigned)p.Qmax, (unsigned)p.Hkv, (unsigned)p.B);
-  // a row has at most `cols` blocks: the smallest CTA that holds it in registers
+  // a row has at most `cols` blocks: a CTA that holds it in registers, of threads
+  // enough that each has few keys and few enough that a scan's barriers are short
+  // (16 rows of 4096 blocks: 5.7 us with 256 threads, 4.7 with 512, 4.8 to 5.2 with
+  // 1024; 256 rows of 16384: 14.5 with 512, 16 and more with 1024)
   if (p.cols <= 256 * 8)
     return launch_dependent(select_blocks_kernel<256, 8, 4>, grid, 256, 0, stream, p);
+  if (p.cols <= 512 * 8)
+    return launch_dependent(select_blocks_kernel<512, 8, 2>, grid, 512, 0, stream, p);
   if (p.cols <= 1024 * 8)
     return launch_dependent(select_blocks_kernel<1024, 8, 1>, grid, 1024, 0, stream, p);
   if (p.cols <= 512 * 32)
