@@ -17,8 +17,9 @@
 // products of up to 96 rows stay below them.  16 sequences of up to
 // 131072 tokens, 8 heads of 128, blocks of 32: 91 MB in 21.5 us, 4.3 TB/s; what
 // keeps it from the memory's rate is the start of the chain (page, queries and
-// lengths, asked for together -> bounds -> products) and the ragged end.  Eight queries of 6 heads of 256 over 262144 tokens, in
-// blocks of 64, are that chain alone, 5.8 us.
+// lengths, asked for together -> bounds -> products) and the ragged end.  Eight
+// queries of 6 heads of 256 over 262144 tokens, in blocks of 64, are that chain
+// alone, 5.8 us.
 #include <algorithm>
 
 #include "common.cuh"

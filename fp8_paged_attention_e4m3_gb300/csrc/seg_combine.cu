@@ -149,22 +149,18 @@ constexpr int kWarpThreads = 256;
 __global__ void __launch_bounds__(kWarpThreads) seg_combine_warps(const SegParams p) {
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const int lane = threadIdx.x & 31;
-  const int nd = p.D / 32, R = p.Qmax * p.G;
-  const int64_t x = (int64_t)blockIdx.x * (kWarpThreads / 32) + (threadIdx.x >> 5);
-  const int64_t rows = (int64_t)p.B * p.Hkv * R;
-  if (x >= rows * nd) return;
-  const int sl = (int)(x % nd);
-  const int64_t row = x / nd;
-  const int r = (int)(row % R);
-  const int64_t st = row / R;
-  const int h = (int)(st % p.Hkv), b = (int)(st / p.Hkv), i = r / p.G;
+  const int nds = p.D == 64 ? 1 : p.D == 128 ? 2 : 3;  // log2 of D / 32
+  const int x = blockIdx.x * (kWarpThreads / 32) + (threadIdx.x >> 5);
+  const int r = x >> nds, sl = x & ((1 << nds) - 1);
+  const int h = blockIdx.y, b = blockIdx.z, i = r / p.G;
+  if (i >= p.Qmax) return;
   uint32_t bits;
   const bool live = row_live(p, b, i, &bits);
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   if (bits != 0u && r == 0 && h == 0 && sl == 0 && lane == 0) atomicOr(p.status, bits);
   const int rg = r / p.N, rr = r - rg * p.N;
   int2 e = make_int2(0, 0);
-  if (live) e = p.tab[st * p.n_rg + rg];
+  if (live) e = p.tab[((int64_t)b * p.Hkv + h) * p.n_rg + rg];
   if (e.y < 0) return;
   const int g = lane >> 3, f = lane & 7;  // eight lanes read 128 bytes of a part; four groups
   const int nP = min(e.y, p.ctas);
@@ -243,10 +239,9 @@ cudaError_t launch_seg_combine(const SegParams &p, cudaStream_t stream) {
     return launch_dependent(seg_combine_rows, grid, kRowThreads, (size_t)p.ctas * 2 * sizeof(float),
                             stream, p);
   }
-  const int64_t warps = (int64_t)p.B * p.Hkv * R * (p.D / 32);
-  const int64_t blocks = (warps + kWarpThreads / 32 - 1) / (kWarpThreads / 32);
-  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  return launch_dependent(seg_combine_warps, dim3((unsigned)blocks), kWarpThreads, 0, stream, p);
+  const int warps = R * (p.D / 32), per = kWarpThreads / 32;
+  const dim3 grid((unsigned)((warps + per - 1) / per), (unsigned)p.Hkv, (unsigned)p.B);
+  return launch_dependent(seg_combine_warps, grid, kWarpThreads, 0, stream, p);
 }
 
 }  // namespace vae4
