@@ -16,10 +16,10 @@
 // CTAs + c + 1, CTAs + c + 2, ...
 //
 // What bounds it.  The keys' bytes, read once: 32 sequences of up to 32749
-// tokens, 8 heads of 128 (1.42 GB), take 265 us with the combine, 0.79 of the
+// tokens, 8 heads of 128 (1.42 GB), take 266 us with the combine, 0.79 of the
 // copy peak, the softmax and the decoders beside the copies using 54 % of the
 // issue slots.  One sequence of 262144 tokens, 48 rows of 256 (134 MB), takes
-// 36.1 us (0.55): 4 us to the first copy (lengths, plan, page), 3 to the first
+// 34.9 us (0.57): 3 us to the first copy (lengths, plan, page), 3 to the first
 // scores, 20 at the memory's rate, up to 4 for the SMs whose rows are raised
 // most often, 4 for the combine.
 //
@@ -334,6 +334,43 @@ done:
   }
 }
 
+// The same for a batch of one unit: no scan (0.7 to 1.2 us less to the first copy).
+template <bool LISTED>
+static __device__ __noinline__ void plan_one(const SegParams &p, Lengths len, int cta,
+                                             volatile int *state, Segment *seg, int *bad, int lane) {
+  int2 v, vis = make_int2(0, 0);
+  if (LISTED && !len.dry) {
+    const BlockStream r = p.streams[0];
+    v = make_int2(r.ql > 0 ? r.n16 : 0, r.ql);
+    vis = make_int2(r.n, r.L);
+  } else {
+    v = len.of(p, 0);
+  }
+  const int total = v.x > 0 ? unit_places(v) : 0;
+  const int q = total > 0 ? (total + p.ctas - 1) / p.ctas : 1;
+  const int a = max(kUnitCost, cta * q), end = min((cta + 1) * q, total);
+  if (lane == 0) {
+    if (end > a) {
+      const bool starts = a == kUnitCost, ends = end == total;
+      Segment s;
+      s.b = 0;
+      s.h_rg = 0;
+      s.k0 = (a - kUnitCost) * 64;
+      s.k1 = min((end - kUnitCost) * 64, LISTED && !len.dry ? vis.x : v.x);
+      s.L = LISTED && !len.dry ? vis.y : v.x;
+      s.ql = v.y;
+      s.slot = !starts ? p.ctas + cta : ends ? -1 : cta;
+      s.pad = 0;
+      seg[0] = s;
+      bad[0] = 0;
+      if (starts && !len.dry) p.tab[0] = make_int2(cta, ends ? -1 : (total - 1) / q - cta + 1);
+    }
+    state[-2] = end > a;
+    state[-1] = 0;
+  }
+  __syncwarp();
+}
+
 // ---------------------------------------------------------------------------
 // Zero the raw V bytes of keys kz .. 63 of a half-tile slot in the columns
 // V decoder warp dq reads (d = 128 mh + 32 dq + 0..31).  The slot was written
@@ -422,6 +459,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool producer = warp == kWKProd || warp == kWVProd;
   const int cta = blockIdx.x;
+  const bool one_unit = p.groups == 1 && p.unit_heads * p.n_rg == 1;
 
   // ---- set-up that touches only this CTA's shared memory and TMEM, done
   // before the grid dependency wait so it overlaps the previous kernel's tail
@@ -452,7 +490,11 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
     // The plan's code runs once on an invented batch, while the previous kernel
     // ends and the barriers and TMEM are set up: its instructions are then at
     // hand when the lengths arrive (its first run took 6000 cycles).
-    plan_segments<LISTED>(p, Lengths{nullptr, 1, true}, N, 0, true, nseg_s + 2, seg_s, bad_s, lane);
+    const Lengths dry{nullptr, 1, true};
+    if (one_unit)
+      plan_one<LISTED>(p, dry, 0, nseg_s + 2, seg_s, bad_s, lane);
+    else
+      plan_segments<LISTED>(p, dry, N, 0, true, nseg_s + 2, seg_s, bad_s, lane);
   }
   if (warp == kWQk) {
     tc::tmem_alloc(sSm + C::S_SCAL + 4, 512);
@@ -488,9 +530,13 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
       for (int x = tid; x < p.groups; x += C::NTHREADS) st_len[x] = group_len(p, x);
       __syncthreads();
     }
-    if (warp == kWKProd)
-      plan_segments<LISTED>(p, Lengths{staged ? st_len : nullptr, p.groups, false}, N, cta, first,
-                            nseg_s + 2, seg_s, bad_s, lane);
+    if (warp == kWKProd) {
+      const Lengths len{staged ? st_len : nullptr, p.groups, false};
+      if (one_unit)
+        plan_one<LISTED>(p, len, cta, nseg_s + 2, seg_s, bad_s, lane);
+      else
+        plan_segments<LISTED>(p, len, N, cta, first, nseg_s + 2, seg_s, bad_s, lane);
+    }
     if (staged) tc::fence_proxy_async_smem();  // the ring is next written by tensor copies
     __syncthreads();
     const int nseg = nseg_s[0];
