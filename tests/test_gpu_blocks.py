@@ -848,6 +848,62 @@ def test_steps_in_a_row_wait_for_one_another():
         assert torch.equal(a, b)
 
 
+def test_captured_calls_on_two_branches():
+    """A graph whose branches run side by side after the writer and join before
+    the sparse call gives the bits of the calls one by one, on every replay."""
+    c = Cache([(3000, 3), (700, 2)], 2, 128, 64, 16, seed=18)
+    Q, G, k = 3, 4, 9
+    q, bd = queries(c, Q, G), bounds_of(c)
+    x = torch.randn(2, Q, 2, 128, generator=torch.Generator().manual_seed(3)).half()
+    cap = c.table.shape[1] * c.page
+    qd, bt, seq, xd = dev(q, c.table, c.seq, x)
+    kv0, sc0, bd0 = c.device(), c.scales.cuda(), bd.cuda()
+    kc, vc, sc, bdd = kv0[0].clone(), kv0[1].clone(), sc0.clone(), bd0.clone()
+    scores = torch.zeros(2, Q, 2, cap // 16, device="cuda")
+    ids = torch.zeros(2, Q, 2, k, dtype=torch.int32, device="cuda")
+    outs = torch.zeros(2, *qd.shape, dtype=torch.float16, device="cuda")
+    ws = vae4.alloc_workspace(2, 8, 2, Q, 128, cap)
+    wl = vae4.alloc_sparse_workspace(2, 8, 2, Q, 128, cap, 16, k)
+
+    def step(main, side):
+        wait = torch.cuda.synchronize if side is None else (lambda: None)
+        vae4.verify_attn_e4m3_append(xd, xd, kc, vc, bt, seq, sc, k_bounds=bdd)
+        wait()
+        if side is not None:
+            side.wait_stream(main)
+        vae4.verify_attn_e4m3_block_scores(qd, bdd, bt, seq, sc, scores, block_tokens=16, stream=side)
+        wait()
+        vae4.verify_attn_e4m3_select_blocks(scores, seq, ids, block_tokens=16, stream=side)
+        wait()
+        vae4.verify_attn_e4m3_block_scaled(qd, kc, vc, bt, seq, sc, outs[0], ws)
+        wait()
+        if side is not None:
+            main.wait_stream(side)
+        vae4.verify_attn_e4m3_sparse(qd, kc, vc, bt, seq, sc, ids, outs[1], wl)
+        wait()
+
+    def restore():
+        for t, o in ((kc, kv0[0]), (vc, kv0[1]), (sc, sc0), (bdd, bd0)):
+            t.copy_(o)
+        for t in (scores, ids, outs):
+            t.zero_()
+        torch.cuda.synchronize()
+
+    step(None, None)
+    want = [t.clone() for t in (kc, vc, sc, bdd, scores, ids, outs)]
+    restore()
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(torch.cuda.current_stream(), side)
+    for _ in range(5):
+        restore()
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip((kc, vc, sc, bdd, scores, ids, outs), want):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert vae4.read_status(ws) == 0 and vae4.read_status(wl) == 0
+
+
 @pytest.mark.parametrize("graph", [False, True])
 @pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
 def test_decoding_steps_together(graph, fmt):
