@@ -163,10 +163,11 @@ __device__ __forceinline__ int div16(int key, unsigned long long m) {
 // Programmatic dependent launch.  A kernel launched so may be placed while the
 // one before it on the stream still runs: it touches global memory only after
 // await_previous(), which every thread calls and which returns when that kernel
-// has ended; the one after it may then be placed early in the same way.
+// has ended; the one after it may then be placed early in the same way (not
+// before: it may read inputs, which earlier kernels wrote, ahead of its wait).
 __device__ __forceinline__ void await_previous() {
-  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 }
 template <class P>
 cudaError_t launch_dependent(void (*kernel)(P), dim3 grid, int threads, size_t smem,
