@@ -16,9 +16,8 @@
 // CTAs + c + 1, CTAs + c + 2, ...
 //
 // What bounds it.  The keys' bytes, read once: 32 sequences of up to 32749
-// tokens, 8 heads of 128 (1.42 GB), take 266 us with the combine, 0.79 of the
-// copy peak, the softmax and the decoders beside the copies using 54 % of the
-// issue slots.  One sequence of 262144 tokens, 48 rows of 256 (134 MB), takes
+// tokens, 8 heads of 128 (1.42 GB), take 234 us with the combine, 0.90 of the
+// copy peak, with the softmax and the decoders beside the copies.  One sequence of 262144 tokens, 48 rows of 256 (134 MB), takes
 // 34.9 us (0.57): 3 us to the first copy (lengths, plan, page), 3 to the first
 // scores, 20 at the memory's rate, up to 4 for the SMs whose rows are raised
 // most often, 4 for the combine.
@@ -39,15 +38,19 @@
 //                     the page (block) is a multiple of, into rings of raw
 //                     half-tiles.  (Boxes of 16 keys of 128 bytes held the
 //                     copies to 0.71 of the copy peak with all other work
-//                     taken out, boxes of 64 to 0.88.)  The K producer also
-//                     plans the segments, the V producer passes on the scales
-//                     (positions, masks) of 512 keys at a time, one 16-key box
-//                     per lane, requested 512 keys ahead.
+//                     taken out, boxes of 64 to 0.88.)  Their loops
+//                     are one warp's serial code and bound the copies of small
+//                     keys: with the scales passed by one of them the batch
+//                     above took 266 us.  The K producer also plans the
+//                     segments.
 //   K decoders (4)  : thread = key; exact FP8 -> FP16 into tensor memory, the
 //                     A operand of S^T = K . Q^T.
 //   V decoders (4)  : transposing 8-bit ldmatrix, the same conversion, into
 //                     tensor memory, the A operand of O^T = V^T . P^T.
-//   score MMA, value MMA: one thread each issues the products of a tile.
+//   score MMA, value MMA: one thread each issues the products of a tile.  The
+//                     score warp also passes on the scales (positions, masks)
+//                     of 512 keys at a time, one 16-key box per lane, requested
+//                     512 keys ahead.
 //   softmax (8)     : thread = key, half of the N rows each.  The reference m
 //                     of a row is raised only when a weight would pass 2^15
 //                     (one vote per tile); then only the rows concerned, and
@@ -115,8 +118,8 @@ struct Cfg {
   static constexpr int PB = 128 * 128;          // P^T, MN-major SW128 (N <= 64)
   static constexpr int RSLOT = 64 * D;          // one raw K or V half-tile
   static constexpr int LIMIT = 232448 - 1024;   // opt-in maximum minus alignment slack
-  // groups of 512 keys whose scales are held: the V producer runs some
-  // tiles ahead of the softmax and must not wait for it here
+  // groups of 512 keys whose scales are held: the score warp runs two tiles
+  // ahead of the softmax and must not wait for it here
   static constexpr int NSG = 4;
   // small region: barriers, scalars, row state, scale boxes, segments
   static constexpr int S_SCAL = 640, S_M = 704, S_BASE = S_M + 512, S_THR = S_BASE + 512,
@@ -515,8 +518,9 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
   const long long LIM = p.wait_limit;
   const int lb = p.box_log2;  // keys per tensor copy
   // counters of the role that run through all segments: half-tiles or tiles,
-  // and segments (score MMA) or groups of scales (softmax, V producer)
+  // and segments (score MMA) or groups of scales (softmax)
   int count = 0, count2 = 0;
+  int groups = 0;  // of scales passed (score MMA)
   bool mma_issued = false;
   bool first = true;
 
@@ -600,83 +604,6 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
       };
       int2 itc = make_int2(0, 0);
       request(itc);
-      // ---- scales, by the V producer, four tiles at a time: lane = one 16-key
-      // box of a group of 512 keys (a box lies in one block).  A group is
-      // requested a group ahead of its use, the page ids that lead to it two.
-      float4 *box_s = reinterpret_cast<float4 *>(gSm + C::S_BOX);
-      uint32_t *mask_s = reinterpret_cast<uint32_t *>(gSm + C::S_MASK);
-      auto step = [&](int2 it) -> int2 {  // (segment, group) after it
-        if (it.x >= nseg) return it;
-        return 4 * (it.y + 1) < tiles_of(it.x) ? make_int2(it.x, it.y + 1) : make_int2(it.x + 1, 0);
-      };
-      auto key_of = [&](int2 it) -> int {  // -1: past the segment
-        if (it.x >= nseg) return -1;
-        const int key = seg_s[it.x].k0 + 512 * it.y + 16 * lane;
-        return key < seg_s[it.x].k1 ? key : -1;
-      };
-      auto load_page = [&](int2 it) -> int {
-        if constexpr (LISTED) return 0;
-        const int key = key_of(it);
-        return key >= 0 ? __ldg(p.bt + (int64_t)seg_s[it.x].b * p.bt_sb + div16(key, p.page_m)) : -1;
-      };
-      float4 f = make_float4(0.f, 0.f, 1.f, 0.f);  // (s_K, s_V); listed: the entry's
-      int2 e = make_int2(0, 0);                    // listed: first token, mask
-      bool live = false;
-      auto load_scales = [&](int2 it, int page) {
-        const int key = key_of(it);
-        live = key >= 0;
-        if constexpr (LISTED) {
-          if (live) {
-            const int x = div16(key, p.blk_m);
-            const BlockEntry *en = p.list + (int64_t)seg_s[it.x].b * p.list_cap + x;
-            e = __ldg(reinterpret_cast<const int2 *>(&en->tok0));
-            e.x += key - x * p.blk;
-            f = __ldg(reinterpret_cast<const float4 *>(&en->alpha));
-          }
-        } else {
-          live = live && page >= 0 && page < p.n_pages;
-          if (live) {
-            const float *sp = p.scales + (int64_t)page * p.s_page +
-                              (int64_t)(seg_s[it.x].h_rg & 0xFFFF) * p.s_head +
-                              (div16(key, p.blk_m) - div16(key, p.page_m) * p.page_blocks);
-            f.x = __ldg(sp);
-            f.y = __ldg(sp + p.s_kv);
-          }
-        }
-      };
-      int2 it0 = make_int2(0, 0), it1 = step(it0);
-      int page1 = -1;
-      if (isv) {
-        load_scales(it0, load_page(it0));
-        page1 = load_page(it1);
-      }
-      auto pass_scales = [&]() -> bool {  // group it0; then request the next
-        const int sl = count2 % C::NSG;
-        if (count2 >= C::NSG &&
-            !tc::mbar_wait_brief(bar(kScEmpty + sl), (count2 / C::NSG - 1) & 1, abort_f, LIM))
-          return false;
-        float4 o = make_float4(0.f, 0.f, 1.f, 0.f);  // past the segment, or invalid
-        if (live) {
-          if constexpr (LISTED) {
-            o = make_float4(f.x, f.y, f.z, __int_as_float(e.x));
-            mask_s[sl * 32 + lane] = (uint32_t)e.y;
-          } else {
-            const float sk = f.x, sv = f.y;
-            if (sk >= kMinScale && sk <= kMaxScale && sv >= kMinScale && sv <= kMaxScale)
-              o = make_float4(p.sm_scale * kLog2e * sk, __log2f(sv), __fdividef(1.f, sv), 0.f);
-            else
-              atomicOr(&bad_s[it0.x], 2);
-          }
-        }
-        box_s[sl * 32 + lane] = o;
-        tc::mbar_arrive(bar(kScFull + sl));
-        ++count2;
-        load_scales(it1, page1);
-        it0 = it1;
-        it1 = step(it1);
-        page1 = load_page(it1);
-        return true;
-      };
       bool ok = true;
       auto produce = [&](auto nb_tag) {
         constexpr int NB = decltype(nb_tag)::value;  // copies per half-tile
@@ -720,9 +647,6 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
                            seg_s[s].k1 - seg_s[s].k0 - 64 * t, mine < p.n_pages ? mine : -1, box, slot,
                            full, lane);
             }
-            // a group's scales follow its first copy (their loads may still be
-            // on the way, and the softmax needs them later than the keys)
-            if (isv && (t & 7) == 0 && !(ok = pass_scales())) break;
             ++count;
             if (++st == nslot) {
               st = 0;
@@ -742,6 +666,80 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
       // The whole warp runs the loop and one elected lane issues, so that the
       // operands stay in uniform registers (TMEM addresses are constants: the
       // CTA holds all 512 columns).
+      // ---- scales, four tiles at a time: lane = one 16-key box of a group of
+      // 512 keys (a box lies in one block).  A group is requested a group ahead
+      // of its use, the page ids that lead to it two.
+      float4 *box_s = reinterpret_cast<float4 *>(gSm + C::S_BOX);
+      uint32_t *mask_s = reinterpret_cast<uint32_t *>(gSm + C::S_MASK);
+      auto step = [&](int2 it) -> int2 {  // (segment, group) after it
+        if (it.x >= nseg) return it;
+        return 4 * (it.y + 1) < tiles_of(it.x) ? make_int2(it.x, it.y + 1) : make_int2(it.x + 1, 0);
+      };
+      auto key_of = [&](int2 it) -> int {  // -1: past the segment
+        if (it.x >= nseg) return -1;
+        const int key = seg_s[it.x].k0 + 512 * it.y + 16 * lane;
+        return key < seg_s[it.x].k1 ? key : -1;
+      };
+      auto load_page = [&](int2 it) -> int {
+        if constexpr (LISTED) return 0;
+        const int key = key_of(it);
+        return key >= 0 ? __ldg(p.bt + (int64_t)seg_s[it.x].b * p.bt_sb + div16(key, p.page_m)) : -1;
+      };
+      float4 f = make_float4(0.f, 0.f, 1.f, 0.f);  // (s_K, s_V); listed: the entry's
+      int2 e = make_int2(0, 0);                    // listed: first token, mask
+      bool live = false;
+      auto load_scales = [&](int2 it, int page) {
+        const int key = key_of(it);
+        live = key >= 0;
+        if constexpr (LISTED) {
+          if (live) {
+            const int x = div16(key, p.blk_m);
+            const BlockEntry *en = p.list + (int64_t)seg_s[it.x].b * p.list_cap + x;
+            e = __ldg(reinterpret_cast<const int2 *>(&en->tok0));
+            e.x += key - x * p.blk;
+            f = __ldg(reinterpret_cast<const float4 *>(&en->alpha));
+          }
+        } else {
+          live = live && page >= 0 && page < p.n_pages;
+          if (live) {
+            const float *sp = p.scales + (int64_t)page * p.s_page +
+                              (int64_t)(seg_s[it.x].h_rg & 0xFFFF) * p.s_head +
+                              (div16(key, p.blk_m) - div16(key, p.page_m) * p.page_blocks);
+            f.x = __ldg(sp);
+            f.y = __ldg(sp + p.s_kv);
+          }
+        }
+      };
+      int2 it0 = make_int2(0, 0), it1 = step(it0);
+      int page1 = -1;
+      load_scales(it0, load_page(it0));
+      page1 = load_page(it1);
+      auto pass_scales = [&]() -> bool {  // group it0; then request the next
+        const int sl = groups % C::NSG;
+        if (groups >= C::NSG && !warp_wait(bar(kScEmpty + sl), (groups / C::NSG - 1) & 1))
+          return false;
+        float4 o = make_float4(0.f, 0.f, 1.f, 0.f);  // past the segment, or invalid
+        if (live) {
+          if constexpr (LISTED) {
+            o = make_float4(f.x, f.y, f.z, __int_as_float(e.x));
+            mask_s[sl * 32 + lane] = (uint32_t)e.y;
+          } else {
+            const float sk = f.x, sv = f.y;
+            if (sk >= kMinScale && sk <= kMaxScale && sv >= kMinScale && sv <= kMaxScale)
+              o = make_float4(p.sm_scale * kLog2e * sk, __log2f(sv), __fdividef(1.f, sv), 0.f);
+            else
+              atomicOr(&bad_s[it0.x], 2);
+          }
+        }
+        box_s[sl * 32 + lane] = o;
+        tc::mbar_arrive(bar(kScFull + sl));
+        ++groups;
+        load_scales(it1, page1);
+        it0 = it1;
+        it1 = step(it1);
+        page1 = load_page(it1);
+        return true;
+      };
       constexpr uint32_t id_qk = tc::idesc_f16(128, N, 0, 0);
       const uint64_t dq0 = tc::smem_desc(sQ, 16, 1024);
       bool ok = true;
@@ -750,6 +748,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
         if (!(ok = warp_wait(bar(kQReady), count2 & 1))) break;
         for (int jl = 0; jl < ntiles; ++jl, ++count) {
           const int j = count, kb = j % C::NKB;
+          if ((jl & 3) == 0 && !(ok = pass_scales())) break;
           if (!(ok = warp_wait(bar(kKReady + kb), (j / C::NKB) & 1))) break;
           if (j >= 2 && !(ok = warp_wait(bar(kSFree + (j & 1)), ((j >> 1) - 1) & 1))) break;
           tc::tc_fence_after();
