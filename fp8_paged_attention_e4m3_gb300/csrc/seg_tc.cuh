@@ -17,10 +17,10 @@
 //
 // What bounds it.  The keys' bytes, read once: 32 sequences of up to 32749
 // tokens, 8 heads of 128 (1.42 GB), take 234 us with the combine, 0.90 of the
-// copy peak, with the softmax and the decoders beside the copies.  One sequence of 262144 tokens, 48 rows of 256 (134 MB), takes
-// 34.9 us (0.57): 3 us to the first copy (lengths, plan, page), 3 to the first
-// scores, 20 at the memory's rate, up to 4 for the SMs whose rows are raised
-// most often, 4 for the combine.
+// copy peak, with the softmax and the decoders beside the copies.  One sequence
+// of 262144 tokens, 48 rows of 256 (134 MB), takes 34.9 us (0.57): 3 us to the
+// first copy (lengths, plan, page), 3 to the first scores, 20 at the memory's
+// rate, up to 4 for the SMs whose rows are raised most often, 4 for the combine.
 //
 // Mathematics.  With t = softmax_scale log2(e) s_K (q . dec(K)) the score of a
 // key in log2 units and g = log2 s_V of its block, its weight is
@@ -38,11 +38,10 @@
 //                     the page (block) is a multiple of, into rings of raw
 //                     half-tiles.  (Boxes of 16 keys of 128 bytes held the
 //                     copies to 0.71 of the copy peak with all other work
-//                     taken out, boxes of 64 to 0.88.)  Their loops
-//                     are one warp's serial code and bound the copies of small
-//                     keys: with the scales passed by one of them the batch
-//                     above took 266 us.  The K producer also plans the
-//                     segments.
+//                     taken out, boxes of 64 to 0.88.)  Their loops are one
+//                     warp's serial code and bound the copies of small keys:
+//                     with the scales passed by one of them the batch above
+//                     took 266 us.  The K producer also plans the segments.
 //   K decoders (4)  : thread = key; exact FP8 -> FP16 into tensor memory, the
 //                     A operand of S^T = K . Q^T.
 //   V decoders (4)  : transposing 8-bit ldmatrix, the same conversion, into
