@@ -524,6 +524,10 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
   bool first = true;
 
   for (;;) {  // up to kMaxSeg segments at a time
+    // Whether the roles run is one answer for the CTA, read here, where no role
+    // runs that could raise the flag: the softmax warps meet at barriers that
+    // have no time limit, so they enter all or none.
+    const bool wound_down = *abort_f != 0;
     // ---- the plan, by the K producer; the lengths of more than 32 groups are
     // staged by all threads in the K ring (idle here), but read as they are if
     // they do not fit
@@ -549,8 +553,8 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
     };
     auto tiles_of = [&](int s) -> int { return (seg_s[s].k1 - seg_s[s].k0 + 127) >> 7; };
 
-    if (*abort_f != 0) {
-      // (wound down: the segments are only marked below)
+    if (wound_down) {
+      // (the segments are only marked below)
     } else if (producer) {
       // =============================== producers (K ring, V ring)
       const bool isv = warp == kWVProd;

@@ -1,0 +1,76 @@
+"""The block-scaled cache's calls where they can go wrong: waits that run out,
+host threads at once, weights far below the largest, NaN queries, invalid
+scales.  References and their tolerances as in test_gpu_blocks.py, unless a
+test derives its own."""
+import math
+import threading
+
+import pytest
+import torch
+
+import fp8_paged_attention_e4m3_gb300 as vae4
+from test_gpu_blocks import FMT, Cache, bounds_of, check, dev, listed, queries, reference
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    vae4.load()
+
+
+def guarded(shape, fill):
+    """An FP16 tensor within a larger buffer, and the buffer's other elements."""
+    n, pad = math.prod(shape), 4096
+    buf = torch.full((n + 2 * pad,), fill, dtype=torch.float16, device="cuda")
+    return buf[pad:pad + n].view(shape), (buf[:pad], buf[pad + n:])
+
+
+TIMEOUTS = [
+    # lens, Q, G, Hkv, D, page, block, layout, num_sms
+    ([(3000, 4), (100, 4), (50, 2)], 4, 3, 2, 128, 32, 16, "tokens", 0),
+    ([(2000, 8)], 8, 6, 1, 256, 16, 16, "tokens", 0),
+    ([(700, 16), (90, 16)], 16, 6, 2, 64, 32, 32, "pool", 5),      # two row groups
+    ([(300, 2)] * 5, 2, 2, 2, 128, 32, 16, "padded", 0),           # 8-byte copies
+    ([(130 + b, 1) for b in range(30)], 1, 2, 4, 64, 16, 16, "tokens", 1),  # 120 segments of one CTA
+]
+
+
+def timed_out(c, q, layout, num_sms, repeats):
+    """Calls whose waits all run out, `repeats` dense and as many sparse ones,
+    and after them one of each that is left alone."""
+    Q, Hq = q.shape[1:3]
+    k, v = c.device(layout)
+    qd, bt, seq, sc = dev(q, c.table, c.seq, c.scales)
+    B, cap = len(c.lens), c.table.shape[1] * c.page
+    ids = torch.arange(5, dtype=torch.int32).expand(B, Q, c.Hkv, 5).contiguous()
+    idd = ids.cuda()
+    for sp in (False, True):
+        n = (vae4.sparse_workspace_bytes(B, Hq, c.Hkv, Q, c.D, cap, c.blk, 5, num_sms) if sp else
+             vae4.block_scaled_workspace_bytes(B, Hq, c.Hkv, Q, c.D, cap, num_sms))
+        ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+        for it in range(repeats + 1):
+            flags = vae4.FLAG_TEST_SHORT_WAITS if it < repeats else 0
+            out, guards = guarded(q.shape, 3.0)
+            if sp:
+                vae4.verify_attn_e4m3_sparse(qd, k, v, bt, seq, sc, idd, out, ws, flags=flags,
+                                             num_sms=num_sms)
+            else:
+                vae4.verify_attn_e4m3_block_scaled(qd, k, v, bt, seq, sc, out, ws, flags=flags,
+                                                   num_sms=num_sms)
+            torch.cuda.synchronize()
+            assert all((g == 3).all() for g in guards)
+            assert vae4.read_status(ws) == (vae4.STATUS_TIMEOUT if flags else 0)
+            if flags:
+                assert not out.any()
+                vae4.clear_status(ws)
+        check(out.cpu(), *reference(c, q, allowed=listed(c, ids) if sp else None))
+
+
+@pytest.mark.parametrize("lens,Q,G,Hkv,D,page,blk,layout,num_sms", TIMEOUTS)
+def test_waits_that_run_out_end_the_call_every_time(lens, Q, G, Hkv, D, page, blk, layout, num_sms):
+    """Whichever role gives up first, and however late the others look: the
+    call ends, its rows are zero, and nothing past them is written."""
+    c = Cache(lens, Hkv, D, page, blk, seed=31)
+    timed_out(c, queries(c, Q, G), layout, num_sms, 40)
