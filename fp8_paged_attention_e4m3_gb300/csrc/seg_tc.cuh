@@ -530,8 +530,9 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
     const bool wound_down = *abort_f != 0;
     // ---- the plan, by the K producer; the lengths of more than 32 groups are
     // staged by all threads in the K ring (idle here), but read as they are if
-    // they do not fit
-    const bool staged = p.groups > 32 && p.groups <= C::NKR * C::RSLOT / 8;
+    // they do not fit, or if copies that a timed-out batch of segments left in
+    // flight may still write the ring
+    const bool staged = !wound_down && p.groups > 32 && p.groups <= C::NKR * C::RSLOT / 8;
     int2 *st_len = reinterpret_cast<int2 *>(gKR);
     if (staged) {
       for (int x = tid; x < p.groups; x += C::NTHREADS) st_len[x] = group_len(p, x);

@@ -74,3 +74,16 @@ def test_waits_that_run_out_end_the_call_every_time(lens, Q, G, Hkv, D, page, bl
     call ends, its rows are zero, and nothing past them is written."""
     c = Cache(lens, Hkv, D, page, blk, seed=31)
     timed_out(c, queries(c, Q, G), layout, num_sms, 40)
+
+
+@pytest.mark.parametrize("lens,Q,G,Hkv,D,page,blk,layout,num_sms", [
+    ([(130 + 7 * b, 1) for b in range(40)], 1, 2, 4, 64, 16, 16, "tokens", 1),
+    ([(200 + b, 3) for b in range(70)], 3, 4, 2, 128, 64, 32, "padded", 2),
+    ([(90, 2)] * 50, 2, 1, 3, 256, 32, 16, "pool", 1),
+])
+def test_waits_that_run_out_with_segments_left(lens, Q, G, Hkv, D, page, blk, layout, num_sms):
+    """More than 32 groups and more segments a CTA than it plans at a time: the
+    later ones are planned while copies of the first may be in flight."""
+    c = Cache(lens, Hkv, D, page, blk, seed=32)
+    assert len(lens) * Hkv > 64 * num_sms
+    timed_out(c, queries(c, Q, G), layout, num_sms, 20)
