@@ -11,6 +11,7 @@
 // way together.  (Filling them in as they were found, 32 blocks of a warp's
 // share after another, took 31.5 us for 16384 blocks; this takes 6.)
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -130,9 +131,23 @@ cudaError_t launch_block_list(const ListParams &p, cudaStream_t stream) {
   const int nblk = (p.capacity + p.blk - 1) / p.blk;
   const int smem = (nblk + 7) / 8 * 16;
   if (smem > 48 * 1024) {  // beyond the default dynamic shared-memory limit
-    const cudaError_t e =
-        cudaFuncSetAttribute(block_list_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
+    // The limit belongs to the function in the device's context, whatever host
+    // thread sets it: once per context, to the most that any call needs, so that
+    // none lowers it between another's setting and launch.
+    constexpr int kDevs = 64;
+    static std::atomic<unsigned long long> configured[kDevs] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+    const unsigned long long ctx = current_context_id();
+    if (dev < 0 || dev >= kDevs || ctx == 0 ||
+        configured[dev].load(std::memory_order_acquire) != ctx) {
+      const cudaError_t e =
+          cudaFuncSetAttribute(block_list_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kMaxListBlocks * 2);
+      if (e != cudaSuccess) return e;
+      if (dev >= 0 && dev < kDevs)
+        configured[dev].store(current_context_id(), std::memory_order_release);
+    }
   }
   return launch_dependent(block_list_kernel, dim3((unsigned)p.Hkv, (unsigned)p.B), kListThreads,
                           (size_t)smem, stream, p);

@@ -4,6 +4,7 @@ scales.  References and their tolerances as in test_gpu_blocks.py, unless a
 test derives its own."""
 import math
 import threading
+import threading
 
 import pytest
 import torch
@@ -87,3 +88,41 @@ def test_waits_that_run_out_with_segments_left(lens, Q, G, Hkv, D, page, blk, la
     c = Cache(lens, Hkv, D, page, blk, seed=32)
     assert len(lens) * Hkv > 64 * num_sms
     timed_out(c, queries(c, Q, G), layout, num_sms, 20)
+
+
+def test_sparse_calls_of_two_host_threads():
+    """Two host threads whose visit lists need different amounts of shared
+    memory, both above the default limit, on a stream each: every call is
+    launched, and each gives what it gives alone."""
+    q = torch.randn(1, 2, 4, 64, generator=torch.Generator().manual_seed(3)).half()
+    work = []
+    for blocks in (24600, 98304):
+        c = Cache([(500, 2)], 1, 64, 16, 16, seed=33)
+        table = torch.full((1, blocks), -1, dtype=torch.int32)
+        table[:, :c.table.shape[1]] = c.table
+        ids = torch.tensor([0, 3, 17, 31], dtype=torch.int32).expand(1, 2, 1, 4).contiguous()
+        k, v = c.device()
+        qd, bt, seq, sc, idd = dev(q, table, c.seq, c.scales, ids)
+        ws = vae4.alloc_sparse_workspace(1, 4, 1, 2, 64, blocks * 16, 16, 4)
+        work.append((c, ids, (qd, k, v, bt, seq, sc, idd, torch.zeros_like(qd), ws), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    go, errors = threading.Barrier(len(work)), []
+
+    def calls(args, stream):
+        try:
+            go.wait()
+            for _ in range(3000):
+                vae4.verify_attn_e4m3_sparse(*args, stream=stream)
+        except Exception as e:  # reported by the test's own thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=calls, args=w[2:]) for w in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for c, ids, args, _ in work:
+        assert vae4.read_status(args[-1]) == 0
+        check(args[-2].cpu(), *reference(c, q, allowed=listed(c, ids)))
