@@ -506,6 +506,17 @@ int verify_attn_e4m3_append(const vae4_tensor *k_new, const vae4_tensor *v_new,
  *     z_t = softmax_scale * s_K[t / S] * q . dec(K_t)
  *     out = sum_t e^(z_t - max z) s_V[t / S] dec(V_t) / sum_t e^(z_t - max z)
  *
+ * Scores, row sums and weighted sums are FP32.  A weight w_t = e^(z_t - max z)
+ * s_V[t / S] enters the product with dec(V_t) in FP16, relative to the largest
+ * of its row, W: to 11 bits down to 2^-14 W, to within 2^-25 W below (less than
+ * that is left out).  So beside FP32 sums and the rounding of out, an element is
+ * off by at most
+ *
+ *     (2^-11 sum_t w_t |dec(V_t)| + 2^-25 W sum_t |dec(V_t)|) / sum_t e^(z_t - max z)
+ *
+ * So with scales far apart a key whose w_t is 2^-k W counts with 25 - k bits
+ * where k > 14, with none past 25, also in channels in which the codes of the
+ * block of W are zero.
  * Arguments, results and errors as verify_attn_e4m3_kv with block_scales in
  * the place of kv_scales.  A block with an invalid scale sets BAD_SCALE and
  * zeroes the rows of its sequence and KV head, as an invalid page does.
@@ -514,7 +525,9 @@ int verify_attn_e4m3_append(const vae4_tensor *k_new, const vae4_tensor *v_new,
  * The batch's keys are divided evenly among the SMs on the device, from the
  * lengths of the call (so a captured graph stays balanced as they change):
  * opt->partition_tokens must be 0 (VAE4_ERR_PARTITION).  At most 65535 KV
- * heads; num_sms counts up to 4096.  Repeated calls give the same bits.  hilo_pv and VAE4_FLAG_WARP_MMA: VAE4_ERR_UNSUPPORTED.
+ * heads; num_sms counts up to 4096.  Repeated calls give the same bits.
+ * hilo_pv (a second product per key step for the residual of the weights) and
+ * VAE4_FLAG_WARP_MMA: VAE4_ERR_UNSUPPORTED.
  */
 int verify_attn_e4m3_block_scaled(const vae4_tensor *q, const vae4_tensor *k_cache,
                                   const vae4_tensor *v_cache, const vae4_tensor *block_table,

@@ -126,3 +126,46 @@ def test_sparse_calls_of_two_host_threads():
     for c, ids, args, _ in work:
         assert vae4.read_status(args[-1]) == 0
         check(args[-2].cpu(), *reference(c, q, allowed=listed(c, ids)))
+
+
+@pytest.mark.parametrize("L,sparse_call", [(64, False), (3000, False), (64, True), (3000, True)])
+@pytest.mark.parametrize("far", [6, 13, 20, 26])
+def test_small_scales_beside_a_large_one_with_zero_codes(L, sparse_call, far):
+    """One block's s_V is 2^far times the others', its codes are zero in half of
+    the channels: what the other blocks give there is seen to the stated bound.
+    With p = e^z / sum e^z, w = p s_V, W its largest in the row and c the codes:
+        |got - out| <= (2^-11 + 2^-11) sum w |c| + 2^-25 W sum |c| + 2^-11 |out| + 2^-25
+    (weights: 2^-11 and 2^-25 W; as much again for FP32 scores and sums, which are
+    off by less; out rounded to FP16)."""
+    c = Cache([(L, 2)], 1, 64, 16, 16, seed=34)
+    q = queries(c, 2, 3)
+    n_blk = -(-L // 16)
+    c.scales[:, 1] = torch.where(c.scales[:, 1].isnan(), c.scales[:, 1], torch.tensor(1.0))
+    big = int(c.table[0, 1])
+    c.scales[big, 1] = 2.0 ** far
+    c.codes[1][big, :, :, :32] = 0
+    if far > 7:  # the other channels inside FP16's range
+        c.codes[1][big, :, :, 32:] &= 0x83
+    K, s = c.values(0, 0), c.scales[c.table[0, :n_blk].long(), 1, 0, 0].double().repeat_interleave(16)[:L]
+    codes = c.values(1, 0)[:, 0] / s[:, None]
+    ids = torch.arange(n_blk, dtype=torch.int32).expand(1, 2, 1, n_blk).contiguous()
+    k, v = c.device()
+    qd, bt, seq, sc, idd = dev(q, c.table, c.seq, c.scales, ids)
+    out, cap = torch.zeros_like(qd), c.table.shape[1] * 16
+    if sparse_call:
+        ws = vae4.alloc_sparse_workspace(1, 3, 1, 2, 64, cap, 16, n_blk)
+        vae4.verify_attn_e4m3_sparse(qd, k, v, bt, seq, sc, idd, out, ws)
+    else:
+        ws = vae4.alloc_workspace(1, 3, 1, 2, 64, cap)
+        vae4.verify_attn_e4m3_block_scaled(qd, k, v, bt, seq, sc, out, ws)
+    assert vae4.read_status(ws) == 0
+    for i in range(2):
+        z = q[0, i].double() @ K[:L - 1 + i, 0].T / 8
+        p = torch.softmax(z, -1)
+        w, cc = p * s[:L - 1 + i], codes[:L - 1 + i]
+        ref = w @ cc
+        tol = (2.0 ** -10 * (w @ cc.abs()) + 2.0 ** -25 * w.amax(-1, keepdim=True) * cc.abs().sum(0) +
+               2.0 ** -11 * ref.abs() + 2.0 ** -25)
+        assert ref.abs().max() < 6e4
+        far_off = ((out[0, i].cpu().double() - ref).abs() - tol).max().item()
+        assert far_off <= 0, far_off
