@@ -1,7 +1,8 @@
 // Combine of attention over a block-scaled cache: merges the FP32 partial
 // states of the units that several CTAs of the split kernel shared,
 //     M = max_p m_p,  w_p = 2^(m_p - M),  out = sum_p w_p O_p / sum_p w_p l_p
-// over the parts with l_p > 0, in a fixed order, rounded once to FP16 (the
+// over the parts with l_p > 0 (a NaN counts, and makes the row NaN: its query or
+// its scores held one), in a fixed order, rounded once to FP16 (the
 // block scales are in O and l already), and writes zeros to padding rows,
 // sequences without tokens, rows without a visible key and units with an
 // invalid part (l < 0).  Units finished in one CTA (parts = -1) are left.
@@ -36,7 +37,7 @@ __device__ __forceinline__ int64_t slot_of(const SegParams &p, int first, int k)
 }
 
 __device__ __forceinline__ uint2 half4(float4 a, float l, bool ok) {
-  if (!ok || !(l > 0.f)) return make_uint2(0u, 0u);
+  if (!ok || l <= 0.f) return make_uint2(0u, 0u);
   return make_uint2(pack_half2(__fdiv_rn(a.x, l), __fdiv_rn(a.y, l)),
                     pack_half2(__fdiv_rn(a.z, l), __fdiv_rn(a.w, l)));
 }
@@ -95,9 +96,9 @@ __global__ void __launch_bounds__(kRowThreads) seg_combine_rows(const SegParams 
   __syncthreads();
   float lam = 0.f;
   for (int x = tid; x < nP; x += kRowThreads) {
-    const float l = ws[x], w = l > 0.f ? exp2f(wm[x] - M) : 0.f;
+    const float l = ws[x], w = l <= 0.f ? 0.f : exp2f(wm[x] - M);
     wm[x] = w;
-    lam += w * l;
+    lam += w * l;  // (NaN if l is)
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) lam += __shfl_xor_sync(0xffffffffu, lam, off);
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(kWarpThreads) seg_combine_warps(const SegParam
     }
 #pragma unroll
     for (int k = 0; k < NPL; ++k) {
-      if (m[k].y > 0.f) {
+      if (!(m[k].y <= 0.f)) {
         const float w = exp2f(m[k].x - M);
         lam += w * m[k].y;
         acc.x += w * v[k].x;

@@ -1241,7 +1241,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
                   const float l = linv_s[row];
                   if (at >= 0)
                     static_cast<__half *>(p.out)[at + d] =
-                        __float2half_rn(l > 0.f ? __fdividef(__uint_as_float(r[e]), l) : 0.f);
+                        __float2half_rn(l <= 0.f ? 0.f : __fdividef(__uint_as_float(r[e]), l));  // (NaN if l is)
                 }
               }
             }

@@ -169,3 +169,43 @@ def test_small_scales_beside_a_large_one_with_zero_codes(L, sparse_call, far):
         assert ref.abs().max() < 6e4
         far_off = ((out[0, i].cpu().double() - ref).abs() - tol).max().item()
         assert far_off <= 0, far_off
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("lens,Q,G,Hkv,D,num_sms", [
+    ([(300, 3), (90, 2)], 3, 4, 2, 128, 1),                    # units finished by their CTA
+    ([(5000, 3)], 3, 4, 2, 64, 0),                             # a part per SM, combined by rows
+    ([(4000, 3)] + [(1500, 2)] * 5, 3, 2, 2, 128, 0),          # combined by warps
+    ([(2000, 16)], 16, 6, 1, 256, 0),                          # two row groups
+])
+def test_a_query_with_a_nan_gives_a_row_of_nan(lens, Q, G, Hkv, D, num_sms, value):
+    """And all others keep their values; in the dense and in the sparse form."""
+    c = Cache(lens, Hkv, D, 32, 16, seed=35)
+    q = queries(c, Q, G)
+    odd = [(0, 0, 0), (0, Q - 1, G * Hkv - 1), (len(lens) - 1, 1, G)] if Hkv > 1 else [(0, 0, 0), (0, 15, 5)]
+    for k, (b, i, h) in enumerate(odd):
+        q[b, i, h, 7 + 20 * k] = value
+    n_blk = -(-max(L for L, _ in lens) // 16)
+    ids = torch.arange(n_blk, dtype=torch.int32).expand(len(lens), Q, Hkv, n_blk).contiguous()
+    k, v = c.device()
+    qd, bt, seq, sc, idd = dev(q, c.table, c.seq, c.scales, ids)
+    clean = q.clone()
+    for b, i, h in odd:
+        clean[b, i, h] = 0
+    ref, tol = reference(c, clean)
+    cap, B, Hq = c.table.shape[1] * 32, len(lens), G * Hkv
+    for sp in (False, True):
+        out = torch.zeros_like(qd)
+        n = (vae4.sparse_workspace_bytes(B, Hq, Hkv, Q, D, cap, 16, n_blk, num_sms) if sp else
+             vae4.block_scaled_workspace_bytes(B, Hq, Hkv, Q, D, cap, num_sms))
+        ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+        if sp:
+            vae4.verify_attn_e4m3_sparse(qd, k, v, bt, seq, sc, idd, out, ws, num_sms=num_sms)
+        else:
+            vae4.verify_attn_e4m3_block_scaled(qd, k, v, bt, seq, sc, out, ws, num_sms=num_sms)
+        assert vae4.read_status(ws) == 0
+        got = out.cpu()
+        for b, i, h in odd:
+            assert got[b, i, h].isnan().all(), (sp, b, i, h)
+            got[b, i, h] = ref[b, i, h].half()
+        check(got, ref, tol)
