@@ -4,7 +4,8 @@
 //     u[g] = sum_d max(q_d, 0) hi_d + min(q_d, 0) lo_d
 //     score = softmax_scale * s_K[j] * max_g u[g]
 // FP32 sums of exact FP16 x FP8 products.  Blocks that query i does not see
-// (their first token lies past its position) score -inf.
+// (their first token lies past its position) score -inf; a NaN or an infinite
+// query gives what the sums give (NaN, mostly).
 //
 // u is a matrix product over 2 D channels, [hi | lo] of 16 blocks (rows of A)
 // times [max(q, 0) | min(q, 0)] of the group's rows (columns of B): warp-level
@@ -39,6 +40,13 @@ constexpr int kScoreWarps = kScoreThreads / 32;
 constexpr int b_stride(int D) { return D + 8; }
 constexpr int score_smem(int D, int NT) {
   return 2 * NT * 8 * b_stride(D) * 2 + kScoreWarps * 16 * (NT * 8 + 1) * 4;
+}
+
+// the larger of two values; NaN if one is
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(d) : "f"(a), "f"(b));
+  return d;
 }
 
 template <int D, int NT, bool E5M2>
@@ -174,7 +182,7 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Score
     const int jo = jj + (lane & 15);
     for (int i = lane >> 4; i < ni; i += 2) {  // 16 blocks of two queries at a time
       float best = ninf;
-      for (int k = 0; k < p.G; ++k) best = fmaxf(best, us[(lane & 15) * RS + i * p.G + k]);
+      for (int k = 0; k < p.G; ++k) best = max_nan(best, us[(lane & 15) * RS + i * p.G + k]);
       if (jo < nblk) {
         const bool seen = (int64_t)jo * p.blk <= L - n + i0 + i;
         p.scores[(int64_t)b * p.o_sb + (int64_t)(i0 + i) * p.o_si + (int64_t)h * p.o_sh + jo] =

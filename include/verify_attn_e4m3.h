@@ -545,7 +545,8 @@ int verify_attn_e4m3_block_scaled(const vae4_tensor *q, const vae4_tensor *k_cac
  *     score[b][i][h][j] = softmax_scale * s_K[j] *
  *         max_g sum_d (max(q_d, 0) dec(hi_d) + min(q_d, 0) dec(lo_d))
  *
- * in FP32, -inf for blocks that query i does not see (j * S > L - q + i).
+ * in FP32 (NaN if a sum is NaN), -inf for blocks that query i does not see
+ * (j * S > L - q + i).
  *  q           F16 [B][Qmax][Hq][D] as for verify_attn_e4m3 (Qmax <= 16, at
  *              most 96 rows per KV head).
  *  scores      F32 [B][Qmax][Hkv][columns], stride[3] == 1; columns >=

@@ -209,3 +209,21 @@ def test_a_query_with_a_nan_gives_a_row_of_nan(lens, Q, G, Hkv, D, num_sms, valu
             assert got[b, i, h].isnan().all(), (sp, b, i, h)
             got[b, i, h] = ref[b, i, h].half()
         check(got, ref, tol)
+
+
+@pytest.mark.parametrize("Q,G,head", [(1, 4, 0), (3, 6, 5), (8, 12, 3), (2, 1, 0)])
+def test_scores_of_a_query_with_a_nan_are_nan(Q, G, head):
+    """In whichever head of the group it is; other queries and KV heads keep
+    their scores, and blocks that the query does not see score -inf."""
+    c = Cache([(400, Q), (50, 1)], 2, 64, 32, 16, seed=36)
+    q, bd = queries(c, Q, G), bounds_of(c)
+    qd, bdd, bt, seq, sc = dev(q, bd, c.table, c.seq, c.scales)
+    scores = torch.full((2, 2, Q, 2, 25), 5.0, device="cuda")
+    vae4.verify_attn_e4m3_block_scores(qd, bdd, bt, seq, sc, scores[0], block_tokens=16)
+    qd[0, Q - 1, G + head, 9] = float("nan")
+    vae4.verify_attn_e4m3_block_scores(qd, bdd, bt, seq, sc, scores[1], block_tokens=16)
+    clean, got = scores.cpu()
+    seen = (400 - 1) // 16 + 1
+    assert got[0, Q - 1, 1, :seen].isnan().all()
+    got[0, Q - 1, 1, :seen] = clean[0, Q - 1, 1, :seen]
+    assert torch.equal(got, clean)
