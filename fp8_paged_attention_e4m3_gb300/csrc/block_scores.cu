@@ -5,7 +5,8 @@
 //     score = softmax_scale * s_K[j] * max_g u[g]
 // FP32 sums of exact FP16 x FP8 products.  Blocks that query i does not see
 // (their first token lies past its position) score -inf; a NaN or an infinite
-// query gives what the sums give (NaN, mostly).
+// query gives what the sums give (NaN, mostly).  A block with an invalid page or
+// scale scores -inf and is reported.
 //
 // u is a matrix product over 2 D channels, [hi | lo] of 16 blocks (rows of A)
 // times [max(q, 0) | min(q, 0)] of the group's rows (columns of B): warp-level
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Score
     if (ok) {
       const int sub = j % p.nb;
       off = (int64_t)phys * p.b_page + (int64_t)h * p.b_head + (int64_t)sub * p.b_blk;
-      x.s = __ldg(p.scales + (int64_t)phys * p.s_page + (int64_t)h * p.s_head + sub) * p.sm_scale;
+      x.s = __ldg(p.scales + (int64_t)phys * p.s_page + (int64_t)h * p.s_head + sub);
     }
     phys = page_of(jj + step);  // in flight with this step's bounds
     x.okm = __ballot_sync(0xffffffffu, ok);
@@ -177,8 +178,11 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Score
       us[(g + 8) * RS + 8 * k + 2 * t + 1] = acc[k][3];
     }
     __syncwarp();
-    const float sj = __shfl_sync(0xffffffffu, x.s, lane & 15);
-    const bool live = (x.okm >> (lane & 15)) & 1u;
+    // (the scale is looked at here, so that the bounds do not wait for it)
+    const float s = __shfl_sync(0xffffffffu, x.s, lane & 15), sj = s * p.sm_scale;
+    const bool page_ok = (x.okm >> (lane & 15)) & 1u;
+    const bool live = page_ok && s >= kMinScale && s <= kMaxScale;
+    if (page_ok && !live && lane < 16 && p.status) atomicOr(p.status, VAE4_STATUS_BAD_SCALE);
     const int jo = jj + (lane & 15);
     for (int i = lane >> 4; i < ni; i += 2) {  // 16 blocks of two queries at a time
       float best = ninf;

@@ -556,7 +556,8 @@ int verify_attn_e4m3_block_scaled(const vae4_tensor *q, const vae4_tensor *k_cac
  *  block_tokens S; page = S * k_bounds->shape[2].
  *  softmax_scale 0 -> 1/sqrt(D).
  *  dev_status, flags as for verify_attn_e4m3_append.
- * A block with an invalid page id scores -inf (BAD_BLOCK).
+ * A block with an invalid page id (BAD_BLOCK) or K scale (BAD_SCALE) scores
+ * -inf.
  */
 int verify_attn_e4m3_block_scores(const vae4_tensor *q, const vae4_tensor *k_bounds,
                                   const vae4_tensor *block_table, const vae4_tensor *seq_lens,

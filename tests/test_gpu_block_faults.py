@@ -227,3 +227,25 @@ def test_scores_of_a_query_with_a_nan_are_nan(Q, G, head):
     assert got[0, Q - 1, 1, :seen].isnan().all()
     got[0, Q - 1, 1, :seen] = clean[0, Q - 1, 1, :seen]
     assert torch.equal(got, clean)
+
+
+@pytest.mark.parametrize("bad", [0.0, -1.0, float("nan"), float("inf"), 2.0 ** 41, 2.0 ** -41])
+def test_scores_report_invalid_scales(bad):
+    """A K scale outside 2^-40 .. 2^40: -inf for its block and head, and the
+    status bit; the limits themselves, V's scales and those of blocks without
+    tokens do no harm."""
+    c = Cache([(230, 2), (40, 1)], 2, 64, 32, 16, seed=37)
+    q, bd = queries(c, 2, 3), bounds_of(c)
+    qd, bdd, bt, seq, sc = dev(q, bd, c.table, c.seq, c.scales)
+    sc[int(c.table[0, 2]), 0, 0, 0], sc[int(c.table[0, 3]), 0, 0, 0] = 2.0 ** 40, 2.0 ** -40
+    sc[int(c.table[0, 4]), 1] = bad
+    scores = torch.full((2, 2, 2, 2, 15), 5.0, device="cuda")
+    status = torch.zeros(2, dtype=torch.int32, device="cuda")
+    vae4.verify_attn_e4m3_block_scores(qd, bdd, bt, seq, sc, scores[0], block_tokens=16, status=status[:1])
+    sc[int(c.table[0, 1]), 0, 1, 1] = bad  # block 3 of head 1
+    vae4.verify_attn_e4m3_block_scores(qd, bdd, bt, seq, sc, scores[1], block_tokens=16, status=status[1:])
+    clean, got = scores.cpu()
+    assert status.tolist() == [0, vae4.STATUS_BAD_SCALE]
+    assert (got[0, :, 1, 3] == -math.inf).all() and clean[0, :, 1, 3].isfinite().all()
+    got[0, :, 1, 3] = clean[0, :, 1, 3]
+    assert torch.equal(got, clean)
