@@ -426,7 +426,8 @@ def alloc_k_bounds(n_pages, Hkv, page, block_tokens, D, device=None):
 # What the calls below need of torch, looked up on first use (torch is imported
 # lazily): these calls run once per layer and step, so their host time counts.
 _torch = None
-_CODES = {}      # torch dtype -> vae4_dtype
+_CODES = {}      # torch dtype -> vae4_dtype, where the cache's bytes are E4M3
+_CODES_E5M2 = {}  # and where they are E5M2
 _raw_stream = None
 _device = None
 # a vae4_tensor of n dimensions: data, dtype | ndim << 32, shape[5], stride[5]
@@ -436,38 +437,42 @@ _PACK = [struct.Struct(f"=2q{n}q{40 - 8 * n}x{n}q{40 - 8 * n}x").pack for n in r
 def _setup():
     global _torch, _raw_stream, _device
     import torch
-    _CODES.update({torch.uint8: VAE4_U8, torch.int32: VAE4_I32, torch.float16: VAE4_F16,
-                   torch.float32: VAE4_F32, torch.bfloat16: VAE4_BF16,
-                   torch.float8_e4m3fn: VAE4_U8, torch.float8_e5m2: VAE4_U8})
+    for codes, fp8 in ((_CODES, torch.float8_e4m3fn), (_CODES_E5M2, torch.float8_e5m2)):
+        codes.update({torch.uint8: VAE4_U8, torch.int32: VAE4_I32, torch.float16: VAE4_F16,
+                      torch.float32: VAE4_F32, torch.bfloat16: VAE4_BF16, fp8: VAE4_U8})
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda dev: torch.cuda.current_stream(dev).cuda_stream)
     _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _torch = torch
 
 
-def _call(name, tensors, rest, stream, opt=None):
+def _call(name, tensors, rest, stream, flags=0, opt=None):
     """lib.verify_attn_e4m3_<name>(tensors..., rest..., stream[, opt]), the
     tensors (None: a null pointer) as packed vae4_tensor structures.  Every
-    tensor has to be on the current device."""
+    tensor has to be on the current device, and one of an FP8 type of the
+    format that ``flags`` gives the cache (uint8 is either)."""
     if _torch is None:
         _setup()
-    args, dev = [], -1
+    codes = _CODES_E5M2 if flags & FLAG_KV_E5M2 else _CODES
+    args, devs = [], set()
     for t in tensors:
         if t is None:
             args.append(None)
             continue
-        d = t.get_device()
-        if d < 0 or (d != dev and dev >= 0):
-            raise ValueError("tensors have to be on one CUDA device")
-        dev = d
-        code = _CODES.get(t.dtype)
+        code = codes.get(t.dtype)
         if code is None:
+            if t.dtype in _CODES or t.dtype in _CODES_E5M2:
+                raise TypeError(f"{t.dtype} beside flags of the other FP8 format")
             raise TypeError(f"unsupported dtype {t.dtype}")
+        devs.add(t.get_device())
         shape = t.shape
         n = len(shape)
         if n > 5:
             raise ValueError("at most 5 dimensions")
         args.append(_PACK[n](t.data_ptr(), code | n << 32, *shape, *t.stride()))
+    dev = devs.pop() if len(devs) == 1 else -1
+    if dev < 0:
+        raise ValueError("tensors have to be on one CUDA device")
     if dev != _device():
         raise ValueError("tensors have to be on the current device")
     st = _raw_stream(dev) if stream is None else _stream_handle(stream)
@@ -494,7 +499,7 @@ def verify_attn_e4m3_append(k_new, v_new, k_cache, v_cache, block_table, seq_len
     element receives the status bits."""
     _call("verify_attn_e4m3_append", (k_new, v_new, k_cache, v_cache, block_table, seq_lens,
                                       block_scales, k_bounds),
-          (_status_pointer(status), flags), stream)
+          (_status_pointer(status), flags), stream, flags)
 
 
 def verify_attn_e4m3_block_scaled(q, k_cache, v_cache, block_table, seq_lens, block_scales, out,
@@ -506,7 +511,7 @@ def verify_attn_e4m3_block_scaled(q, k_cache, v_cache, block_table, seq_lens, bl
     as verify_attn_e4m3_kv.  ``workspace`` from alloc_workspace."""
     opt = Options(softmax_scale, 0, max_seq_len, num_sms, flags, 0)
     _call("verify_attn_e4m3_block_scaled", (q, k_cache, v_cache, block_table, seq_lens,
-                                            block_scales, out, workspace), (), stream, opt)
+                                            block_scales, out, workspace), (), stream, flags, opt)
     return out
 
 
@@ -518,7 +523,7 @@ def verify_attn_e4m3_sparse(q, k_cache, v_cache, block_table, seq_lens, block_sc
     ``workspace`` from alloc_sparse_workspace."""
     opt = Options(softmax_scale, 0, max_seq_len, num_sms, flags, 0)
     _call("verify_attn_e4m3_sparse", (q, k_cache, v_cache, block_table, seq_lens, block_scales,
-                                      block_ids, out, workspace), (), stream, opt)
+                                      block_ids, out, workspace), (), stream, flags, opt)
     return out
 
 
@@ -529,7 +534,7 @@ def verify_attn_e4m3_block_scores(q, k_bounds, block_table, seq_lens, block_scal
     upper bound of the group's logits in the block; see the header."""
     _call("verify_attn_e4m3_block_scores", (q, k_bounds, block_table, seq_lens, block_scales,
                                             scores),
-          (block_tokens, softmax_scale, _status_pointer(status), flags), stream)
+          (block_tokens, softmax_scale, _status_pointer(status), flags), stream, flags)
     return scores
 
 
