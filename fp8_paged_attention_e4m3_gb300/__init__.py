@@ -485,9 +485,11 @@ def _call(name, tensors, rest, stream, flags=0, opt=None):
 def _status_pointer(status):
     if status is None:
         return None
-    import torch
-    if status.dtype != torch.int32 or status.numel() < 1 or not status.is_cuda:
-        raise ValueError("status: an int32 tensor on the device")
+    if _torch is None:
+        _setup()
+    dev = status.get_device()
+    if status.dtype != _torch.int32 or status.numel() < 1 or dev < 0 or dev != _device():
+        raise ValueError("status: an int32 tensor on the current device")
     return status.data_ptr()
 
 

@@ -41,3 +41,52 @@ def test_fp8_types_have_to_agree_with_the_flags(name):
                         (torch.uint8, vae4.FLAG_KV_E5M2)):
         with pytest.raises(ValueError, match="device"):
             CALLS[name](arguments(kind), flags=flags)
+
+
+class OnDevice:
+    """What the binding asks of a CUDA tensor, on a device that need not exist."""
+
+    def __init__(self, t, device):
+        self.t, self.device = t, device
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def get_device(self):
+        return self.device
+
+    @property
+    def is_cuda(self):
+        return self.device >= 0
+
+    def data_ptr(self):
+        return 0x100000
+
+
+@pytest.mark.parametrize("name", ["append", "scores", "select"])
+def test_status_has_to_be_on_the_current_device(name, monkeypatch):
+    """Device 0 is current: a status word on device 1 or on the host is refused
+    before the library is called; one on device 0 reaches it."""
+    a = {k: OnDevice(t, 0) for k, t in arguments(torch.uint8).items()}
+    calls = dict(CALLS, select=lambda a, **kw: vae4.verify_attn_e4m3_select_blocks(
+        a["scores"], a["seq"], a["ids"], block_tokens=16, **kw))
+    reached = []
+
+    class Library:
+        def __getattr__(self, fn):
+            return lambda *args: reached.append(fn) or 0
+
+    with pytest.raises(ValueError):  # (looks up what it needs of torch)
+        vae4.verify_attn_e4m3_select_blocks(*[arguments(torch.uint8)[k] for k in ("scores", "seq", "ids")],
+                                            block_tokens=16)
+    monkeypatch.setattr(vae4, "_lib", Library())
+    monkeypatch.setattr(vae4, "_device", lambda: 0)
+    monkeypatch.setattr(vae4, "_raw_stream", lambda dev: 0)
+    word = torch.zeros(1, dtype=torch.int32)
+    for wrong in (OnDevice(word, 1), word, OnDevice(word.float(), 0), OnDevice(word[:0], 0)):
+        with pytest.raises(ValueError, match="status"):
+            calls[name](a, status=wrong)
+    assert not reached
+    for right in (None, OnDevice(word, 0)):
+        calls[name](a, status=right)
+    assert len(reached) == 2
