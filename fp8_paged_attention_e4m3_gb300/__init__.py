@@ -387,10 +387,15 @@ decode_table = verify_attn_e4m3_decode_table
 
 def alloc_workspace(B, Hq, Hkv, Qmax, D, max_seq_len, partition_tokens=0, device=None):
     """A zeroed workspace of the right size (torch allocation, 256-B aligned),
-    for the head-scaled calls and verify_attn_e4m3_block_scaled alike."""
+    for the head-scaled calls and verify_attn_e4m3_block_scaled alike (for the
+    head-scaled calls alone where the other refuses the batch as too large)."""
     import torch
-    n = max(workspace_bytes(B, Hq, Hkv, Qmax, D, max_seq_len, partition_tokens),
-            block_scaled_workspace_bytes(B, Hq, Hkv, Qmax, D, max_seq_len))
+    n = workspace_bytes(B, Hq, Hkv, Qmax, D, max_seq_len, partition_tokens)
+    try:
+        n = max(n, block_scaled_workspace_bytes(B, Hq, Hkv, Qmax, D, max_seq_len))
+    except Vae4Error as e:
+        if ERRORS.get(e.code) != "VAE4_ERR_SHAPE":
+            raise
     return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
 
 

@@ -90,3 +90,27 @@ def test_status_has_to_be_on_the_current_device(name, monkeypatch):
     for right in (None, OnDevice(word, 0)):
         calls[name](a, status=right)
     assert len(reached) == 2
+
+
+@pytest.mark.parametrize("shape,both", [
+    ((1024, 8, 8, 1, 128, 1 << 23), False),
+    ((8192, 64, 8, 1, 128, 1 << 20), False),
+    ((65535, 8, 8, 1, 128, 1 << 17), False),
+    ((2, 12, 2, 8, 128, 4096), True),
+])
+def test_a_workspace_for_every_batch_of_the_head_scaled_calls(shape, both, monkeypatch):
+    """Batches past the block-scaled plan's line of 2^30 places get the
+    head-scaled calls' workspace; others one that serves both."""
+    head, blocked = vae4.workspace_bytes, vae4.block_scaled_workspace_bytes
+    monkeypatch.setattr(vae4, "workspace_bytes", lambda *a: head(*a, num_sms=152))
+    monkeypatch.setattr(vae4, "block_scaled_workspace_bytes", lambda *a: blocked(*a, num_sms=152))
+    monkeypatch.setattr(torch, "zeros", lambda n, **kw: n)
+    n = vae4.alloc_workspace(*shape, device="cpu")
+    if both:
+        assert n == max(head(*shape, num_sms=152), blocked(*shape, num_sms=152))
+    else:
+        with pytest.raises(vae4.Vae4Error):
+            blocked(*shape, num_sms=152)
+        assert n == head(*shape, num_sms=152)
+    with pytest.raises(vae4.Vae4Error):  # what no call takes
+        vae4.alloc_workspace(1, 7, 2, 1, 128, 4096, device="cpu")
