@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Score
   auto query = [&](int x) -> uint4 {
     const int r = x / (D / 8), c = x - r * (D / 8), i = r / p.G;
     if (x >= kChunks || r >= p.qn * p.G || i0 + i >= p.Qmax) return make_uint4(0u, 0u, 0u, 0u);
-    return __ldg(reinterpret_cast<const uint4 *>(static_cast<const __half *>(p.q) + (int64_t)b * p.q_sb +
+    return load_dep(reinterpret_cast<const uint4 *>(static_cast<const __half *>(p.q) + (int64_t)b * p.q_sb +
                                                  (int64_t)(i0 + i) * p.q_si +
                                                  (int64_t)(h * p.G + r - i * p.G) * p.q_sh + 8 * c));
   };
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Score
   int j0 = (blockIdx.x * kScoreWarps + warp) * 16;
   int phys = 0;
   if (const int lp = (j0 + lane) / p.nb; lane < 16 && lp < p.max_pages)
-    phys = __ldg(p.bt + (int64_t)b * p.bt_sb + lp);
+    phys = load_dep(p.bt + (int64_t)b * p.bt_sb + lp);
   const int L = p.seq[(int64_t)b * p.seq_sb];
   const int n = p.seq_has_qlen ? p.seq[(int64_t)b * p.seq_sb + 1] : p.Qmax;
   const bool long_l = L > 0 && (L - 1) / p.blk >= p.cols;  // more blocks than columns
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Score
   // the page and scale of block j0 + lane (lanes 0 .. 15)
   auto page_of = [&](int jj) -> int {
     const int j = jj + lane;
-    return lane < 16 && j < nblk ? __ldg(p.bt + (int64_t)b * p.bt_sb + j / p.nb) : 0;
+    return lane < 16 && j < nblk ? load_dep(p.bt + (int64_t)b * p.bt_sb + j / p.nb) : 0;
   };
   const int ni = min(n - i0, p.qn);
   if (ni <= 0) return;
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Score
     if (ok) {
       const int sub = j % p.nb;
       off = (int64_t)phys * p.b_page + (int64_t)h * p.b_head + (int64_t)sub * p.b_blk;
-      x.s = __ldg(p.scales + (int64_t)phys * p.s_page + (int64_t)h * p.s_head + sub);
+      x.s = load_dep(p.scales + (int64_t)phys * p.s_page + (int64_t)h * p.s_head + sub);
     }
     phys = page_of(jj + step);  // in flight with this step's bounds
     x.okm = __ballot_sync(0xffffffffu, ok);
@@ -128,9 +128,9 @@ __global__ void __launch_bounds__(kScoreThreads) block_scores_kernel(const Score
       const uint8_t *base = p.bounds + o + 16 * t;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        x.a[0][r][c] = live ? __ldg(reinterpret_cast<const uint4 *>(base + p.b_mm + 64 * c))
+        x.a[0][r][c] = live ? load_dep(reinterpret_cast<const uint4 *>(base + p.b_mm + 64 * c))
                             : make_uint4(0u, 0u, 0u, 0u);
-        x.a[1][r][c] = live ? __ldg(reinterpret_cast<const uint4 *>(base + 64 * c))
+        x.a[1][r][c] = live ? load_dep(reinterpret_cast<const uint4 *>(base + 64 * c))
                             : make_uint4(0u, 0u, 0u, 0u);
       }
     }

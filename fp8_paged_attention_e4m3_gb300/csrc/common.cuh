@@ -165,9 +165,16 @@ __device__ __forceinline__ int div16(int key, unsigned long long m) {
 // await_previous(), which every thread calls and which returns when that kernel
 // has ended; the one after it may then be placed early in the same way (not
 // before: it may read inputs, which earlier kernels wrote, ahead of its wait).
+// What an earlier kernel may have written is read by load_dep, never through the
+// read-only path (__ldg): that one is for data that nobody writes as long as the
+// kernel is there, and a dependent is there while its inputs are being written.
 __device__ __forceinline__ void await_previous() {
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+}
+template <class T>
+__device__ __forceinline__ T load_dep(const T *p) {
+  return *p;
 }
 template <class P>
 cudaError_t launch_dependent(void (*kernel)(P), dim3 grid, int threads, size_t smem,

@@ -600,10 +600,10 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
         raw = make_int2(-1, 0);
         if (key >= 0) {
           if constexpr (LISTED)
-            raw = __ldg(reinterpret_cast<const int2 *>(
+            raw = load_dep(reinterpret_cast<const int2 *>(
                 p.list + (int64_t)seg_s[it.x].b * p.list_cap + div16(key, unit_m)));
           else
-            raw.x = __ldg(p.bt + (int64_t)seg_s[it.x].b * p.bt_sb + div16(key, unit_m));
+            raw.x = load_dep(p.bt + (int64_t)seg_s[it.x].b * p.bt_sb + div16(key, unit_m));
         }
       };
       int page = 0, tok = 0;  // of the lane's copy; the page past the last one reads as zeros
@@ -695,7 +695,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
       auto load_page = [&](int2 it) -> int {
         if constexpr (LISTED) return 0;
         const int key = key_of(it);
-        return key >= 0 ? __ldg(p.bt + (int64_t)seg_s[it.x].b * p.bt_sb + div16(key, p.page_m)) : -1;
+        return key >= 0 ? load_dep(p.bt + (int64_t)seg_s[it.x].b * p.bt_sb + div16(key, p.page_m)) : -1;
       };
       float4 f = make_float4(0.f, 0.f, 1.f, 0.f);  // (s_K, s_V); listed: the entry's
       int2 e = make_int2(0, 0);                    // listed: first token, mask
@@ -707,9 +707,9 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
           if (live) {
             const int x = div16(key, p.blk_m);
             const BlockEntry *en = p.list + (int64_t)seg_s[it.x].b * p.list_cap + x;
-            e = __ldg(reinterpret_cast<const int2 *>(&en->tok0));
+            e = load_dep(reinterpret_cast<const int2 *>(&en->tok0));
             e.x += key - x * p.blk;
-            f = __ldg(reinterpret_cast<const float4 *>(&en->alpha));
+            f = load_dep(reinterpret_cast<const float4 *>(&en->alpha));
           }
         } else {
           live = live && page >= 0 && page < p.n_pages;
@@ -717,8 +717,8 @@ __global__ void __launch_bounds__(Cfg<D, N>::NTHREADS, 1)
             const float *sp = p.scales + (int64_t)page * p.s_page +
                               (int64_t)(seg_s[it.x].h_rg & 0xFFFF) * p.s_head +
                               (div16(key, p.blk_m) - div16(key, p.page_m) * p.page_blocks);
-            f.x = __ldg(sp);
-            f.y = __ldg(sp + p.s_kv);
+            f.x = load_dep(sp);
+            f.y = load_dep(sp + p.s_kv);
           }
         }
       };

@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_blocks_kernel(const Se
   if constexpr (kKeys > 0) {
 #pragma unroll
     for (int e = 0; e < kKeys; ++e)  // all under way together
-      key[e] = __float_as_uint(__ldg(sc + min(x0 + 32 * e + lane, v - 1)));
+      key[e] = __float_as_uint(load_dep(sc + min(x0 + 32 * e + lane, v - 1)));
     if (x0 >= c0 && x0 + 32 * kKeys <= min(x1, c1)) {  // candidates alone
 #pragma unroll
       for (int e = 0; e < kKeys; ++e) key[e] = score_key(__uint_as_float(key[e]));
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_blocks_kernel(const Se
         for (int k = 0; k < 4; ++k) f(x0 + 32 * (e + k) + lane, key[e + k]);
       }
     } else {
-      for (int x = x0; x < x1; x += 32) f(x + lane, key_of(x + lane, __ldg(sc + min(x + lane, v - 1))));
+      for (int x = x0; x < x1; x += 32) f(x + lane, key_of(x + lane, load_dep(sc + min(x + lane, v - 1))));
     }
   };
   uint32_t m = (uint32_t)(p.k - p.sink - p.local);  // how many of them (fewer than there are)

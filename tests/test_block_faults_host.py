@@ -1,5 +1,8 @@
 """The binding of the block-scaled cache's calls on the host: what it has to
 refuse, and what it must not.  No compute call is made here."""
+import glob
+import os
+
 import pytest
 import torch
 
@@ -114,3 +117,16 @@ def test_a_workspace_for_every_batch_of_the_head_scaled_calls(shape, both, monke
         assert n == head(*shape, num_sms=152)
     with pytest.raises(vae4.Vae4Error):  # what no call takes
         vae4.alloc_workspace(1, 7, 2, 1, 128, 4096, device="cpu")
+
+
+def test_dependent_kernels_read_their_inputs_coherently():
+    """A kernel launched as a programmatic dependent is there while the kernels
+    before it write its inputs: the read-only path, which is not coherent with
+    such writes, is not for it."""
+    csrc = os.path.join(os.path.dirname(vae4.__file__), "csrc")
+    files = [f for name in ("append.cu", "block_*.cu", "select_blocks.cu", "seg_*.cu*")
+             for f in glob.glob(os.path.join(csrc, name))]
+    assert len(files) >= 9
+    for f in files:
+        text = open(f).read()
+        assert "__ldg(" not in text and "ld.global.nc" not in text, f
