@@ -71,7 +71,7 @@ int64_t attention_bytes(int B, int Hq, int Hkv, int Qmax, int D, int max_seq_len
     return VAE4_ERR_SHAPE;
   if (D != 64 && D != 128 && D != 256) return VAE4_ERR_UNSUPPORTED;
   if (Hq % Hkv != 0) return VAE4_ERR_GQA;
-  const int rows = Qmax * (Hq / Hkv);
+  const int64_t rows = (int64_t)Qmax * (Hq / Hkv);
   if (align_up(rows, 16) > kMaxRowsPad) return VAE4_ERR_UNSUPPORTED;
   int sms = num_sms;
   if (sms < 0) return VAE4_ERR_SHAPE;

@@ -130,3 +130,12 @@ def test_dependent_kernels_read_their_inputs_coherently():
     for f in files:
         text = open(f).read()
         assert "__ldg(" not in text and "ld.global.nc" not in text, f
+
+
+def test_workspace_sizes_refuse_rows_past_32_bits():
+    """2^32 + 16 rows are not 16."""
+    for fn in (lambda *a: vae4.block_scaled_workspace_bytes(*a, 152),
+               lambda *a: vae4.sparse_workspace_bytes(*a, 16, 4, 152)):
+        with pytest.raises(vae4.Vae4Error, match="UNSUPPORTED"):
+            fn(1, (1 << 28) + 1, 1, 16, 64, 1000)
+        assert fn(1, 1, 1, 16, 64, 1000) > 0
