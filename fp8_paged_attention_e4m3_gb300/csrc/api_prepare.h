@@ -9,6 +9,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "block_params.h"
 #include "kernels.h"
 #include "params.h"
 #include "verify_attn_e4m3.h"

@@ -34,7 +34,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "common.cuh"
+#include "block_common.cuh"
 #include "kernels.h"
 #include "verify_attn_e4m3.h"
 

@@ -13,7 +13,7 @@
 #include <algorithm>
 #include <atomic>
 
-#include "common.cuh"
+#include "block_common.cuh"
 #include "kernels.h"
 #include "verify_attn_e4m3.h"
 

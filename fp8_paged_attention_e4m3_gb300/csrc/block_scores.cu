@@ -24,7 +24,7 @@
 // alone, 5.8 us.
 #include <algorithm>
 
-#include "common.cuh"
+#include "block_common.cuh"
 #include "kernels.h"
 #include "verify_attn_e4m3.h"
 

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stddef.h>
 
+#include "block_params.h"
 #include "params.h"
 
 namespace vae4 {

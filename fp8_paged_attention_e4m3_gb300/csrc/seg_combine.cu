@@ -14,7 +14,7 @@
 // (7.5 MB, in L2) take 4 us after the split kernel.
 #include <algorithm>
 
-#include "common.cuh"
+#include "block_common.cuh"
 #include "kernels.h"
 #include "verify_attn_e4m3.h"
 

@@ -81,10 +81,8 @@
 #include <atomic>
 #include <type_traits>
 
-#include "common.cuh"
+#include "block_common.cuh"
 #include "kernels.h"
-#include "params.h"
-#include "tc_ptx.cuh"
 #include "verify_attn_e4m3.h"
 
 namespace vae4 {

@@ -22,7 +22,7 @@
 // scan over the bins, next digit, each behind a barrier.  16 rows of 4096
 // blocks take 4.7 us, 256 rows of up to 16384 blocks 14.5 us (of which reading
 // the row is a third).
-#include "common.cuh"
+#include "block_common.cuh"
 #include "kernels.h"
 #include "verify_attn_e4m3.h"
 

@@ -82,19 +82,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
-// mbar_wait with everything but the first probe out of line: a kernel whose
-// warps run many different loops is bound by instruction fetches, and a wait
-// that is usually over should not take 40 instructions of each.
-static __device__ __noinline__ bool mbar_wait_more(uint32_t bar, uint32_t parity,
-                                                   volatile int *abort, long long limit) {
-  return mbar_wait(bar, parity, abort, limit);
-}
-__device__ __forceinline__ bool mbar_wait_brief(uint32_t bar, uint32_t parity, volatile int *abort,
-                                                long long limit) {
-  if (limit >= kMinWaitLimit && mbar_try_wait(bar, parity)) return true;
-  return mbar_wait_more(bar, parity, abort, limit);
-}
-
 // ------------------------------------------------------------------ TMA
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int x, int y,
                                             uint32_t bar) {
@@ -287,14 +274,6 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
-}
-// One lane of the (converged) warp, the same at every call.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(r));
-  return r != 0;
 }
 // Arrive on `bar` once every tcgen05 operation this thread issued so far is done.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {

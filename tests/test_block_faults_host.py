@@ -139,3 +139,15 @@ def test_workspace_sizes_refuse_rows_past_32_bits():
         with pytest.raises(vae4.Vae4Error, match="UNSUPPORTED"):
             fn(1, (1 << 28) + 1, 1, 16, 64, 1000)
         assert fn(1, 1, 1, 16, 64, 1000) > 0
+
+
+def test_profiled_sources_hold_the_head_scaled_kernels_alone():
+    """bench.py reports the head-scaled kernel's DRAM traffic while the sources
+    that were profiled are unchanged: what only the block-scaled kernels use
+    stays out of them, or a change there would void the record."""
+    import bench
+    for rel in bench.SPLIT_SOURCES:
+        text = open(os.path.join(bench.ROOT, rel)).read()
+        for name in ("SegParams", "AppendParams", "ScoreParams", "SelectParams", "ListParams",
+                     "launch_dependent(", "elect_one", "mbar_wait_brief"):
+            assert name not in text, (rel, name)
