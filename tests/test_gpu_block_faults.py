@@ -249,3 +249,101 @@ def test_scores_report_invalid_scales(bad):
     assert (got[0, :, 1, 3] == -math.inf).all() and clean[0, :, 1, 3].isfinite().all()
     got[0, :, 1, 3] = clean[0, :, 1, 3]
     assert torch.equal(got, clean)
+
+
+def one_token(B, H, G, D, seed):
+    """Sequences of one token each: whatever the scores, a row is its V."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    table = torch.randperm(B, generator=g, device="cuda").int().view(B, 1)
+    x = torch.randn(2, B, 1, H, D, generator=g, device="cuda").half()
+    q = torch.randn(B, 1, G * H, D, generator=g, device="cuda").half()
+    cache = [torch.full((B, 16, H, D), 0x7F, dtype=torch.uint8, device="cuda") for _ in (0, 1)]
+    return (table, x, q, cache, vae4.alloc_block_scales(B, H, 16, 16),
+            vae4.alloc_k_bounds(B, H, 16, 16, D), torch.ones(B, 2, dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("B,H,G", [(65535, 1, 1), (1, 32767, 2), (300, 200, 1), (2, 1, 96), (1, 3, 32)])
+def test_the_largest_grids(B, H, G):
+    """The most sequences and KV heads that the calls take, and the most heads
+    on one KV head: append, attention, scores, choice and sparse attention."""
+    D = 64
+    table, x, q, (kc, vc), sc, bd, seq = one_token(B, H, G, D, B + H)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    vae4.verify_attn_e4m3_append(x[0], x[1], kc, vc, table, seq, sc, k_bounds=bd, status=status)
+    pg = table[:, 0].long()
+    v = vc[pg, 0].view(torch.float8_e4m3fn).float() * sc[pg, 1, :, :1]        # [B][H][D]
+    k = kc[pg, 0].view(torch.float8_e4m3fn).float() * sc[pg, 0, :, :1]
+    for got, new in ((k, x[0]), (v, x[1])):  # a code is off by at most half a step: 2^-4, or 2^-10 s
+        new = new[:, 0].float()
+        assert ((got - new).abs() <= 2.0 ** -4 * new.abs() + 2.0 ** -10 * new.abs().amax(-1, keepdim=True) / 224).all()
+    want = v.half().repeat_interleave(G, 1)[:, None]
+    out, out2 = torch.zeros_like(q), torch.zeros_like(q)
+    scores = torch.zeros(B, 1, H, 1, device="cuda")
+    ids = torch.full((B, 1, H, 2), 7, dtype=torch.int32, device="cuda")
+    ws = vae4.alloc_workspace(B, G * H, H, 1, D, 16)
+    wl = vae4.alloc_sparse_workspace(B, G * H, H, 1, D, 16, 16, 2)
+    vae4.verify_attn_e4m3_block_scaled(q, kc, vc, table, seq, sc, out, ws)
+    vae4.verify_attn_e4m3_block_scores(q, bd, table, seq, sc, scores, block_tokens=16, status=status)
+    vae4.verify_attn_e4m3_select_blocks(scores, seq, ids, block_tokens=16, status=status)
+    vae4.verify_attn_e4m3_sparse(q, kc, vc, table, seq, sc, ids, out2, wl)
+    assert int(status) == 0 and vae4.read_status(ws) == 0 and vae4.read_status(wl) == 0
+    for o in (out, out2):  # one weight of 1 and one division: the rounding to FP16, and 2^-11 for the rest
+        assert ((o.float() - want.float()).abs() <= 2.0 ** -10 * want.float().abs() + 2.0 ** -24).all()
+    assert (ids[..., 0] == 0).all() and (ids[..., 1] == -1).all()
+    z = torch.einsum("bhgd,bhd->bhg", q[:, 0].double().view(B, H, G, D), k.double()).amax(-1) / 8
+    mags = torch.einsum("bhgd,bhd->bhg", q[:, 0].double().abs().view(B, H, G, D), k.double().abs()).amax(-1) / 8
+    assert ((scores[:, 0, :, 0].double() - z).abs() <= (2 * D + 4) * 2.0 ** -24 * mags).all()
+
+
+def test_lengths_without_q_and_strided_arguments():
+    """[B] lengths (q = Qmax for all) and rows that do not lie together: every
+    argument a view into a larger tensor, whose other elements stay as they are."""
+    B, Q, H, G, D, page, blk, cap = 3, 3, 2, 4, 128, 64, 16, 256
+    lens = [(150, Q), (3, Q), (77, Q)]
+    c = Cache(lens, H, D, page, blk, seed=38)
+    c.scales = torch.exp2(c.scales.log2().round())  # as earlier calls left them
+    g = torch.Generator().manual_seed(4)
+    q = queries(c, Q, G)
+    x = torch.randn(2, B, Q, H, D, generator=g).half()
+
+    def wide(t, extra):
+        big = torch.full([n + e for n, e in zip(t.shape, extra)], 9, dtype=t.dtype, device="cuda")
+        view = big[tuple(slice(0, n) for n in t.shape)]
+        view.copy_(t)
+        return big, view
+
+    results = []
+    for strided in (False, True):
+        e = (lambda *n: n) if strided else (lambda *n: [0] * len(n))
+        kc, vc = c.device()
+        seq = wide(torch.tensor(lens, dtype=torch.int32), (0, 1))[1][:, 0] if strided else c.seq[:, 0].contiguous().cuda()
+        table = wide(c.table, e(0, 3))[1]
+        sc = wide(c.scales, e(0, 1, 1, 0))[1]
+        bd = wide(bounds_of(c), e(0, 1, 0, 0, 0))[1]
+        qd, xk, xv = wide(q, e(1, 1, 1, 8))[1], wide(x[0], e(0, 2, 1, 16))[1], wide(x[1], e(1, 0, 3, 8))[1]
+        cols = cap // blk
+        sbig, scores = wide(torch.zeros(B, Q, H, cols), e(0, 1, 1, 5))
+        ibig, ids = wide(torch.zeros(B, Q, H, 4, dtype=torch.int32), e(1, 1, 1, 3))
+        obig, out = wide(torch.zeros_like(q), e(0, 1, 2, 8))
+        o2big, out2 = wide(torch.zeros_like(q), e(0, 0, 1, 8))
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        top = table.shape[1] * page
+        ws, wl = vae4.alloc_workspace(B, G * H, H, Q, D, top), vae4.alloc_sparse_workspace(B, G * H, H, Q, D, top, blk, 4)
+        vae4.verify_attn_e4m3_append(xk, xv, kc, vc, table, seq, sc, k_bounds=bd, status=status)
+        vae4.verify_attn_e4m3_block_scaled(qd, kc, vc, table, seq, sc, out, ws)
+        vae4.verify_attn_e4m3_block_scores(qd, bd, table, seq, sc, scores, block_tokens=blk, status=status)
+        vae4.verify_attn_e4m3_select_blocks(scores, seq, ids, block_tokens=blk, status=status)
+        vae4.verify_attn_e4m3_sparse(qd, kc, vc, table, seq, sc, ids, out2, wl)
+        assert int(status) == 0 and vae4.read_status(ws) == 0 and vae4.read_status(wl) == 0
+        results.append([kc, vc, sc.contiguous().view(torch.int32), bd, scores, ids, out, out2])
+        for big, view in ((sbig, scores), (ibig, ids), (obig, out), (o2big, out2)):
+            rest = big.clone()
+            rest[tuple(slice(0, n) for n in view.shape)] = 9
+            assert (rest == 9).all()
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    now = Cache(lens, H, D, page, blk, seed=38)
+    now.table, now.codes = c.table, [results[0][0].cpu(), results[0][1].cpu()]
+    now.scales = results[0][2].view(torch.float32).cpu()
+    check(results[0][6].cpu(), *reference(now, q))
+    check(results[0][7].cpu(), *reference(now, q, allowed=listed(now, results[0][5].cpu())))
