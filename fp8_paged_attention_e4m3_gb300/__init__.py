@@ -459,7 +459,7 @@ def _call(name, tensors, rest, stream, flags=0, opt=None):
     if _torch is None:
         _setup()
     codes = _CODES_E5M2 if flags & FLAG_KV_E5M2 else _CODES
-    args, devs = [], set()
+    args, dev = [], None
     for t in tensors:
         if t is None:
             args.append(None)
@@ -469,14 +469,15 @@ def _call(name, tensors, rest, stream, flags=0, opt=None):
             if t.dtype in _CODES or t.dtype in _CODES_E5M2:
                 raise TypeError(f"{t.dtype} beside flags of the other FP8 format")
             raise TypeError(f"unsupported dtype {t.dtype}")
-        devs.add(t.get_device())
+        d = t.get_device()
+        if d != dev:
+            dev = d if dev is None else -1
         shape = t.shape
         n = len(shape)
         if n > 5:
             raise ValueError("at most 5 dimensions")
         args.append(_PACK[n](t.data_ptr(), code | n << 32, *shape, *t.stride()))
-    dev = devs.pop() if len(devs) == 1 else -1
-    if dev < 0:
+    if dev is None or dev < 0:
         raise ValueError("tensors have to be on one CUDA device")
     if dev != _device():
         raise ValueError("tensors have to be on the current device")

@@ -16,18 +16,22 @@
 // can need; it is also the scale of an all-zero block, so that the next row
 // of the block is free to choose.
 //
-// One CTA per (block, head and K | V, sequence).  The rows and their codes cross
-// memory once each (a row's 16 bits in, 8 out): a thread asks for its rows before
-// it knows the page and keeps them in registers between the maximum and the
-// rounding, and tracks the bounds as 16-bit values, since rounding to a code is
-// monotonic.  2 x 16384 new tokens, 8 heads of 128: 202 MB in 33.8 us, 6.0 TB/s,
-// 0.88 of the copy peak.  What had kept it from that were instructions, not bytes:
-// 256 threads of four rows each took 43.6 us with 69 percent of the issue slots in
-// use, since what a warp does once per block (lengths, page, scale, bounds) then
-// costs as much as its rows; and 48 us before products with the inverse scale
-// stayed in 16 bits and divisions by the page and the block became products.  A
-// step of few rows is the launch and the chain lengths -> rows -> maximum ->
-// store: 2.1 to 3.1 us.
+// One CTA per (block, head and K | V, sequence).  A thread asks for its rows
+// before it knows the page and keeps up to eight of them in registers between the
+// maximum and the rounding, so that the rows of a block of up to 64 tokens at
+// D = 128 (128 at 64, 32 at 256) and their codes cross memory once each (a row's
+// 16 bits in, 8 out); it tracks the bounds as 16-bit values, since rounding to a
+// code is monotonic.  2 x 16384 new tokens, 8 heads of 128, blocks of 64: 202 MB
+// in 33.8 us, 6.0 TB/s, 0.88 of the copy peak.  What had kept it from that were
+// instructions, not bytes: 256 threads of four rows each took 43.6 us with 69
+// percent of the issue slots in use, since what a warp does once per block
+// (lengths, page, scale, bounds) then costs as much as its rows; and 48 us before
+// products with the inverse scale stayed in 16 bits and divisions by the page and
+// the block became products.  Rows past the eighth of a thread are loaded again
+// for the rounding: blocks of 128 tokens 48.6 us, of 256 59.9; of 64 at D = 256
+// 47.2 (of 32: 32.7), of 128 58.1, of 256 63.1, for as many bytes.  A step of few
+// rows is the launch and the chain lengths -> rows -> maximum -> store: 2.1 to
+// 3.1 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -430,8 +434,8 @@ cudaError_t launch_h(const AppendParams &p, bool bf16, bool e5m2, dim3 grid, cud
 template <int D>
 cudaError_t launch_d(const AppendParams &p, bool bf16, bool e5m2, dim3 grid, cudaStream_t st) {
   // Four rows per thread where they hold a block's new rows, else eight (a block
-  // of 64 tokens at D = 128 is then read once): 34.4 us for the prompts above,
-  // 46 with four; eight cost a step of few rows 0.2 us more
+  // of 64 tokens at D = 128 is then read once): 33.9 us for the prompts above,
+  // 45.5 with four; eight cost a step of few rows 0.2 to 0.3 us more
   constexpr int rows = kAppendThreads / (D / 8);  // per pass
   return std::min(p.blk, p.Qmax) <= 4 * rows ? launch_h<D, 4>(p, bf16, e5m2, grid, st)
                                              : launch_h<D, 8>(p, bf16, e5m2, grid, st);

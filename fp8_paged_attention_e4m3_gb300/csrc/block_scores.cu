@@ -17,11 +17,14 @@
 // and the matching share of B is 4 consecutive halves of a query's row.  The
 // bytes of the bounds bound it (2 D per block and head, read once); the tensor
 // products of up to 96 rows stay below them.  16 sequences of up to
-// 131072 tokens, 8 heads of 128, blocks of 32: 91 MB in 21.5 us, 4.3 TB/s; what
+// 131072 tokens, 8 heads of 128, blocks of 32: 91 MB in 20.1 us, 4.5 TB/s; what
 // keeps it from the memory's rate is the start of the chain (page, queries and
-// lengths, asked for together -> bounds -> products) and the ragged end.  Eight
-// queries of 6 heads of 256 over 262144 tokens, in blocks of 64, are that chain
-// alone, 5.8 us.
+// lengths, asked for together -> bounds -> products) and the ragged end, of a grid
+// sized for the columns, not the lengths.  Eight queries of 6 heads of 256 over
+// 262144 tokens, in blocks of 64, are that chain alone, 5.7 us.  More rows on
+// a KV head cost products: 16 sequences of up to 131072 tokens in blocks of 64, 8
+// KV heads of 128 with 6 query heads each, take 11.9 us with one query and 70.6
+// with sixteen (96 rows).
 #include <algorithm>
 
 #include "block_common.cuh"
@@ -239,8 +242,8 @@ cudaError_t launch_t(const ScoreParams &p, cudaStream_t stream) {
   }
   // CTAs for one and a half loads of every SM (as far as shared memory allows),
   // whose warps then take several steps: each CTA reads and splits the queries,
-  // and those of short sequences leave room early.  22.4 us for the batch above,
-  // 22.9 with one load, 22.8 with two; the next step's bounds on their way during
+  // and those of short sequences leave room early.  20.2 us for the batch above,
+  // 21.5 with one load, 20.0 with two; the next step's bounds on their way during
   // one's products cost more registers than they gain (1 us)
   const int64_t per = kScoreWarps * 16, rows = (int64_t)p.Hkv * p.parts * p.B;
   const int64_t need = std::max<int64_t>(1, (p.cols + per - 1) / per);
@@ -255,8 +258,8 @@ cudaError_t launch_t(const ScoreParams &p, cudaStream_t stream) {
 template <int D, bool E5M2>
 cudaError_t launch_n(ScoreParams p, cudaStream_t stream) {
   // Few blocks: the queries are split over CTAs until there are two per SM.  The
-  // eight queries above take 6.2 us by twos, 6.4 by fours, 8.8 one by one; all by
-  // one CTA 8.4
+  // eight queries above take 5.7 us by twos, 7.9 one by one, 6.8 all by one CTA;
+  // by fours 5.1 now, 6.4 when the rule was made
   const int64_t ctas = (p.cols + 16 * kScoreWarps - 1) / (16 * kScoreWarps) * (int64_t)p.Hkv * p.B;
   p.parts = 1;
   p.qn = p.Qmax;

@@ -19,9 +19,11 @@
 // again in each pass, and every warp counts and then writes its segment.
 //
 // The steps of the search bound it, not the bytes (4 per score): histogram,
-// scan over the bins, next digit, each behind a barrier.  16 rows of 4096
-// blocks take 4.7 us, 256 rows of up to 16384 blocks 14.5 us (of which reading
-// the row is a third).
+// scan over the bins, next digit, each behind a barrier and each over all keys
+// of the row.  16 rows of 4096 blocks take 4.8 us, 256 rows of up to 16384 blocks
+// 14.6 us (of which reading the row is a third).  Rows past 16384 blocks are read
+// again in each pass: 256 rows of 16384 13.7 us, of 16400 29.2, of 25000 43.2; two
+// rows 8.6, 17.0 and 22.6, of 100000 97.
 #include "block_common.cuh"
 #include "kernels.h"
 #include "verify_attn_e4m3.h"
