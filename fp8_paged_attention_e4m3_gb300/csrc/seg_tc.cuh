@@ -17,10 +17,13 @@
 //
 // What bounds it.  The keys' bytes, read once: 32 sequences of up to 32749
 // tokens, 8 heads of 128 (1.42 GB), take 234 us with the combine, 0.90 of the
-// copy peak, with the softmax and the decoders beside the copies.  One sequence
-// of 262144 tokens, 48 rows of 256 (134 MB), takes 34.9 us (0.57): 3 us to the
-// first copy (lengths, plan, page), 3 to the first scores, 20 at the memory's
-// rate, up to 4 for the SMs whose rows are raised most often, 4 for the combine.
+// copy peak (245 on some GPUs), with the softmax and the decoders beside the
+// copies.  One sequence of 262144 tokens, 48 rows of 256 (134 MB), takes 35.0 us
+// (0.57): 3 us to the first copy (lengths, plan, page), 3 to the first scores, 20
+// at the memory's rate, up to 4 for the SMs whose rows are raised most often, 4
+// for the combine.  Two row groups (more than 64 rows a KV head) each read the
+// keys: 96 rows over the same sequence take 52.9 us.  Strides that no tensor map
+// takes (8-byte copies): 68 and 752 us.
 //
 // Mathematics.  With t = softmax_scale log2(e) s_K (q . dec(K)) the score of a
 // key in log2 units and g = log2 s_V of its block, its weight is
