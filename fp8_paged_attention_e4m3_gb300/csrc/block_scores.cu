@@ -14,17 +14,16 @@
 // channels is free as long as A and B agree, so a thread takes 16 consecutive
 // bytes of a block's bounds as its share of four k-steps: A goes from memory
 // to the fragments with one 16-byte load per 16 channels and no shared memory,
-// and the matching share of B is 4 consecutive halves of a query's row.  The
-// bytes of the bounds bound it (2 D per block and head, read once); the tensor
-// products of up to 96 rows stay below them.  16 sequences of up to
-// 131072 tokens, 8 heads of 128, blocks of 32: 91 MB in 20.1 us, 4.5 TB/s; what
-// keeps it from the memory's rate is the start of the chain (page, queries and
-// lengths, asked for together -> bounds -> products) and the ragged end, of a grid
-// sized for the columns, not the lengths.  Eight queries of 6 heads of 256 over
-// 262144 tokens, in blocks of 64, are that chain alone, 5.7 us.  More rows on
-// a KV head cost products: 16 sequences of up to 131072 tokens in blocks of 64, 8
-// KV heads of 128 with 6 query heads each, take 11.9 us with one query and 70.6
-// with sixteen (96 rows).
+// and the matching share of B is 4 consecutive halves of a query's row.  With few
+// rows a KV head the bytes of the bounds bound it (2 D per block and head, read
+// once).  16 sequences of up to 131072 tokens, 8 heads of 128, blocks of 32: 91 MB
+// in 20.1 us, 4.5 TB/s; what keeps it from the memory's rate is the start of the
+// chain (page, queries and lengths, asked for together -> bounds -> products) and
+// the ragged end, of a grid sized for the columns, not the lengths.  Eight queries
+// of 6 heads of 256 over 262144 tokens, in blocks of 64, are that chain alone,
+// 5.7 us.  More rows cost products and maxima: 16 sequences of up to 131072 tokens
+// in blocks of 64, 8 KV heads of 128 with 6 query heads each, take 11.9 us with one
+// query and 70.6 with sixteen (96 rows).
 #include <algorithm>
 
 #include "block_common.cuh"

@@ -520,8 +520,8 @@ int verify_attn_e4m3_append(const vae4_tensor *k_new, const vae4_tensor *v_new,
  * Arguments, results and errors as verify_attn_e4m3_kv with block_scales in
  * the place of kv_scales.  A block with an invalid scale sets BAD_SCALE and
  * zeroes the rows of its sequence and KV head, as an invalid page does.  A
- * query with a NaN, or with an infinity that makes its scores infinite or NaN,
- * gives a row of NaN.
+ * query with a score of NaN or +infinity gives a row of NaN, one whose scores
+ * are all -infinity zeros.
  *  workspace   at least verify_attn_e4m3_block_scaled_workspace_bytes(...)
  *              bytes.
  * The batch's keys are divided evenly among the SMs on the device, from the

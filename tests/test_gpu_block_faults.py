@@ -347,3 +347,20 @@ def test_lengths_without_q_and_strided_arguments():
     now.scales = results[0][2].view(torch.float32).cpu()
     check(results[0][6].cpu(), *reference(now, q))
     check(results[0][7].cpu(), *reference(now, q, allowed=listed(now, results[0][5].cpu())))
+
+
+def test_a_query_whose_scores_are_all_minus_infinity_gives_zeros():
+    """An infinite query against keys that are all negative in its channel."""
+    c = Cache([(900, 2)], 1, 64, 16, 16, seed=39)
+    c.codes[0][..., 3] = torch.where(c.codes[0][..., 3] == 0x7F, c.codes[0][..., 3], torch.tensor(0xB8, dtype=torch.uint8))
+    q = queries(c, 2, 3)
+    ref, tol = reference(c, q)
+    q[0, 1, 2, 3] = float("inf")
+    ref[0, 1, 2] = tol[0, 1, 2] = 0
+    k, v = c.device()
+    qd, bt, seq, sc = dev(q, c.table, c.seq, c.scales)
+    out, cap = torch.full_like(qd, 3), c.table.shape[1] * 16
+    ws = vae4.alloc_workspace(1, 3, 1, 2, 64, cap)
+    vae4.verify_attn_e4m3_block_scaled(qd, k, v, bt, seq, sc, out, ws)
+    assert vae4.read_status(ws) == 0
+    check(out.cpu(), ref, tol)
