@@ -29,6 +29,9 @@ STATUS_TIMEOUT = 0x8
 STATUS_PLAN = 0x10
 STATUS_BAD_SCALE = 0x20
 STATUS_BAD_VALUE = 0x40
+STATUS_NO_PAGES = 0x80
+STATUS_BAD_COUNT = 0x100
+STATUS_BAD_PARENT = 0x200
 
 ERRORS = {
     0: "VAE4_OK", -1: "VAE4_ERR_NULL", -2: "VAE4_ERR_DTYPE", -3: "VAE4_ERR_SHAPE",
@@ -50,6 +53,9 @@ EXPORTS = (
     "verify_attn_e4m3_block_scores", "verify_attn_e4m3_select_blocks",
     "verify_attn_e4m3_sparse", "verify_attn_e4m3_block_scaled_workspace_bytes",
     "verify_attn_e4m3_sparse_workspace_bytes",
+    "verify_attn_e4m3_copy_pages", "verify_attn_e4m3_fork_pages",
+    "verify_attn_e4m3_resize_pages", "verify_attn_e4m3_pages_workspace_bytes",
+    "verify_attn_e4m3_compact_pages",
 )
 
 NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -142,13 +148,18 @@ def load(build_if_stale: bool = True):
                            ("block_scaled", [VP] * 9 + [O]),
                            ("sparse", [VP] * 10 + [O]),
                            ("block_scores", [VP] * 6 + [I, F, VP, I, VP]),
-                           ("select_blocks", [VP] * 3 + [I, I, I, VP, VP])):
+                           ("select_blocks", [VP] * 3 + [I, I, I, VP, VP]),
+                           ("copy_pages", [VP] * 7), ("fork_pages", [VP] * 5),
+                           ("resize_pages", [VP] * 5 + [I, VP, VP]),
+                           ("compact_pages", [VP] * 5)):
             fn = getattr(lib, "verify_attn_e4m3_" + name)
             fn.argtypes, fn.restype = args, ctypes.c_int
         lib.verify_attn_e4m3_block_scaled_workspace_bytes.argtypes = [ctypes.c_int] * 7
         lib.verify_attn_e4m3_block_scaled_workspace_bytes.restype = ctypes.c_int64
         lib.verify_attn_e4m3_sparse_workspace_bytes.argtypes = [ctypes.c_int] * 9
         lib.verify_attn_e4m3_sparse_workspace_bytes.restype = ctypes.c_int64
+        lib.verify_attn_e4m3_pages_workspace_bytes.argtypes = [ctypes.c_int64]
+        lib.verify_attn_e4m3_pages_workspace_bytes.restype = ctypes.c_int64
         _lib = lib
         return lib
 
@@ -588,3 +599,69 @@ def alloc_sparse_workspace(B, Hq, Hkv, Qmax, D, max_seq_len, block_tokens, block
     import torch
     n = sparse_workspace_bytes(B, Hq, Hkv, Qmax, D, max_seq_len, block_tokens, blocks)
     return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+# ----------------------------------------------------------------------------
+# the pages' lives
+# ----------------------------------------------------------------------------
+def alloc_ref_counts(n_pages, device=None):
+    """Counts (int32 [n_pages]) of a pool whose pages are all free (torch
+    allocation); its block table is -1 throughout."""
+    import torch
+    return torch.zeros(n_pages, dtype=torch.int32, device=device or "cuda")
+
+
+def verify_attn_e4m3_pages_workspace_bytes(n_pages) -> int:
+    n = load().verify_attn_e4m3_pages_workspace_bytes(n_pages)
+    if n < 0:
+        raise Vae4Error(int(n), "pages_workspace_bytes")
+    return int(n)
+
+
+pages_workspace_bytes = verify_attn_e4m3_pages_workspace_bytes
+
+
+def alloc_pages_workspace(n_pages, device=None):
+    """A workspace for verify_attn_e4m3_resize_pages (torch allocation, 256-B
+    aligned)."""
+    import torch
+    return torch.empty(pages_workspace_bytes(n_pages), dtype=torch.uint8, device=device or "cuda")
+
+
+def verify_attn_e4m3_copy_pages(k_cache, v_cache, pairs, *, block_scales=None, k_bounds=None,
+                                status=None, stream=None):
+    """Copy whole pages of a cache, and of its block scales and bounds, for every
+    (source, destination) pair of ``pairs`` (int32 [n][2]); (-1, -1) copies
+    nothing.  Caches of either FP8 format.  See the header."""
+    if _torch is None:
+        _setup()
+    flags = FLAG_KV_E5M2 if k_cache.dtype == _torch.float8_e5m2 else 0  # a type, not a meaning
+    _call("verify_attn_e4m3_copy_pages", (k_cache, v_cache, pairs, block_scales, k_bounds),
+          (_status_pointer(status),), stream, flags)
+
+
+def verify_attn_e4m3_fork_pages(block_table, ref_counts, parents, *, status=None, stream=None):
+    """Make row b of the block table the row parents[b] (int32 [B]; -1: empty),
+    and count the pages' entries, in place; see the header."""
+    _call("verify_attn_e4m3_fork_pages", (block_table, ref_counts, parents),
+          (_status_pointer(status),), stream)
+
+
+def verify_attn_e4m3_resize_pages(block_table, seq_lens, ref_counts, copies, workspace, *,
+                                  page_tokens: int, status=None, stream=None):
+    """Give every sequence the pages of ``seq_lens`` (int32 [B][2]: (L, q)), those
+    of its last q tokens its own, and free the others, in place; ``copies``
+    (int32 [B][2]) receives the (old, new) pages to copy.  ``workspace`` from
+    alloc_pages_workspace.  See the header."""
+    _call("verify_attn_e4m3_resize_pages", (block_table, seq_lens, ref_counts, copies, workspace),
+          (page_tokens, _status_pointer(status)), stream)
+    return copies
+
+
+def verify_attn_e4m3_compact_pages(block_table, ref_counts, moves, *, status=None, stream=None):
+    """Move pages in use to the lowest ids, at most as many as ``moves`` (int32
+    [m][2]) holds, in the table and the counts; ``moves`` receives the (old, new)
+    pages to copy.  See the header."""
+    _call("verify_attn_e4m3_compact_pages", (block_table, ref_counts, moves),
+          (_status_pointer(status),), stream)
+    return moves

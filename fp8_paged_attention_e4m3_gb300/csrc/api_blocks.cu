@@ -7,55 +7,6 @@ using namespace vae4;
 
 namespace {
 
-// lengths: I32 [B] or [B][2]
-int check_seq(const vae4_tensor *seq, int64_t B, int *has_qlen) {
-  if (seq->dtype != VAE4_I32) return VAE4_ERR_DTYPE;
-  *has_qlen = 0;
-  if (seq->ndim == 1) {
-    if (seq->shape[0] != B) return VAE4_ERR_SHAPE;
-  } else if (seq->ndim == 2) {
-    if (seq->shape[0] != B || seq->shape[1] != 2) return VAE4_ERR_SHAPE;
-    if (seq->stride[1] != 1) return VAE4_ERR_STRIDE;
-    *has_qlen = 1;
-  } else {
-    return VAE4_ERR_SHAPE;
-  }
-  if (seq->stride[0] < 0 || seq->stride[0] > INT32_MAX) return VAE4_ERR_STRIDE;
-  return VAE4_OK;
-}
-
-int check_table(const vae4_tensor *bt, int64_t B) {
-  if (bt->dtype != VAE4_I32) return VAE4_ERR_DTYPE;
-  if (bt->ndim != 2 || bt->shape[0] != B || bt->shape[1] < 1 || bt->shape[1] > INT32_MAX)
-    return VAE4_ERR_SHAPE;
-  if (bt->stride[1] != 1 || bt->stride[0] < 0) return VAE4_ERR_STRIDE;
-  return VAE4_OK;
-}
-
-// bounds: U8 [n_pages][Hkv][blocks per page][2][D], d contiguous, the other
-// strides multiples of 16
-int check_bounds(const vae4_tensor *b, int64_t n_pages, int64_t Hkv, int64_t nb, int64_t D) {
-  if (b->dtype != VAE4_U8) return VAE4_ERR_DTYPE;
-  if (b->ndim != 5 || b->shape[0] != n_pages || b->shape[1] != Hkv || b->shape[2] != nb ||
-      b->shape[3] != 2 || b->shape[4] != D)
-    return VAE4_ERR_SHAPE;
-  if (b->stride[4] != 1) return VAE4_ERR_STRIDE;
-  for (int k = 0; k < 4; ++k)
-    if (b->stride[k] < 0 || b->stride[k] % 16 != 0 || b->stride[k] >= ((int64_t)1 << 40))
-      return VAE4_ERR_STRIDE;
-  if (!al16(b->data)) return VAE4_ERR_MISALIGNED;
-  return VAE4_OK;
-}
-
-// an output whose elements along a dimension of more than one share memory
-bool overlaps(const vae4_tensor *t, int dims, int64_t inner) {
-  for (int k = 0; k < dims; ++k)
-    if (t->shape[k] > 1 && t->stride[k] < inner) return true;
-  return false;
-}
-
-cudaStream_t cu(vae4_stream s) { return reinterpret_cast<cudaStream_t>(s); }
-
 int run_attention(const Prepared &pr, cudaStream_t st) {
   if (pr.sparse && launch_block_list(pr.lp, st) != cudaSuccess) return VAE4_ERR_CUDA;
   if (launch_seg(pr.gp, st) != cudaSuccess) return VAE4_ERR_CUDA;

@@ -263,6 +263,55 @@ inline int check_ids(const vae4_tensor *ids, int64_t B, int64_t Qmax, int64_t Hk
   return VAE4_OK;
 }
 
+// lengths: I32 [B] or [B][2]
+inline int check_seq(const vae4_tensor *seq, int64_t B, int *has_qlen) {
+  if (seq->dtype != VAE4_I32) return VAE4_ERR_DTYPE;
+  *has_qlen = 0;
+  if (seq->ndim == 1) {
+    if (seq->shape[0] != B) return VAE4_ERR_SHAPE;
+  } else if (seq->ndim == 2) {
+    if (seq->shape[0] != B || seq->shape[1] != 2) return VAE4_ERR_SHAPE;
+    if (seq->stride[1] != 1) return VAE4_ERR_STRIDE;
+    *has_qlen = 1;
+  } else {
+    return VAE4_ERR_SHAPE;
+  }
+  if (seq->stride[0] < 0 || seq->stride[0] > INT32_MAX) return VAE4_ERR_STRIDE;
+  return VAE4_OK;
+}
+
+inline int check_table(const vae4_tensor *bt, int64_t B) {
+  if (bt->dtype != VAE4_I32) return VAE4_ERR_DTYPE;
+  if (bt->ndim != 2 || bt->shape[0] != B || bt->shape[1] < 1 || bt->shape[1] > INT32_MAX)
+    return VAE4_ERR_SHAPE;
+  if (bt->stride[1] != 1 || bt->stride[0] < 0) return VAE4_ERR_STRIDE;
+  return VAE4_OK;
+}
+
+// bounds: U8 [n_pages][Hkv][blocks per page][2][D], d contiguous, the other
+// strides multiples of 16
+inline int check_bounds(const vae4_tensor *b, int64_t n_pages, int64_t Hkv, int64_t nb, int64_t D) {
+  if (b->dtype != VAE4_U8) return VAE4_ERR_DTYPE;
+  if (b->ndim != 5 || b->shape[0] != n_pages || b->shape[1] != Hkv || b->shape[2] != nb ||
+      b->shape[3] != 2 || b->shape[4] != D)
+    return VAE4_ERR_SHAPE;
+  if (b->stride[4] != 1) return VAE4_ERR_STRIDE;
+  for (int k = 0; k < 4; ++k)
+    if (b->stride[k] < 0 || b->stride[k] % 16 != 0 || b->stride[k] >= ((int64_t)1 << 40))
+      return VAE4_ERR_STRIDE;
+  if (!al16(b->data)) return VAE4_ERR_MISALIGNED;
+  return VAE4_OK;
+}
+
+// an output whose elements along a dimension of more than one share memory
+inline bool overlaps(const vae4_tensor *t, int dims, int64_t inner) {
+  for (int k = 0; k < dims; ++k)
+    if (t->shape[k] > 1 && t->stride[k] < inner) return true;
+  return false;
+}
+
+inline cudaStream_t cu(vae4_stream s) { return reinterpret_cast<cudaStream_t>(s); }
+
 // Attention over a block-scaled cache: the CTAs, and the workspace: status |
 // (max, sum) [2 CTAs][N][2] | unnormalised O [2 CTAs][N][D] | (first CTA,
 // parts) [streams][row groups] | sparse attention (k > 0): stream records |

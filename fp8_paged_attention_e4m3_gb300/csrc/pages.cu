@@ -1,0 +1,488 @@
+// The pages' lives: copying pages of a cache, and a pool's fork, resize and compaction.
+//
+// A pool is a block table and a count for every page of the table entries that hold
+// it (0: free, below 0: kept).  Everything that a call decides follows from the pool
+// alone, in one order (sequences ascending, then places, then page ids), so that its
+// results do not depend on how the threads run: counts are changed by integer
+// additions, and ranks come from prefix sums.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "block_common.cuh"
+#include "kernels.h"
+#include "page_params.h"
+#include "verify_attn_e4m3.h"
+
+namespace vae4 {
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+// ---------------------------------------------------------------------------
+// copy: every pair's pages, all slabs.
+//
+// One CTA per pair and 1024 vectors of 16 bytes: four loads per thread in flight
+// before the first store.  The slabs of a page are numbered one after another (from
+// multiples of 32, so that a warp copies from one slab).
+constexpr int kCopyThreads = 256, kCopyUnroll = 4;
+
+__device__ __forceinline__ int64_t slab_offset(const PageSlab &s, int v, int vec) {
+  if (s.n[2] == 1) return (int64_t)v * vec;
+  const int r = v / s.run, c = v - r * s.run;
+  const int r1 = r / s.n[2], i2 = r - r1 * s.n[2];
+  const int i0 = r1 / s.n[1], i1 = r1 - i0 * s.n[1];
+  return i0 * s.s[0] + i1 * s.s[1] + i2 * s.s[2] + (int64_t)c * vec;
+}
+
+__global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_constant__ CopyParams p) {
+  await_previous();
+  const int32_t *pr = p.pairs + (int64_t)blockIdx.x * p.pair_sb;
+  const int src = load_dep(pr), dst = load_dep(pr + 1);
+  if (src == dst) return;  // padding (-1, -1) too
+  if (src < 0 || dst < 0 || src >= p.n_pages || dst >= p.n_pages) {
+    if (threadIdx.x == 0 && blockIdx.y == 0 && p.status) atomicOr(p.status, VAE4_STATUS_BAD_BLOCK);
+    return;
+  }
+  for (int v0 = blockIdx.y * (kCopyThreads * kCopyUnroll); v0 < p.vecs;
+       v0 += gridDim.y * (kCopyThreads * kCopyUnroll)) {
+    uint4 x[kCopyUnroll];
+    uint8_t *to[kCopyUnroll];
+    int size[kCopyUnroll];
+#pragma unroll
+    for (int u = 0; u < kCopyUnroll; ++u) {
+      const int v = v0 + u * kCopyThreads + (int)threadIdx.x;
+      int k = 0;
+#pragma unroll
+      for (int t = 1; t < 4; ++t)
+        if (v >= p.slab[t].first) k = t;
+      const PageSlab &s = p.slab[k];
+      size[u] = 0;
+      if (v - s.first < s.vecs) {
+        const int vec = p.vec[k];
+        const int64_t off = slab_offset(s, v - s.first, vec);
+        const uint8_t *from = s.base + src * s.ps + off;
+        to[u] = s.base + dst * s.ps + off;
+        size[u] = vec;
+        if (vec == 16)
+          x[u] = load_dep(reinterpret_cast<const uint4 *>(from));
+        else if (vec == 8)
+          *reinterpret_cast<uint2 *>(&x[u]) = load_dep(reinterpret_cast<const uint2 *>(from));
+        else
+          x[u].x = load_dep(reinterpret_cast<const uint32_t *>(from));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kCopyUnroll; ++u) {
+      if (size[u] == 16)
+        *reinterpret_cast<uint4 *>(to[u]) = x[u];
+      else if (size[u] == 8)
+        *reinterpret_cast<uint2 *>(to[u]) = make_uint2(x[u].x, x[u].y);
+      else if (size[u] == 4)
+        *reinterpret_cast<uint32_t *>(to[u]) = x[u].x;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// counts
+
+// A page's count, changed by others of this grid meanwhile.
+__device__ __forceinline__ int count_of(const PoolParams &p, int e) { return __ldcg(p.counts + e); }
+
+// One entry of page e more or less; what is kept stays, and a count that is zero
+// although an entry holds the page is reported and left.
+__device__ __forceinline__ void add_count(const PoolParams &p, int e, int by, unsigned &bad) {
+  const int c = count_of(p, e);
+  if (c > 0)
+    atomicAdd(p.counts + e, by);
+  else if (c == 0)
+    bad |= VAE4_STATUS_BAD_COUNT;
+}
+
+__device__ __forceinline__ void report(uint32_t *status, unsigned bad) {
+  bad = __reduce_or_sync(0xffffffffu, bad);
+  if (bad && status && (threadIdx.x & 31) == 0) atomicOr(status, bad);
+}
+
+// ---------------------------------------------------------------------------
+// fork: row b <- row parents[b].
+//
+// A CTA takes all rows of some columns into shared memory before it writes any, so
+// rows may change places.  An entry of a row with m children counts m - 1 more.
+constexpr int kForkThreads = 512;
+
+__global__ void __launch_bounds__(kForkThreads) fork_pages_kernel(const __grid_constant__ ForkParams p) {
+  extern __shared__ int smem[];
+  const PoolParams &o = p.pool;
+  const int W = p.width, B = o.B, tid = threadIdx.x;
+  int *parent = smem, *kids = smem + B, *tile = smem + 2 * B;  // [B][W]
+  for (int b = tid; b < B; b += kForkThreads) kids[b] = 0;
+  __syncthreads();
+  await_previous();
+  unsigned bad = 0;
+  const int c0 = blockIdx.x * W, log_w = __ffs(W) - 1;
+  for (int x = tid; x < B << log_w; x += kForkThreads) {
+    const int b = x >> log_w, c = c0 + (x & (W - 1));
+    tile[x] = c < o.cols ? load_dep(o.bt + b * o.bt_sb + c) : -1;
+  }
+  for (int b = tid; b < B; b += kForkThreads) {
+    int from = load_dep(p.parents + b);
+    if (from < -1 || from >= B) {
+      bad |= VAE4_STATUS_BAD_PARENT;
+      from = b;  // the row stays
+    }
+    parent[b] = from;
+    if (from >= 0) atomicAdd(kids + from, 1);
+  }
+  __syncthreads();
+  for (int x = tid; x < B << log_w; x += kForkThreads) {
+    const int b = x >> log_w, c = c0 + (x & (W - 1));
+    const int e = tile[x], more = kids[b] - 1;
+    if (e < -1 || e >= o.n_pages)
+      bad |= VAE4_STATUS_BAD_BLOCK;
+    else if (e >= 0 && more != 0)
+      add_count(o, e, more, bad);
+    const int from = parent[b];
+    if (from != b && c < o.cols) o.bt[b * o.bt_sb + c] = from >= 0 ? tile[(from << log_w) + (x & (W - 1))] : -1;
+  }
+  report(o.status, bad);
+}
+
+// ---------------------------------------------------------------------------
+// resize and compact: one cluster, whose warps share the table's entries and the
+// pages evenly in ascending ranges.  Between steps that read what others wrote the
+// cluster meets (its barrier orders their memory); ranks across the cluster are
+// exchanged through distributed shared memory.
+constexpr int kPoolThreads = 1024, kPoolCtas = 8;
+constexpr int kPoolWarps = kPoolThreads / 32 * kPoolCtas;
+
+struct ClusterSums {
+  int2 warp[kPoolThreads / 32];
+  int2 cta[kPoolCtas];
+};
+
+// Sums of a pair over all warps of the cluster (returned), and over those before
+// this one (*before).  Every thread calls it; `s` is used once.
+__device__ __forceinline__ int2 cluster_sums(ClusterSums &s, int2 mine, int2 *before) {
+  cg::cluster_group cl = cg::this_cluster();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = (int)cl.block_rank();
+  if (lane == 0) s.warp[warp] = mine;
+  __syncthreads();
+  const int2 w = s.warp[lane];
+  if (warp == 0) {
+    const int2 t = make_int2((int)__reduce_add_sync(0xffffffffu, (unsigned)w.x),
+                             (int)__reduce_add_sync(0xffffffffu, (unsigned)w.y));
+    if (lane < kPoolCtas) *cl.map_shared_rank(&s.cta[rank], lane) = t;
+  }
+  cl.sync();
+  const int2 c = lane < kPoolCtas ? s.cta[lane] : make_int2(0, 0);
+  const int2 bw = lane < warp ? w : make_int2(0, 0), bc = lane < rank ? c : make_int2(0, 0);
+  before->x = (int)__reduce_add_sync(0xffffffffu, (unsigned)(bw.x + bc.x));
+  before->y = (int)__reduce_add_sync(0xffffffffu, (unsigned)(bw.y + bc.y));
+  return make_int2((int)__reduce_add_sync(0xffffffffu, (unsigned)c.x),
+                   (int)__reduce_add_sync(0xffffffffu, (unsigned)c.y));
+}
+
+// The warp's share of n things: [x, y), x and y multiples of 32 (but for y = n).
+__device__ __forceinline__ int2 share(int64_t n, int gwarp) {
+  const int64_t per = (n + kPoolWarps * 32 - 1) / (kPoolWarps * 32) * 32;
+  return make_int2((int)min(n, gwarp * per), (int)min(n, (gwarp + 1) * per));
+}
+
+// f(index, value) over the warp's share of the table's entries, row after row;
+// every lane calls it, an index past the share with value -2
+constexpr int kBatch = 8;  // loads in flight per thread
+template <class F>
+__device__ __forceinline__ void each_entry(const PoolParams &o, int2 part, F f) {
+  const int lane = threadIdx.x & 31;
+  for (int x0 = part.x; x0 < part.y; x0 += 32 * kBatch) {
+    int e[kBatch], b[kBatch], j[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int x = x0 + 32 * u + lane;
+      b[u] = (int)((unsigned)x / (unsigned)o.cols);
+      j[u] = x - b[u] * o.cols;
+      e[u] = x < part.y ? __ldcg(o.bt + b[u] * o.bt_sb + j[u]) : -2;
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (x0 + 32 * u < part.y) f(b[u], j[u], e[u], x0 + 32 * u + lane < part.y);
+  }
+}
+// f(page, count, in the share) over the warp's share of the pages
+template <class F>
+__device__ __forceinline__ void each_page(const PoolParams &o, int2 part, F f) {
+  const int lane = threadIdx.x & 31;
+  for (int x0 = part.x; x0 < part.y; x0 += 32 * kBatch) {
+    int c[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int x = x0 + 32 * u + lane;
+      c[u] = x < part.y ? count_of(o, x) : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (x0 + 32 * u < part.y) f(x0 + 32 * u + lane, c[u], x0 + 32 * u + lane < part.y);
+  }
+}
+
+// resize: pages past a row's length go back; then entries without a page and
+// written entries of pages that others hold too get the lowest free ones.
+__global__ void __launch_bounds__(kPoolThreads, 1)
+    resize_pages_kernel(const __grid_constant__ ResizeParams p) {
+  extern __shared__ int2 row[];  // (pages, first page written) of each row; pages = -1: the row stays
+  __shared__ ClusterSums sums;
+  cg::cluster_group cl = cg::this_cluster();
+  const PoolParams &o = p.pool;
+  const int tid = threadIdx.x, lane = tid & 31, rank = (int)cl.block_rank();
+  const int gwarp = rank * (kPoolThreads / 32) + (tid >> 5);
+  const unsigned below = (1u << lane) - 1u;
+  await_previous();
+  unsigned bad = 0;
+  for (int b = tid; b < o.B; b += kPoolThreads) {
+    const int32_t *s = p.seq + (int64_t)b * p.seq_sb;
+    const int L = load_dep(s), q = p.seq_has_qlen ? load_dep(s + 1) : 0;
+    int2 r = make_int2(-1, 0);
+    if (L < 0 || L > o.cols * p.page)
+      bad |= VAE4_STATUS_BAD_LENGTH;
+    else if (q < 0 || q > L)
+      bad |= VAE4_STATUS_BAD_QLEN;
+    else
+      r = make_int2((L + p.page - 1) / p.page, q > 0 ? (L - q) / p.page : o.cols);
+    row[b] = r;
+    if (rank == 0) {
+      p.copies[b * p.copies_sb] = -1;
+      p.copies[b * p.copies_sb + 1] = -1;
+    }
+  }
+  __syncthreads();
+  const int2 part = share((int64_t)o.B * o.cols, gwarp);
+  each_entry(o, part, [&](int b, int j, int e, bool in) {
+    if (!in) return;
+    if (e < -1 || e >= o.n_pages) {
+      bad |= VAE4_STATUS_BAD_BLOCK;
+    } else if (row[b].x >= 0 && j >= row[b].x && e >= 0) {
+      o.bt[b * o.bt_sb + j] = -1;
+      add_count(o, e, -1, bad);
+    }
+  });
+  cl.sync();
+  // entries that need a page: evaluated twice, with no count changed in between that
+  // an entry of the table holds
+  auto needs = [&](int b, int j, int e, bool in) -> bool {
+    if (!in || j >= row[b].x) return false;
+    if (e == -1) return true;
+    if (e < 0 || e >= o.n_pages || j < row[b].y) return false;
+    const int c = count_of(o, e);
+    return c > 1 || c < 0;
+  };
+  int2 mine = make_int2(0, 0), before;
+  each_entry(o, part, [&](int b, int j, int e, bool in) {
+    mine.x += __popc(__ballot_sync(0xffffffffu, needs(b, j, e, in)));
+  });
+  const int2 ids = share(o.n_pages, gwarp);
+  each_page(o, ids, [&](int, int c, bool in) { mine.y += __popc(__ballot_sync(0xffffffffu, in && c == 0)); });
+  const int2 total = cluster_sums(sums, mine, &before);
+  const int served = min(total.x, total.y);
+  if (total.x > total.y) bad |= VAE4_STATUS_NO_PAGES;
+  if (before.y < served) {
+    int at = before.y;
+    each_page(o, ids, [&](int x, int c, bool in) {
+      const unsigned m = __ballot_sync(0xffffffffu, in && c == 0);
+      const int r = at + __popc(m & below);
+      if (in && c == 0 && r < served) __stcg(p.list + r, x);
+      at += __popc(m);
+    });
+  }
+  cl.sync();
+  if (mine.x > 0 && before.x < served) {
+    int at = before.x;
+    each_entry(o, part, [&](int b, int j, int e, bool in) {
+      const bool want = needs(b, j, e, in);
+      const unsigned m = __ballot_sync(0xffffffffu, want);
+      const int r = at + __popc(m & below);
+      at += __popc(m);
+      if (!want || r >= served) return;
+      const int id = __ldcg(p.list + r);
+      __stcg(p.list + r, e);  // the page that it gives up, counted down below
+      o.bt[b * o.bt_sb + j] = id;
+      __stcg(o.counts + id, 1);
+      if (e < 0 || j != row[b].y) return;
+      const int32_t *s = p.seq + (int64_t)b * p.seq_sb;
+      if ((load_dep(s) - load_dep(s + 1)) % p.page != 0) {
+        p.copies[b * p.copies_sb] = e;
+        p.copies[b * p.copies_sb + 1] = id;
+      }
+    });
+  }
+  cl.sync();
+  for (int r = rank * kPoolThreads + tid; r < served; r += kPoolCtas * kPoolThreads) {
+    const int e = __ldcg(p.list + r);
+    if (e >= 0) add_count(o, e, -1, bad);
+  }
+  report(o.status, bad);
+}
+
+// compact: with n pages in use, the highest pages with id >= n go to the lowest free
+// ones below n.  A page that moves leaves its rank in the place of its count until
+// the table's entries have been looked up there.
+__global__ void __launch_bounds__(kPoolThreads, 1)
+    compact_pages_kernel(const __grid_constant__ CompactParams p) {
+  __shared__ ClusterSums sums[2];
+  cg::cluster_group cl = cg::this_cluster();
+  const PoolParams &o = p.pool;
+  const int tid = threadIdx.x, lane = tid & 31, rank = (int)cl.block_rank();
+  const int gwarp = rank * (kPoolThreads / 32) + (tid >> 5);
+  const unsigned below = (1u << lane) - 1u;
+  await_previous();
+  const int2 ids = share(o.n_pages, gwarp);
+  int2 mine = make_int2(0, 0), before;  // (pages in use, pages that may move)
+  each_page(o, ids, [&](int, int c, bool in) {
+    mine.x += __popc(__ballot_sync(0xffffffffu, in && c != 0));
+    mine.y += __popc(__ballot_sync(0xffffffffu, in && c > 0));
+  });
+  const int n = cluster_sums(sums[0], mine, &before).x;
+  // holes below n and pages to move from n on
+  if (ids.y <= n) {
+    mine = make_int2(ids.y - ids.x - mine.x, 0);
+  } else if (ids.x >= n) {
+    mine.x = 0;
+  } else {
+    mine = make_int2(0, 0);
+    each_page(o, ids, [&](int x, int c, bool in) {
+      mine.x += __popc(__ballot_sync(0xffffffffu, in && c == 0 && x < n));
+      mine.y += __popc(__ballot_sync(0xffffffffu, in && c > 0 && x >= n));
+    });
+  }
+  const int2 total = cluster_sums(sums[1], mine, &before);
+  const int moved = min(p.n, total.y);  // (no fewer holes than pages to move)
+  if (mine.x > 0 && before.x < moved) {
+    int at = before.x;
+    each_page(o, ids, [&](int x, int c, bool in) {
+      const bool hole = in && c == 0 && x < n;
+      const unsigned m = __ballot_sync(0xffffffffu, hole);
+      const int r = at + __popc(m & below);
+      if (hole && r < moved) __stcg(p.moves + r * p.moves_sb + 1, x);
+      at += __popc(m);
+    });
+  }
+  if (mine.y > 0 && total.y - before.y - mine.y < moved) {
+    int at = total.y - before.y;  // ranks descend with the id
+    each_page(o, ids, [&](int x, int c, bool in) {
+      const bool goes = in && c > 0 && x >= n;
+      const unsigned m = __ballot_sync(0xffffffffu, goes);
+      const int r = at - 1 - __popc(m & below);
+      if (goes && r < moved) __stcg(p.moves + r * p.moves_sb, x);
+      at -= __popc(m);
+    });
+  }
+  const int first = rank * kPoolThreads + tid;
+  for (int r = moved + first; r < p.n; r += kPoolCtas * kPoolThreads) {
+    __stcg(p.moves + r * p.moves_sb, -1);
+    __stcg(p.moves + r * p.moves_sb + 1, -1);
+  }
+  if (moved == 0) return;  // the same for the whole cluster, and no remote access is left
+  cl.sync();
+  for (int r = first; r < moved; r += kPoolCtas * kPoolThreads) {
+    const int from = __ldcg(p.moves + r * p.moves_sb), to = __ldcg(p.moves + r * p.moves_sb + 1);
+    __stcg(o.counts + to, count_of(o, from));
+    __stcg(o.counts + from, INT32_MIN + r);
+  }
+  cl.sync();
+  const int lowest = __ldcg(p.moves + (moved - 1) * p.moves_sb);
+  unsigned bad = 0;
+  each_entry(o, share((int64_t)o.B * o.cols, gwarp), [&](int b, int j, int e, bool in) {
+    if (!in) return;
+    if (e < -1 || e >= o.n_pages) {
+      bad |= VAE4_STATUS_BAD_BLOCK;
+    } else if (e >= lowest) {
+      const int r = (int)((unsigned)count_of(o, e) ^ 0x80000000u);
+      // (a kept page's count may look like a rank)
+      if (r >= 0 && r < moved && __ldcg(p.moves + r * p.moves_sb) == e)
+        o.bt[b * o.bt_sb + j] = __ldcg(p.moves + r * p.moves_sb + 1);
+    }
+  });
+  report(o.status, bad);
+  cl.sync();
+  for (int r = first; r < moved; r += kPoolCtas * kPoolThreads)
+    __stcg(o.counts + __ldcg(p.moves + r * p.moves_sb), 0);
+}
+
+// The limit of a kernel's dynamic shared memory, raised once per context to the most
+// that any call needs (as for the visit lists).
+template <auto Kernel>
+cudaError_t allow_smem(size_t most, size_t smem) {
+  if (smem <= 48 * 1024) return cudaSuccess;
+  constexpr int kDevs = 64;
+  static std::atomic<unsigned long long> configured[kDevs] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+  const unsigned long long ctx = current_context_id();
+  if (dev >= 0 && dev < kDevs && ctx != 0 && configured[dev].load(std::memory_order_acquire) == ctx)
+    return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+  if (e == cudaSuccess && dev >= 0 && dev < kDevs)
+    configured[dev].store(current_context_id(), std::memory_order_release);
+  return e;
+}
+
+template <class P>
+cudaError_t launch_cluster(void (*kernel)(P), size_t smem, cudaStream_t stream, const P &p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kPoolCtas);
+  cfg.blockDim = dim3(kPoolThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kPoolCtas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+}  // namespace
+
+cudaError_t launch_copy_pages(const CopyParams &p, cudaStream_t stream) {
+  const int per = kCopyThreads * kCopyUnroll;
+  const int parts = std::min((p.vecs + per - 1) / per, 65535);
+  return launch_dependent(copy_pages_kernel, dim3((unsigned)p.n, (unsigned)parts), kCopyThreads, 0,
+                          stream, p);
+}
+
+cudaError_t launch_fork_pages(const ForkParams &in, int num_sms, cudaStream_t stream) {
+  constexpr int kMost = kMaxForkRows * (4 * 4 + 8);
+  ForkParams p = in;
+  const int B = p.pool.B;
+  // 128-byte pieces of rows, but narrower ones until every SM has a CTA (32 bytes at
+  // least) or the tile fits
+  p.width = 32;
+  while (p.width > 8 && (p.pool.cols + p.width - 1) / p.width < num_sms) p.width /= 2;
+  while (p.width > 4 && B * (4 * p.width + 8) > kMost) p.width /= 2;
+  const size_t smem = (size_t)B * (4 * p.width + 8);
+  const cudaError_t e = allow_smem<fork_pages_kernel>(kMost, smem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(fork_pages_kernel, dim3((unsigned)((p.pool.cols + p.width - 1) / p.width)),
+                          kForkThreads, smem, stream, p);
+}
+
+cudaError_t launch_resize_pages(const ResizeParams &p, cudaStream_t stream) {
+  const size_t smem = (size_t)p.pool.B * sizeof(int2);
+  const cudaError_t e = allow_smem<resize_pages_kernel>(kMaxResizeRows * sizeof(int2), smem);
+  if (e != cudaSuccess) return e;
+  return launch_cluster(resize_pages_kernel, smem, stream, p);
+}
+
+cudaError_t launch_compact_pages(const CompactParams &p, cudaStream_t stream) {
+  return launch_cluster(compact_pages_kernel, 0, stream, p);
+}
+
+}  // namespace vae4

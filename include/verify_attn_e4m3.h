@@ -162,6 +162,9 @@ enum vae4_error {
 #define VAE4_STATUS_BAD_SCALE 0x20u /* a block scale is not within 2^-40 .. 2^40 */
 #define VAE4_STATUS_BAD_VALUE 0x40u /* append: a NaN (stored as 0), or an infinity or a value
                                        beyond 2^30 times the format's largest (saturated) */
+#define VAE4_STATUS_NO_PAGES 0x80u  /* resize: fewer free pages than entries that need one */
+#define VAE4_STATUS_BAD_COUNT 0x100u /* an entry holds a page whose count is 0 */
+#define VAE4_STATUS_BAD_PARENT 0x200u /* fork: a parent that is neither -1 nor a row */
 
 /*
  * verify_attn_e4m3 -- the verify step (split kernel + combine kernel).
@@ -620,6 +623,106 @@ int64_t verify_attn_e4m3_block_scaled_workspace_bytes(int B, int Hq, int Hkv, in
 int64_t verify_attn_e4m3_sparse_workspace_bytes(int B, int Hq, int Hkv, int Qmax, int D,
                                                 int max_seq_len, int block_tokens, int blocks,
                                                 int num_sms);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The pages' lives.  (No counterpart on the pages, whose engine keeps its block
+ * tables on the host: these are additions of this library.)
+ *
+ * A pool is
+ *  block_table I32 [B][max_pages], stride[1] == 1, rows that share no memory: the
+ *              pages of each sequence in order, -1 where there is none (every
+ *              entry of a row counts here, not those of its length alone);
+ *  ref_counts  I32 [n_pages], stride[0] == 1: how many entries of the table hold
+ *              the page; 0: it is free; below 0: it is kept, in use without being
+ *              counted, handed out, moved or freed.
+ * The calls change both in place and leave them consistent.  All that they decide
+ * follows from the pool alone, in ascending order of sequences, places and page
+ * ids: the same pool gives the same result.  Two calls on a pool must not overlap.
+ * One table serves the caches of all layers: the calls that change it say which
+ * pages have to be copied, and verify_attn_e4m3_copy_pages copies them for each.
+ *  dev_status  optional device pointer to a status word (NULL = none).  An entry
+ *              that is neither -1 nor a page's id sets BAD_BLOCK and stays, and
+ *              a page that an entry holds although its count is 0 sets BAD_COUNT
+ *              where it should be counted down or up, and stays 0.
+ * At most 2^30 table entries and pages.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * verify_attn_e4m3_copy_pages -- copy whole pages within a cache.
+ *  k_cache, v_cache  U8 [n_pages][page][Hkv][D] as for verify_attn_e4m3_kv.
+ *  pairs       I32 [n][2], stride[1] == 1: (source, destination) page ids, such as
+ *              the lists that verify_attn_e4m3_resize_pages and
+ *              verify_attn_e4m3_compact_pages write.  Pairs of equal ids, (-1, -1)
+ *              among them, copy nothing; other invalid ids: BAD_BLOCK, and nothing
+ *              is copied for the pair.  Destinations have to differ from one
+ *              another and from every other pair's source.
+ *  block_scales, k_bounds  as for verify_attn_e4m3_append, or NULL: a
+ *              block-scaled cache's scales and bounds move with the pages.
+ */
+int verify_attn_e4m3_copy_pages(const vae4_tensor *k_cache, const vae4_tensor *v_cache,
+                                const vae4_tensor *pairs, const vae4_tensor *block_scales,
+                                const vae4_tensor *k_bounds, uint32_t *dev_status,
+                                vae4_stream stream);
+
+/*
+ * verify_attn_e4m3_fork_pages -- every row of the table becomes the row of its
+ * parent (as it was before the call): row b holds the pages of row parents[b], none
+ * if that is -1.
+ *  parents     I32 [B], stride[0] == 1; b itself: the row stays.  Any other value
+ *              than -1 .. B - 1: BAD_PARENT, and the row stays.
+ * So rows can be forked (a parent with several children; its pages are shared),
+ * dropped, and change places, as in a step of beam search.  A row of m children
+ * adds m - 1 to the count of each of its pages.  At most 8192 rows.
+ */
+int verify_attn_e4m3_fork_pages(const vae4_tensor *block_table, const vae4_tensor *ref_counts,
+                                const vae4_tensor *parents, uint32_t *dev_status,
+                                vae4_stream stream);
+
+/*
+ * verify_attn_e4m3_resize_pages -- give every sequence the pages of its next step.
+ *  seq_lens    I32 [B][2]: (L, q) as verify_attn_e4m3_append takes them next: L
+ *              tokens of which the last q are about to be written (I32 [B]: none).
+ *              0 <= q <= L (else BAD_QLEN), L <= max_pages * page_tokens (else
+ *              BAD_LENGTH); the row of an invalid pair stays.
+ *  copies      I32 [B][2], stride[1] == 1, written in full.
+ *  workspace   U8, at least verify_attn_e4m3_pages_workspace_bytes(n_pages) bytes,
+ *              256-byte aligned; nothing in it has to be set or kept.
+ * In this order:
+ *  1. entries at or past ceil(L / page_tokens) are given back: they become -1, and
+ *     their pages' counts go down (L = 0 frees a sequence, a smaller L gives
+ *     rejected drafts back);
+ *  2. an entry below that needs a page if it is -1, or if it lies at or past
+ *     (L - q) / page_tokens, so that tokens are written there, and its page is held
+ *     by other entries too or kept.  The entries that need one get the free pages,
+ *     the lowest ids first, rows and places ascending, with count 1;
+ *  3. the counts of the pages that were replaced go down.
+ * Where the first page that is written was replaced and holds earlier tokens of the
+ * sequence ((L - q) % page_tokens > 0), copies[b] = (old page, new page), else
+ * (-1, -1): copy them (verify_attn_e4m3_copy_pages) before writing.  With fewer free
+ * pages than entries that need one, the last of these stay as they are (NO_PAGES):
+ * do not write before another call has served them.  At most 16384 rows.
+ */
+int verify_attn_e4m3_resize_pages(const vae4_tensor *block_table, const vae4_tensor *seq_lens,
+                                  const vae4_tensor *ref_counts, const vae4_tensor *copies,
+                                  const vae4_tensor *workspace, int32_t page_tokens,
+                                  uint32_t *dev_status, vae4_stream stream);
+
+/* Bytes of workspace of a verify_attn_e4m3_resize_pages call. */
+int64_t verify_attn_e4m3_pages_workspace_bytes(int64_t n_pages);
+
+/*
+ * verify_attn_e4m3_compact_pages -- bring the pages in use to the low ids.
+ *  moves       I32 [m][2], stride[1] == 1, written in full.
+ * With n pages whose count is not 0: the pages of ids >= n with a count above 0,
+ * the highest first, take the free ids below n, the lowest first, m of them at
+ * most.  moves lists their (old id, new id), then (-1, -1); table and counts are
+ * changed.  Copy the pages (verify_attn_e4m3_copy_pages) before the table is used.
+ */
+int verify_attn_e4m3_compact_pages(const vae4_tensor *block_table, const vae4_tensor *ref_counts,
+                                   const vae4_tensor *moves, uint32_t *dev_status,
+                                   vae4_stream stream);
 
 #ifdef __cplusplus
 }
