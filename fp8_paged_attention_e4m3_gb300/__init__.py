@@ -56,6 +56,7 @@ EXPORTS = (
     "verify_attn_e4m3_copy_pages", "verify_attn_e4m3_fork_pages",
     "verify_attn_e4m3_resize_pages", "verify_attn_e4m3_pages_workspace_bytes",
     "verify_attn_e4m3_compact_pages",
+    "verify_attn_e4m3_chunk", "verify_attn_e4m3_chunk_workspace_bytes",
 )
 
 NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -147,6 +148,7 @@ def load(build_if_stale: bool = True):
         for name, args in (("append", [VP] * 9 + [I, VP]),
                            ("block_scaled", [VP] * 9 + [O]),
                            ("sparse", [VP] * 10 + [O]),
+                           ("chunk", [VP] * 9 + [O]),
                            ("block_scores", [VP] * 6 + [I, F, VP, I, VP]),
                            ("select_blocks", [VP] * 3 + [I, I, I, VP, VP]),
                            ("copy_pages", [VP] * 7), ("fork_pages", [VP] * 5),
@@ -158,6 +160,8 @@ def load(build_if_stale: bool = True):
         lib.verify_attn_e4m3_block_scaled_workspace_bytes.restype = ctypes.c_int64
         lib.verify_attn_e4m3_sparse_workspace_bytes.argtypes = [ctypes.c_int] * 9
         lib.verify_attn_e4m3_sparse_workspace_bytes.restype = ctypes.c_int64
+        lib.verify_attn_e4m3_chunk_workspace_bytes.argtypes = [ctypes.c_int] * 7
+        lib.verify_attn_e4m3_chunk_workspace_bytes.restype = ctypes.c_int64
         lib.verify_attn_e4m3_pages_workspace_bytes.argtypes = [ctypes.c_int64]
         lib.verify_attn_e4m3_pages_workspace_bytes.restype = ctypes.c_int64
         _lib = lib
@@ -598,6 +602,40 @@ def alloc_sparse_workspace(B, Hq, Hkv, Qmax, D, max_seq_len, block_tokens, block
     256-B aligned)."""
     import torch
     n = sparse_workspace_bytes(B, Hq, Hkv, Qmax, D, max_seq_len, block_tokens, blocks)
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+# ----------------------------------------------------------------------------
+# chunks of new tokens
+# ----------------------------------------------------------------------------
+def verify_attn_e4m3_chunk(q, k_cache, v_cache, block_table, seq_lens, scales, out, workspace, *,
+                           softmax_scale: float = 0.0, max_seq_len: int = 0, num_sms: int = 0,
+                           flags: int = 0, stream=None):
+    """Attention of each sequence's last q tokens (f16 or bf16 [B][Qmax][Hq][D],
+    up to 65536 of them, such as a prompt) over its paged cache, into ``out``.
+    ``scales``: f32 [Hkv][2], or the block scales of a block-scaled cache.
+    ``workspace`` from alloc_chunk_workspace.  See the header."""
+    opt = Options(softmax_scale, 0, max_seq_len, num_sms, flags, 0)
+    _call("verify_attn_e4m3_chunk", (q, k_cache, v_cache, block_table, seq_lens, scales, out,
+                                     workspace), (), stream, flags, opt)
+    return out
+
+
+def verify_attn_e4m3_chunk_workspace_bytes(B, Hq, Hkv, Qmax, D, max_seq_len, num_sms=0) -> int:
+    n = load().verify_attn_e4m3_chunk_workspace_bytes(B, Hq, Hkv, Qmax, D, max_seq_len, num_sms)
+    if n < 0:
+        raise Vae4Error(int(n), "chunk_workspace_bytes")
+    return int(n)
+
+
+chunk_workspace_bytes = verify_attn_e4m3_chunk_workspace_bytes
+
+
+def alloc_chunk_workspace(B, Hq, Hkv, Qmax, D, max_seq_len, device=None):
+    """A zeroed workspace for verify_attn_e4m3_chunk (torch allocation, 256-B
+    aligned)."""
+    import torch
+    n = chunk_workspace_bytes(B, Hq, Hkv, Qmax, D, max_seq_len)
     return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
 
 

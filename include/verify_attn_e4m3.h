@@ -64,7 +64,7 @@ enum vae4_dtype {
   VAE4_I32 = 2,
   VAE4_F16 = 3,
   VAE4_F32 = 4,
-  VAE4_BF16 = 5 /* verify_attn_e4m3_append's new rows only */
+  VAE4_BF16 = 5 /* verify_attn_e4m3_append's new rows, verify_attn_e4m3_chunk's queries */
 };
 
 /* A strided view.  `data` is a device pointer unless an entry point says
@@ -623,6 +623,53 @@ int64_t verify_attn_e4m3_block_scaled_workspace_bytes(int B, int Hq, int Hkv, in
 int64_t verify_attn_e4m3_sparse_workspace_bytes(int B, int Hq, int Hkv, int Qmax, int D,
                                                 int max_seq_len, int block_tokens, int blocks,
                                                 int num_sms);
+
+/*
+ * verify_attn_e4m3_chunk -- attention of a chunk of new tokens: any number of
+ * queries per sequence, such as a prompt or a part of it, over the paged cache that
+ * already holds their keys.  (No counterpart on the pages: an addition of this
+ * library.)
+ *
+ *     z_t = softmax_scale * s_K * q . dec(K_t),  t = 0 .. L - q + i for query i
+ *     out = sum_t e^(z_t - max z) s_V dec(V_t) / sum_t e^(z_t - max z)
+ *
+ *  q           F16 or BF16 [B][Qmax][Hq][D], D in {64, 128, 256}, Qmax <= 65536;
+ *              stride[3] == 1, other strides multiples of 8 elements, 16-byte
+ *              aligned.  Rows i < q of sequence b are its last q tokens; the others
+ *              are padding and are not read.
+ *  k_cache, v_cache, block_table, seq_lens: as for verify_attn_e4m3_kv.
+ *  scales      F32 [Hkv][2] = (s_K, s_V) per KV head, or the block scales of a
+ *              block-scaled cache, F32 [n_pages][2][Hkv][page / S]; within
+ *              2^-40 .. 2^40 (others: BAD_SCALE).
+ *  out         as q (its type and shape), no two elements in one place.  Padding
+ *              rows are left as they were; rows i < q of sequences without tokens
+ *              or with invalid lengths get zeros.
+ *  workspace   at least verify_attn_e4m3_chunk_workspace_bytes(...) bytes; its first
+ *              word is the status word, as for verify_attn_e4m3.
+ *  opt         as for verify_attn_e4m3_block_scaled: partition_tokens must be 0
+ *              (VAE4_ERR_PARTITION); VAE4_FLAG_WARP_MMA and hilo_pv:
+ *              VAE4_ERR_UNSUPPORTED.
+ * A query that sees a token in an invalid page or block gives zeros (BAD_BLOCK,
+ * BAD_SCALE); the others of the sequence are not concerned.  A query with a score of
+ * NaN or +infinity gives a row of NaN, one whose scores are all -infinity zeros.
+ * Scores, sums and weighted sums are FP32 and a weight enters its product in FP16, as
+ * for verify_attn_e4m3_block_scaled and with its bound; K enters the scores exactly,
+ * as FP16 or (with BF16 queries) BF16.
+ * The batch is divided evenly among the SMs on the device, from the lengths of the
+ * call, long contexts of few queries too.  Repeated calls give the same bits.
+ */
+int verify_attn_e4m3_chunk(const vae4_tensor *q, const vae4_tensor *k_cache,
+                           const vae4_tensor *v_cache, const vae4_tensor *block_table,
+                           const vae4_tensor *seq_lens, const vae4_tensor *scales,
+                           const vae4_tensor *out, const vae4_tensor *workspace,
+                           vae4_stream stream, const vae4_options *opt);
+
+/* Bytes of workspace of a verify_attn_e4m3_chunk call: the status word, and for each
+ * SM (up to 1024; fewer if the batch has fewer tiles of 128 keys) 32 bytes and two
+ * FP32 partial states, (max, sum) and unnormalised P.V of 256 rows (D = 256: 128).
+ * Arguments and errors as verify_attn_e4m3_workspace_bytes. */
+int64_t verify_attn_e4m3_chunk_workspace_bytes(int B, int Hq, int Hkv, int Qmax, int D,
+                                               int max_seq_len, int num_sms);
 
 /*
  * ---------------------------------------------------------------------------
