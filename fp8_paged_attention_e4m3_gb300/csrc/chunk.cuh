@@ -25,15 +25,19 @@ template <int D>
 struct Cfg {
   static constexpr int MT = D <= 128 ? 2 : 1;  // row tiles
   static constexpr int R = MT * 128;           // rows of a unit
+  static constexpr int RING = 4;               // pieces held, of K and of V
   static constexpr int NC = D / 64;            // 16 KB pieces of a K or V tile
   static constexpr int KPC = 128 / NC;         // keys per piece of V
-  static constexpr int RING = 4;               // pieces held, of K and of V
   static constexpr int PIECE = 16384;
   static constexpr int QT = 128 * D * 2;       // one tile of queries
   static constexpr int NSW = 4 * MT;           // softmax warps
-  // warps: softmax, K decoders (4), V decoders (4), MMA, plan
-  static constexpr int W_K = NSW, W_V = NSW + 4, W_MMA = NSW + 8, W_PLAN = NSW + 9;
-  static constexpr int NTHREADS = 32 * (NSW + 10);
+  // warps: softmax, decoders, MMA, plan; up to 16 in all leave each 128 registers
+  static constexpr int ND = MT == 2 ? 6 : 8;
+  static constexpr int W_DEC = NSW, W_MMA = NSW + ND, W_PLAN = W_MMA + 1;
+  static constexpr int NTHREADS = 32 * (W_PLAN + 1);
+  // A decoder that waits for a place has passed the one before it of any other warp's
+  // (no more pieces are under way than the rings hold), so parities are unambiguous.
+  static_assert(ND <= 2 * RING, "decoders");
   // TMEM columns: scores (and weights in their place), accumulators
   static constexpr int SCOL = 0, OCOL = 256;
   static constexpr int NSEG = 4, NGRP = 4;     // segments, groups of four tiles held
@@ -205,9 +209,10 @@ static __device__ __noinline__ Segment plan_next(const ChunkParams &p, int R, in
 }
 
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ uint4 load_raw(const uint8_t *p, int wide) {
+template <bool WIDE>
+__device__ __forceinline__ uint4 load_raw(const uint8_t *p) {
   uint4 v;
-  if (wide) {
+  if constexpr (WIDE) {
     asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
@@ -241,6 +246,28 @@ __device__ __forceinline__ uint32_t pack16(float a, float b, int bf16) {
   return pack_half2(a, b);
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
+      " add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
 template <int D>
 __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid_constant__ ChunkParams p) {
   using C = Cfg<D>;
@@ -264,10 +291,9 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
 
   if (tid < C::NBARS) {
     uint32_t cnt = 1;
-    if (tid >= C::B_SEGE && tid < C::B_SEGE + C::NSEG) cnt = C::NSW + 9;
+    if (tid >= C::B_SEGE && tid < C::B_SEGE + C::NSEG) cnt = C::NSW + C::ND + 1;
     if (tid >= C::B_INFOF && tid < C::B_INFOF + C::NGRP) cnt = 32;
-    if (tid >= C::B_INFOE && tid < C::B_INFOE + C::NGRP) cnt = C::NSW + 8;
-    if ((tid >= C::B_KF && tid < C::B_KF + C::RING) || (tid >= C::B_VF && tid < C::B_VF + C::RING)) cnt = 4;
+    if (tid >= C::B_INFOE && tid < C::B_INFOE + C::NGRP) cnt = C::NSW + C::ND;
     if ((tid >= C::B_QF && tid < C::B_QF + 2) || (tid >= C::B_PF && tid < C::B_PF + 2) ||
         (tid >= C::B_OE && tid < C::B_OE + 2))
       cnt = 128;
@@ -346,167 +372,158 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
     }
   } else if (warp == C::W_MMA) {
     // =============================== the products, issued by one elected lane
+    // (what the issue depends on stays the same for the warp, in uniform registers, and
+    // ring slots follow from a tile's number: the issue is one warp's serial code)
     const uint32_t id_qk = tc::idesc_f16(128, 128, 0, 0) | (p.bf16 ? (1u << 7 | 1u << 10) : 0u);
     constexpr uint32_t id_pv = tc::idesc_f16(128, D, 0, 1);
-    int ns = 0, nk = 0, nv = 0;  // segments, pieces of K and V
-    int nt[2] = {0, 0};          // score tiles issued (MT = 2: per row tile; else per buffer)
-    int np[2] = {0, 0};          // weight tiles consumed
-    int nq[2] = {0, 0};          // segments of each row tile
+    const uint64_t dq = tc::smem_desc(sQ, 16, 1024), dk = tc::smem_desc(sK, 16, 1024),
+                   dv = tc::smem_desc(sV, C::KPC * 128, 1024);
+    constexpr int TPR = C::RING / C::NC;  // tiles that a ring holds
+    int ns = 0;
+    uint32_t kt = 0, vt = 0;     // tiles of K and V taken
+    // parities, a bit each: weight tiles taken from a buffer, segments of a row tile; and
+    // whether a row tile has had one
+    uint32_t np = 0, nq = 0, had = 0;
+    uint32_t buf = 0;            // MT = 1: the next buffer for scores
     bool ok = true;
+    // scores of row tile t into buffer s from the next tile of K
+    auto scores = [&](auto t_, uint32_t s, bool last) {
+      constexpr int t = decltype(t_)::value;
+      const uint32_t r = kt % TPR, ph = (kt / TPR) & 1;
+#pragma unroll
+      for (int c = 0; c < C::NC; ++c) {
+        if (t == 0) ok = ok && warp_wait(bar(C::B_KF + r * C::NC + c), ph);
+        tc::tc_fence_after();
+        if (ok && tc::elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc::mma_ss(C::SCOL + s * 128, dq + (t * C::QT + c * 16384) / 16 + 2 * k,
+                       dk + (r * C::NC + c) * (C::PIECE / 16) + 2 * k, id_qk, c > 0 || k > 0);
+          if (last) tc::mma_commit(bar(C::B_KE + r * C::NC + c));
+          if (c == C::NC - 1) tc::mma_commit(bar(C::B_SF + s));
+        }
+        __syncwarp();
+      }
+      mma_issued = true;
+      if (last) ++kt;
+    };
+    // the accumulator of row tile t takes the weights in buffer s
+    auto values = [&](auto t_, uint32_t s, bool first, bool last) {
+      constexpr int t = decltype(t_)::value;
+      const uint32_t r = vt % TPR, ph = (vt / TPR) & 1;
+      ok = ok && warp_wait(bar(C::B_PF + s), (np >> s) & 1);
+      np ^= 1u << s;
+      if (first && ((had >> t) & 1)) ok = ok && warp_wait(bar(C::B_OE + t), ((nq >> t) & 1) ^ 1);
+#pragma unroll
+      for (int c = 0; c < C::NC; ++c) {
+        if (t == 0) ok = ok && warp_wait(bar(C::B_VF + r * C::NC + c), ph);
+        tc::tc_fence_after();
+        if (ok && tc::elect_one()) {
+#pragma unroll
+          for (int k = 0; k < C::KPC / 16; ++k)
+            tc::mma_ts(C::OCOL + t * D, C::SCOL + s * 128 + (c * (C::KPC / 16) + k) * 8,
+                       dv + (r * C::NC + c) * (C::PIECE / 16) + 128 * k, id_pv, !first || c > 0 || k > 0);
+          if (last) tc::mma_commit(bar(C::B_VE + r * C::NC + c));
+          if (c == C::NC - 1) tc::mma_commit(bar(C::B_PV + s));
+        }
+        __syncwarp();
+      }
+      if (last) ++vt;
+    };
+    constexpr std::integral_constant<int, 0> T0{};
+    constexpr std::integral_constant<int, C::MT - 1> T1{};
     while (ok) {
       if (!(ok = warp_wait(bar(C::B_SEGF + ns % C::NSEG), (ns / C::NSEG) & 1))) break;
-      const int j0 = seg_s[ns % C::NSEG].j0, j1 = seg_s[ns % C::NSEG].j1;
-      const int live = C::MT == 2 && seg_s[ns % C::NSEG].rows > 128 ? 2 : 1;
+      const Segment &sg = seg_s[ns % C::NSEG];
+      const int tiles = __shfl_sync(0xffffffffu, sg.j1 - sg.j0, 0);
+      const bool two = C::MT == 2 && __shfl_sync(0xffffffffu, sg.rows, 0) > 128;
       __syncwarp();
       if (tc::elect_one()) tc::mbar_arrive(bar(C::B_SEGE + ns % C::NSEG));
       ++ns;
-      if (j1 <= j0) break;
-      // scores of row tile t into buffer s from the next tile of K
-      auto scores = [&](int t, int s, bool last) -> bool {
-  #pragma unroll
-        for (int c = 0; c < C::NC; ++c) {
-          const int x = nk + c;
-          if (t == 0 && !warp_wait(bar(C::B_KF + x % C::RING), (x / C::RING) & 1)) return false;
-          tc::tc_fence_after();
-          if (tc::elect_one()) {
-            const uint64_t a = tc::smem_desc(sQ + t * C::QT + c * 16384, 16, 1024);
-            const uint64_t b = tc::smem_desc(sK + (x % C::RING) * C::PIECE, 16, 1024);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              tc::mma_ss(C::SCOL + s * 128, a + 2 * k, b + 2 * k, id_qk, c > 0 || k > 0);
-            if (last) tc::mma_commit(bar(C::B_KE + x % C::RING));
-            if (c == C::NC - 1) tc::mma_commit(bar(C::B_SF + s));
+      if (tiles <= 0) break;
+      ok = warp_wait(bar(C::B_QF), nq & 1);
+      if (two) ok = ok && warp_wait(bar(C::B_QF + 1), (nq >> 1) & 1);
+#pragma unroll 1
+      for (int j = -1; j < tiles && ok; ++j) {
+        const bool more = j + 1 < tiles;
+        if constexpr (C::MT == 2) {
+          if (j >= 0) values(T0, 0, j == 0, !two);
+          if (more) scores(T0, 0, !two);
+          if (two) {
+            if (j >= 0) values(T1, 1, j == 0, true);
+            if (more) scores(T1, 1, true);
           }
-          __syncwarp();
-        }
-        mma_issued = true;
-        ++nt[s];
-        if (last) nk += C::NC;
-        return true;
-      };
-      // the accumulator of row tile t takes the weights in buffer s
-      auto values = [&](int t, int s, bool first, bool last) -> bool {
-        if (!warp_wait(bar(C::B_PF + s), np[s] & 1)) return false;
-        ++np[s];
-        if (first && nq[t] > 0 && !warp_wait(bar(C::B_OE + t), (nq[t] - 1) & 1)) return false;
-#pragma unroll
-        for (int c = 0; c < C::NC; ++c) {
-          const int x = nv + c;
-          if (t == 0 && !warp_wait(bar(C::B_VF + x % C::RING), (x / C::RING) & 1)) return false;
-          tc::tc_fence_after();
-          if (tc::elect_one()) {
-            const uint64_t b = tc::smem_desc(sV + (x % C::RING) * C::PIECE, C::KPC * 128, 1024);
-#pragma unroll
-            for (int k = 0; k < C::KPC / 16; ++k)
-              tc::mma_ts(C::OCOL + t * D, C::SCOL + s * 128 + (c * (C::KPC / 16) + k) * 8, b + 128 * k,
-                         id_pv, !first || c > 0 || k > 0);
-            if (last) tc::mma_commit(bar(C::B_VE + x % C::RING));
-            if (c == C::NC - 1) tc::mma_commit(bar(C::B_PV + s));
-          }
-          __syncwarp();
-        }
-        if (last) nv += C::NC;
-        return true;
-      };
-      for (int t = 0; t < live && ok; ++t) ok = warp_wait(bar(C::B_QF + t), nq[t] & 1);
-      if constexpr (C::MT == 2) {
-        for (int t = 0; t < live && ok; ++t) ok = scores(t, t, t == live - 1);
-        for (int j = j0; j < j1 && ok; ++j)
-          for (int t = 0; t < live && ok; ++t) {
-            ok = values(t, t, j == j0, t == live - 1);
-            if (ok && j + 1 < j1) ok = scores(t, t, t == live - 1);
-          }
-      } else {
-        int s = nt[0] == nt[1] ? 0 : 1;  // buffers alternate through all segments
-        ok = ok && scores(0, s, true);
-        for (int j = j0; j < j1 && ok; ++j, s ^= 1) {
-          if (j + 1 < j1) ok = scores(0, s ^ 1, true);
-          ok = ok && values(0, s, j == j0, true);
+        } else {  // buffers alternate through all segments
+          if (more) scores(T0, buf, true);
+          if (j >= 0) values(T0, buf ^ 1, j == 0, true);
+          if (more) buf ^= 1;
         }
       }
-      for (int t = 0; t < live; ++t) ++nq[t];
+      nq ^= two ? 3u : 1u;
+      had |= two ? 3u : 1u;
     }
-  } else if (warp >= C::W_K) {
-    // =============================== decoders: 4 lanes per 64-wide row piece
-    const bool isv = warp >= C::W_V;
-    const int w = (warp - C::W_K) & 3, r8 = lane >> 2, u = lane & 3;
-    const uint8_t *base = (isv ? p.v_base : p.k_base) + 16 * u;
-    const int64_t ts = isv ? p.v_ts : p.k_ts;
-    const int64_t off0 = r8 * ts, off1 = (8 + r8) * ts;
-    const uint32_t ring = isv ? sV : sK;
-    const int fullb = isv ? C::B_VF : C::B_KF, emptyb = isv ? C::B_VE : C::B_KE;
-    const uint32_t dst = (uint32_t)(32 * w + r8) * 128 + 0u;
+  } else if (warp >= C::W_DEC) {
+    // =============================== decoders: a warp per piece
+    // Pieces of K and V in the order K, V of tile 0, K, V of tile 1, ... go round the
+    // warps.  A piece's 128 rows of 64 bytes are requested at once, 4 lanes per row, and
+    // decoded when they are there and their place is free: the other warps' pieces are
+    // under way meanwhile.
+    const int r8 = lane >> 2, u = lane & 3;
+    const uint32_t dst = (uint32_t)r8 * 128;
     const uint32_t x0 = (uint32_t)((2 * u) ^ r8) << 4, x1 = (uint32_t)((2 * u + 1) ^ r8) << 4;
-    const int wide = p.wide;
-    auto decode = [&](auto mode) {
-      constexpr Decode M = decltype(mode)::value;
-      constexpr int AHEAD = 3;  // pieces requested before the one that is decoded
-      uint4 raw[AHEAD][4];
-      bool have[AHEAD];
+    const uint8_t *kb = p.k_base + 16 * u + r8 * p.k_ts, *vb = p.v_base + 16 * u + r8 * p.v_ts;
+    const int64_t k8 = 8 * p.k_ts, v8 = 8 * p.v_ts;
+    constexpr int PPT = 2 * C::NC;  // pieces per tile
+    int ns = 0, ng = 0;
+    uint32_t tiles = 0;             // before the segment
+    int turn = warp - C::W_DEC;     // pieces until the warp's next one
+    bool ok = true;
+    while (ok) {
+      if (!(ok = warp_wait(bar(C::B_SEGF + ns % C::NSEG), (ns / C::NSEG) & 1))) break;
+      const Segment &sg = seg_s[ns % C::NSEG];
+      const int j0 = sg.j0, n = sg.j1 - sg.j0, kend = sg.kend;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar(C::B_SEGE + ns % C::NSEG));
+      ++ns;
+      if (n <= 0) break;
+      for (int g0 = 0; g0 < n && ok; g0 += 4, ++ng) {
+        const int pieces = min(4, n - g0) * PPT;
+        if (!(ok = warp_wait(bar(C::B_INFOF + ng % C::NGRP), (ng / C::NGRP) & 1))) break;
+#pragma unroll 1
+        for (; turn < pieces; turn += C::ND) {
+          const int jl = turn / PPT, pc = turn % PPT, c = pc % C::NC;
+          const bool isv = pc >= C::NC;
+          const uint32_t x = (tiles + g0 + jl) * C::NC + c;  // the piece's number among K's or V's
+          // rows run over 128 keys of 64 channels (K), or over the piece's keys of
+          // 64 channels after another (V)
+          const Box *bx = box_s + (ng % C::NGRP) * 32 + jl * 8 + (isv ? c * (C::KPC / 16) : 0);
+          const int left = kend - (j0 + g0 + jl) * kTile - (isv ? c * C::KPC : 0) - r8;  // keys from row r8 on
+          const uint8_t *base = (isv ? vb : kb + 64 * c);
+          const int64_t s8 = isv ? v8 : k8;
+          uint4 raw[16];
+          auto request = [&](auto wide_) {
 #pragma unroll
-      for (int a = 0; a < AHEAD; ++a) have[a] = false;
-      int ns = 0, ng = 0;            // segments and groups begun
-      int j = 0, j0 = 0, j1 = 0, kend = 0, c = 0;
-      bool open = false, more = true, ok = true;
-      // request the next piece
-      auto request = [&](uint4 (&r)[4]) -> bool {
-        if (!more) return false;
-        if (!open) {
-          if (!(ok = warp_wait(bar(C::B_SEGF + ns % C::NSEG), (ns / C::NSEG) & 1))) return more = false;
-          const Segment &s = seg_s[ns % C::NSEG];
-          j = j0 = s.j0;
-          j1 = s.j1;
-          kend = s.kend;
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(bar(C::B_SEGE + ns % C::NSEG));
-          ++ns;
-          if (j1 <= j0) return more = false;
-          open = true;
-          c = 0;
-        }
-        const int jl = j - j0, g = ng % C::NGRP;
-        if (c == 0 && (jl & 3) == 0 && !(ok = warp_wait(bar(C::B_INFOF + g), (ng / C::NGRP) & 1)))
-          return more = false;
-        // the warp's 32 rows of the piece: 16-key boxes 2w, 2w + 1 of K; of V rows
-        // run over the piece's keys, then over groups of 64 channels
-        const int key_w = isv ? c * C::KPC + (32 * w) % C::KPC : 32 * w;
-        const int d0 = isv ? 64 * ((32 * w) / C::KPC) : 64 * c;
-        const Box *bx = box_s + g * 32 + (jl & 3) * 8 + (key_w >> 4);
-        const int key = j * kTile + key_w + r8;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const long long at = isv ? bx[i >> 1].v : bx[i >> 1].k;
-          r[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (at >= 0 && key + 8 * i < kend) r[i] = load_raw(base + at + (i & 1 ? off1 : off0) + d0, wide);
-        }
-        if (++c == C::NC) {
-          c = 0;
-          ++j;
-          if (j == j1 || ((j - j0) & 3) == 0) {
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(bar(C::B_INFOE + g));
-            ++ng;
-          }
-          open = j < j1;
-        }
-        return true;
-      };
-      int n = 0;  // pieces decoded
-      for (bool any = true; any;) {
-        any = false;
-#pragma unroll
-        for (int a = 0; a < AHEAD; ++a) {
-          if (have[a]) {
-            const int slot = n % C::RING;
-            if (n >= C::RING && !(ok = warp_wait(bar(emptyb + slot), (n / C::RING - 1) & 1))) {
-              any = false;
-              more = false;
-              break;
+            for (int i = 0; i < 16; ++i) {
+              const int iv = i % (C::KPC / 8), dv0 = 64 * (i / (C::KPC / 8));  // V: row in the channels' group
+              const int b16 = isv ? iv >> 1 : i >> 1;
+              const long long at = isv ? bx[b16].v : bx[b16].k;
+              const bool live = at >= 0 && (isv ? 8 * iv : 8 * i) < left;
+              raw[i] = make_uint4(0u, 0u, 0u, 0u);
+              if (live) raw[i] = load_raw<decltype(wide_)::value>(base + at + (i & 1 ? s8 : 0) + (isv ? dv0 : 0));
             }
-            const uint32_t to = ring + slot * C::PIECE + dst;
+          };
+          if (p.wide)
+            request(std::true_type{});
+          else
+            request(std::false_type{});
+          const uint32_t slot = x % C::RING, use = x / C::RING;
+          if (use > 0 && !(ok = warp_wait(bar((isv ? C::B_VE : C::B_KE) + slot), (use - 1) & 1))) break;
+          const uint32_t to = (isv ? sV : sK) + slot * C::PIECE + dst;
+          auto decode = [&](auto mode) {
+            constexpr Decode M = decltype(mode)::value;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t v[4] = {raw[a][i].x, raw[a][i].y, raw[a][i].z, raw[a][i].w};
+            for (int i = 0; i < 16; ++i) {
+              const uint32_t v[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
               uint32_t o[8];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
@@ -516,25 +533,26 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
               st_shared16(to + i * 1024 + x0, o[0], o[1], o[2], o[3]);
               st_shared16(to + i * 1024 + x1, o[4], o[5], o[6], o[7]);
             }
-            tc::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(bar(fullb + slot));
-            ++n;
+          };
+          if (!isv && p.bf16) {
+            if (p.e5m2)
+              decode(std::integral_constant<Decode, Decode::E5M2_BF16>{});
+            else
+              decode(std::integral_constant<Decode, Decode::E4M3_BF16>{});
+          } else if (p.e5m2) {
+            decode(std::integral_constant<Decode, Decode::E5M2_F16>{});
+          } else {
+            decode(std::integral_constant<Decode, Decode::E4M3_F16>{});
           }
-          have[a] = request(raw[a]);
-          any |= have[a];
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(bar((isv ? C::B_VF : C::B_KF) + slot));
         }
+        turn -= pieces;
+        __syncwarp();
+        if (ok && lane == 0) tc::mbar_arrive(bar(C::B_INFOE + ng % C::NGRP));
       }
-    };
-    if (!isv && p.bf16) {
-      if (p.e5m2)
-        decode(std::integral_constant<Decode, Decode::E5M2_BF16>{});
-      else
-        decode(std::integral_constant<Decode, Decode::E4M3_BF16>{});
-    } else if (p.e5m2) {
-      decode(std::integral_constant<Decode, Decode::E5M2_F16>{});
-    } else {
-      decode(std::integral_constant<Decode, Decode::E4M3_F16>{});
+      tiles += n;
     }
   } else {
     // =============================== softmax: thread = row of tile t
@@ -600,22 +618,36 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
         const int k0 = j * kTile;
         const bool masked = k0 + kTile - 1 > min_lim;
         const uint32_t sc = tbase + lane_off + C::SCOL + sb * 128;
-        float mx = -kInf;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t r[32];
-          tc::tmem_ld32(sc + 32 * c, r);
-          tc::tmem_wait_ld();
-          if (masked) {
+        if (masked) {  // what the row does not see becomes -infinity in place
+          int see = lim - k0;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c, see -= 32) {
+            uint32_t x[32];
+            tc::tmem_ld32(sc + 32 * c, x);
+            tc::tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (k0 + 32 * c + e > lim) r[e] = 0xff800000u;
+              if (e > see) x[e] = 0xff800000u;
+            tc::tmem_st32(sc + 32 * c, x);
           }
+          tc::tmem_wait_st();
+        }
+        // the row's scores, 32 at a time, the next requested before these are looked at
+        uint32_t r[2][32];
+        float mx = -kInf;
+        tc::tmem_ld32(sc, r[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t(&x)[32] = r[c & 1];
+          tc::tmem_wait_ld();
+          tc::tmem_ld32(sc + 32 * ((c + 1) & 3), r[(c + 1) & 1]);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            float mb = __uint_as_float(r[16 * k]);
+            auto score = [&](int e) -> float { return __uint_as_float(x[16 * k + e]); };
+            float mb = max3(score(0), score(1), score(2));
 #pragma unroll
-            for (int e = 1; e < 16; ++e) mb = fmaxf(mb, __uint_as_float(r[16 * k + e]));
+            for (int e = 3; e < 15; e += 2) mb = max3(mb, score(e), score(e + 1));
+            mb = fmaxf(mb, score(15));
             mx = fmaxf(mx, fmaf(mb, bx[2 * c + k].a, bx[2 * c + k].g));
           }
         }
@@ -641,32 +673,36 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
           }
         }
         const float base = m == -kInf ? 0.f : m;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t r[32], h[16];
-          tc::tmem_ld32(sc + 32 * c, r);
-          tc::tmem_wait_ld();
-          if (masked) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (k0 + 32 * c + e > lim) r[e] = 0xff800000u;
-          }
+        // weights of 32 keys from y into the place of 16 scores that have been read
+        auto weigh = [&](const uint32_t (&y)[32], int c) {
+          uint32_t h[16];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const Box &x = bx[2 * c + k];
-            const float A = x.a, B = x.g - base;
-            float sum = 0.f;
+            const float4 x = *reinterpret_cast<const float4 *>(&bx[2 * c + k].a);  // a, g, inv, bad
+            const float2 A = make_float2(x.x, x.x), B = make_float2(x.y - base, x.y - base);
+            float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float e0 = fast_exp2(fmaf(__uint_as_float(r[16 * k + 2 * e]), A, B));
-              const float e1 = fast_exp2(fmaf(__uint_as_float(r[16 * k + 2 * e + 1]), A, B));
-              sum += e0 + e1;
-              h[8 * k + e] = pack_half2(e0, e1);
+              float2 w = fma2(make_float2(__uint_as_float(y[16 * k + 2 * e]), __uint_as_float(y[16 * k + 2 * e + 1])),
+                              A, B);
+              w.x = fast_exp2(w.x);
+              w.y = fast_exp2(w.y);
+              sum = add2(sum, w);
+              h[8 * k + e] = pack_half2(w.x, w.y);
             }
-            l = fmaf(sum, x.inv, l);
-            if (x.bad && k0 + 16 * (2 * c + k) <= lim) bad = true;
+            l = fmaf(sum.x + sum.y, x.z, l);
+            if (__float_as_int(x.w) && k0 + 16 * (2 * c + k) <= lim) bad = true;
           }
           tc::tmem_st16(sc + 16 * c, h);
+        };
+#pragma unroll 1
+        for (int c = 0; c < 4; c += 2) {
+          tc::tmem_wait_ld();
+          tc::tmem_ld32(sc + 32 * (c + 1), r[1]);
+          weigh(r[0], c);
+          tc::tmem_wait_ld();
+          if (c == 0) tc::tmem_ld32(sc + 64, r[0]);
+          weigh(r[1], c + 1);
         }
         tc::tmem_wait_st();
         tc::tc_fence_before();
