@@ -29,6 +29,9 @@ struct Cfg {
   static constexpr int NC = D / 64;            // 16 KB pieces of a K or V tile
   static constexpr int KPC = 128 / NC;         // keys per piece of V
   static constexpr int PIECE = 16384;
+  // pieces that are passed on and given back together: a wait or an arrival between the
+  // products costs the tensor cores some 60 cycles
+  static constexpr int GR = NC < 2 ? 1 : 2, NG = NC / GR;
   static constexpr int QT = 128 * D * 2;       // one tile of queries
   static constexpr int NSW = 4 * MT;           // softmax warps
   // warps: softmax, decoders, MMA, plan; up to 16 in all leave each 128 registers
@@ -49,7 +52,7 @@ struct Cfg {
                        B_PF = B_SF + 2, B_PV = B_PF + 2, B_OE = B_PV + 2, B_DRAIN = B_OE + 2,
                        NBARS = B_DRAIN + 1;
   static constexpr int S_SCAL = 512, S_SEG = 576, S_INFO = S_SEG + NSEG * 64,
-                       S_ROW = S_INFO + NGRP * 32 * 32, SMALL = S_ROW + R * 8;
+                       S_ROW = S_INFO + NGRP * 4 * 256, SMALL = S_ROW + R * 8;
   static constexpr int SMEM = OFF_SMALL + SMALL + 1024;
   static_assert(NBARS * 8 <= S_SCAL && SMEM <= 232448, "shared memory");
 };
@@ -63,13 +66,14 @@ struct Segment {
 };
 static_assert(sizeof(Segment) == 64, "layout");
 
-// 16 keys: where their rows start, their scales
-struct alignas(16) Box {
-  long long k, v;  // offsets from the caches' bases; -1: no keys, or invalid
-  float a, g, inv; // a score in log2 units per raw product, log2 s_V, 1 / s_V
-  int bad;
+// What the roles have to know of a tile, for each of its boxes of 16 keys.
+struct alignas(16) Tile {
+  long long k[8], v[8];  // where the rows start, from the caches' bases; -1: no keys, or invalid
+  float a[8], g[8];      // a score in log2 units per raw product, log2 s_V
+  float inv[8];          // 1 / s_V
+  int bad[8];
 };
-static_assert(sizeof(Box) == 32, "layout");
+static_assert(sizeof(Tile) == 256, "layout");
 
 // ---------------------------------------------------------------------------
 // The plan.  Units are (sequence, KV head, R rows of the chunk's q G rows, query by
@@ -284,7 +288,7 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
   auto bar = [&](int i) -> uint32_t { return sSm + 8u * (uint32_t)i; };
   volatile int *abort_f = reinterpret_cast<volatile int *>(gSm + C::S_SCAL);
   Segment *seg_s = reinterpret_cast<Segment *>(gSm + C::S_SEG);
-  Box *box_s = reinterpret_cast<Box *>(gSm + C::S_INFO);
+  Tile *tile_s = reinterpret_cast<Tile *>(gSm + C::S_INFO);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x;
@@ -294,6 +298,7 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
     if (tid >= C::B_SEGE && tid < C::B_SEGE + C::NSEG) cnt = C::NSW + C::ND + 1;
     if (tid >= C::B_INFOF && tid < C::B_INFOF + C::NGRP) cnt = 32;
     if (tid >= C::B_INFOE && tid < C::B_INFOE + C::NGRP) cnt = C::NSW + C::ND;
+    if ((tid >= C::B_KF && tid < C::B_KF + C::RING) || (tid >= C::B_VF && tid < C::B_VF + C::RING)) cnt = C::GR;
     if ((tid >= C::B_QF && tid < C::B_QF + 2) || (tid >= C::B_PF && tid < C::B_PF + 2) ||
         (tid >= C::B_OE && tid < C::B_OE + 2))
       cnt = 128;
@@ -337,11 +342,9 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
       const int32_t *row = p.bt + (int64_t)s.b * p.bt_sb;
       for (int key0 = s.j0 * kTile; key0 < s.j1 * kTile; key0 += 4 * kTile, ++ng) {
         const int key = key0 + 16 * lane;
-        Box x;
-        x.k = x.v = -1;
-        x.a = x.inv = 1.f;
-        x.g = 0.f;
-        x.bad = 0;
+        long long xk = -1, xv = -1;
+        float xa = 1.f, xg = 0.f, xi = 1.f;
+        int bad = 0;
         if (key < s.kend) {
           const int lp = div16(key, p.page_m), slot = key - lp * p.page;
           const int page = load_dep(row + lp);
@@ -352,21 +355,27 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
             const float sk = load_dep(sp), sv = load_dep(sp + p.s_kv);
             bits = VAE4_STATUS_BAD_SCALE;
             if (sk >= kMinScale && sk <= kMaxScale && sv >= kMinScale && sv <= kMaxScale) {
-              x.k = (long long)page * p.k_ps + slot * p.k_ts + s.h * p.k_hs;
-              x.v = (long long)page * p.v_ps + slot * p.v_ts + s.h * p.v_hs;
-              x.a = p.alpha * sk;
-              x.g = __log2f(sv);
-              x.inv = __fdividef(1.f, sv);
+              xk = (long long)page * p.k_ps + slot * p.k_ts + s.h * p.k_hs;
+              xv = (long long)page * p.v_ps + slot * p.v_ts + s.h * p.v_hs;
+              xa = p.alpha * sk;
+              xg = __log2f(sv);
+              xi = __fdividef(1.f, sv);
               bits = 0;
             }
           }
           if (bits) {
-            x.bad = 1;
+            bad = 1;
             atomicOr(p.status, bits);
           }
         }
         if (ng >= C::NGRP && !(ok = warp_wait(bar(C::B_INFOE + ng % C::NGRP), (ng / C::NGRP - 1) & 1))) break;
-        box_s[(ng % C::NGRP) * 32 + lane] = x;
+        Tile &x = tile_s[(ng % C::NGRP) * 4 + (lane >> 3)];
+        x.k[lane & 7] = xk;
+        x.v[lane & 7] = xv;
+        x.a[lane & 7] = xa;
+        x.g[lane & 7] = xg;
+        x.inv[lane & 7] = xi;
+        x.bad[lane & 7] = bad;
         tc::mbar_arrive(bar(C::B_INFOF + ng % C::NGRP));
       }
     }
@@ -389,18 +398,20 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
     // scores of row tile t into buffer s from the next tile of K
     auto scores = [&](auto t_, uint32_t s, bool last) {
       constexpr int t = decltype(t_)::value;
-      const uint32_t r = kt % TPR, ph = (kt / TPR) & 1;
+      const uint32_t r = kt % TPR * C::NC, ph = (kt / TPR) & 1;
 #pragma unroll
-      for (int c = 0; c < C::NC; ++c) {
-        if (t == 0) ok = ok && warp_wait(bar(C::B_KF + r * C::NC + c), ph);
+      for (int g = 0; g < C::NG; ++g) {
+        const uint32_t x = r + g * C::GR;  // the group's first piece in the ring
+        if (t == 0) ok = ok && warp_wait(bar(C::B_KF + x / C::GR), ph);
         tc::tc_fence_after();
         if (ok && tc::elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc::mma_ss(C::SCOL + s * 128, dq + (t * C::QT + c * 16384) / 16 + 2 * k,
-                       dk + (r * C::NC + c) * (C::PIECE / 16) + 2 * k, id_qk, c > 0 || k > 0);
-          if (last) tc::mma_commit(bar(C::B_KE + r * C::NC + c));
-          if (c == C::NC - 1) tc::mma_commit(bar(C::B_SF + s));
+          for (int k = 0; k < 4 * C::GR; ++k)
+            tc::mma_ss(C::SCOL + s * 128,
+                       dq + (t * C::QT + g * C::GR * 16384) / 16 + (k >> 2) * 1024 + 2 * (k & 3),
+                       dk + x * (C::PIECE / 16) + (k >> 2) * 1024 + 2 * (k & 3), id_qk, g > 0 || k > 0);
+          if (g == C::NG - 1) tc::mma_commit(bar(C::B_SF + s));
+          if (last) tc::mma_commit(bar(C::B_KE + x / C::GR));
         }
         __syncwarp();
       }
@@ -408,23 +419,26 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
       if (last) ++kt;
     };
     // the accumulator of row tile t takes the weights in buffer s
-    auto values = [&](auto t_, uint32_t s, bool first, bool last) {
+    auto values = [&](auto t_, uint32_t s, bool first, bool done, bool last) {
       constexpr int t = decltype(t_)::value;
-      const uint32_t r = vt % TPR, ph = (vt / TPR) & 1;
+      const uint32_t r = vt % TPR * C::NC, ph = (vt / TPR) & 1;
+      constexpr int KP = C::KPC / 16;  // steps of 16 keys per piece
       ok = ok && warp_wait(bar(C::B_PF + s), (np >> s) & 1);
       np ^= 1u << s;
       if (first && ((had >> t) & 1)) ok = ok && warp_wait(bar(C::B_OE + t), ((nq >> t) & 1) ^ 1);
 #pragma unroll
-      for (int c = 0; c < C::NC; ++c) {
-        if (t == 0) ok = ok && warp_wait(bar(C::B_VF + r * C::NC + c), ph);
+      for (int g = 0; g < C::NG; ++g) {
+        const uint32_t x = r + g * C::GR;
+        if (t == 0) ok = ok && warp_wait(bar(C::B_VF + x / C::GR), ph);
         tc::tc_fence_after();
         if (ok && tc::elect_one()) {
 #pragma unroll
-          for (int k = 0; k < C::KPC / 16; ++k)
-            tc::mma_ts(C::OCOL + t * D, C::SCOL + s * 128 + (c * (C::KPC / 16) + k) * 8,
-                       dv + (r * C::NC + c) * (C::PIECE / 16) + 128 * k, id_pv, !first || c > 0 || k > 0);
-          if (last) tc::mma_commit(bar(C::B_VE + r * C::NC + c));
-          if (c == C::NC - 1) tc::mma_commit(bar(C::B_PV + s));
+          for (int k = 0; k < KP * C::GR; ++k)
+            tc::mma_ts(C::OCOL + t * D, C::SCOL + s * 128 + (g * KP * C::GR + k) * 8,
+                       dv + x * (C::PIECE / 16) + (k / KP) * 1024 + 128 * (k % KP), id_pv,
+                       !first || g > 0 || k > 0);
+          if (last) tc::mma_commit(bar(C::B_VE + x / C::GR));
+          if (done && g == C::NG - 1) tc::mma_commit(bar(C::B_PV + s));
         }
         __syncwarp();
       }
@@ -447,15 +461,15 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
       for (int j = -1; j < tiles && ok; ++j) {
         const bool more = j + 1 < tiles;
         if constexpr (C::MT == 2) {
-          if (j >= 0) values(T0, 0, j == 0, !two);
+          if (j >= 0) values(T0, 0, j == 0, !more, !two);
           if (more) scores(T0, 0, !two);
           if (two) {
-            if (j >= 0) values(T1, 1, j == 0, true);
+            if (j >= 0) values(T1, 1, j == 0, !more, true);
             if (more) scores(T1, 1, true);
           }
         } else {  // buffers alternate through all segments
           if (more) scores(T0, buf, true);
-          if (j >= 0) values(T0, buf ^ 1, j == 0, true);
+          if (j >= 0) values(T0, buf ^ 1, j == 0, true, true);
           if (more) buf ^= 1;
         }
       }
@@ -496,7 +510,8 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
           const uint32_t x = (tiles + g0 + jl) * C::NC + c;  // the piece's number among K's or V's
           // rows run over 128 keys of 64 channels (K), or over the piece's keys of
           // 64 channels after another (V)
-          const Box *bx = box_s + (ng % C::NGRP) * 32 + jl * 8 + (isv ? c * (C::KPC / 16) : 0);
+          const Tile &tl = tile_s[(ng % C::NGRP) * 4 + jl];
+          const long long *bx = isv ? tl.v + c * (C::KPC / 16) : tl.k;
           const int left = kend - (j0 + g0 + jl) * kTile - (isv ? c * C::KPC : 0) - r8;  // keys from row r8 on
           const uint8_t *base = (isv ? vb : kb + 64 * c);
           const int64_t s8 = isv ? v8 : k8;
@@ -506,7 +521,7 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
             for (int i = 0; i < 16; ++i) {
               const int iv = i % (C::KPC / 8), dv0 = 64 * (i / (C::KPC / 8));  // V: row in the channels' group
               const int b16 = isv ? iv >> 1 : i >> 1;
-              const long long at = isv ? bx[b16].v : bx[b16].k;
+              const long long at = bx[b16];
               const bool live = at >= 0 && (isv ? 8 * iv : 8 * i) < left;
               raw[i] = make_uint4(0u, 0u, 0u, 0u);
               if (live) raw[i] = load_raw<decltype(wide_)::value>(base + at + (i & 1 ? s8 : 0) + (isv ? dv0 : 0));
@@ -517,7 +532,7 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
           else
             request(std::false_type{});
           const uint32_t slot = x % C::RING, use = x / C::RING;
-          if (use > 0 && !(ok = warp_wait(bar((isv ? C::B_VE : C::B_KE) + slot), (use - 1) & 1))) break;
+          if (use > 0 && !(ok = warp_wait(bar((isv ? C::B_VE : C::B_KE) + slot / C::GR), (use - 1) & 1))) break;
           const uint32_t to = (isv ? sV : sK) + slot * C::PIECE + dst;
           auto decode = [&](auto mode) {
             constexpr Decode M = decltype(mode)::value;
@@ -546,7 +561,7 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
           }
           tc::fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(bar((isv ? C::B_VF : C::B_KF) + slot));
+          if (lane == 0) tc::mbar_arrive(bar((isv ? C::B_VF : C::B_KF) + slot / C::GR));
         }
         turn -= pieces;
         __syncwarp();
@@ -561,31 +576,50 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
     long long *row_s = reinterpret_cast<long long *>(gSm + C::S_ROW) + t * 128;
     int ns = 0, ng = 0, count = 0;
     bool alive = true;
-    // the value product of tile x (of all segments) is done; with two score buffers up
-    // to two of them are under way, so each buffer has a barrier of its own
-    auto values_done = [&](int x) -> bool {
-      return C::MT == 2 ? warp_wait(bar(C::B_PV + t), x & 1)
-                        : warp_wait(bar(C::B_PV + (x & 1)), (x >> 1) & 1);
+    // The products run in the order of their issue.  With two row tiles the value product
+    // of a tile is issued before the scores of the next, so it is done when they are
+    // there, and only a segment's last one has an arrival of its own (of segment n of the
+    // row tile).  With one the scores come first, up to two value products (of tiles x of
+    // all segments) are under way, and each buffer's has one.
+    auto values_done = [&](int x) -> bool { return warp_wait(bar(C::B_PV + (x & 1)), (x >> 1) & 1); };
+    auto last_done = [&](int x, int n) -> bool {
+      return C::MT == 2 ? warp_wait(bar(C::B_PV + t), n & 1) : values_done(x);
     };
+    int nlive = 0;
     for (;;) {
       alive = alive && warp_wait(bar(C::B_SEGF + ns % C::NSEG), (ns / C::NSEG) & 1);
       if (tc::named_bar_or(1 + t, 128, !alive)) break;  // one answer for the four warps
-      const Segment s = seg_s[ns % C::NSEG];
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(bar(C::B_SEGE + ns % C::NSEG));
+      // (the segment's place is given back at its end: what is needed once is read there)
+      const Segment &s = seg_s[ns % C::NSEG];
+      const uint32_t seg_free = bar(C::B_SEGE + ns % C::NSEG);
       ++ns;
-      if (s.j1 <= s.j0) break;
+      const int j0 = s.j0, j1 = s.j1;
+      if (j1 <= j0) break;
       if (t * 128 >= s.rows) {  // no row of this tile: only the groups go by
-        for (int j = s.j0; j < s.j1; j += 4, ++ng) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(seg_free);
+        for (int j = j0; j < j1; j += 4, ++ng) {
           alive = alive && warp_wait(bar(C::B_INFOF + ng % C::NGRP), (ng / C::NGRP) & 1);
           if (alive && lane == 0) tc::mbar_arrive(bar(C::B_INFOE + ng % C::NGRP));
         }
         continue;
       }
-      const int rr = s.row0 + t * 128 + tr, i = rr / p.G;
-      const bool live = t * 128 + tr < s.rows;
-      const long long head = (long long)(s.h * p.G + rr - i * p.G);
-      row_s[tr] = live ? s.b * p.q_sb + i * p.q_si + head * p.q_sh : -1;
+      // the row's query and head, and whether it is one of the unit's
+      auto row_of = [&](int &i, long long &head) -> bool {
+        const int rr = s.row0 + t * 128 + tr;
+        i = rr / p.G;
+        head = s.h * p.G + rr - i * p.G;
+        return t * 128 + tr < s.rows;
+      };
+      int lim;  // the last key that the row sees (rows past the unit's: all, of zeros)
+      {
+        int i;
+        long long head;
+        const bool live = row_of(i, head);
+        row_s[tr] = live ? s.b * p.q_sb + i * p.q_si + head * p.q_sh : -1;
+        lim = live ? s.L - s.q + i : s.kend - 1;
+      }
+      const int min_lim = __reduce_min_sync(0xffffffffu, lim);
       tc::named_bar(1 + t, 128);
       {
         constexpr int QCH = D / 8;  // 16-byte pieces per row
@@ -601,20 +635,22 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
         tc::fence_proxy_async_smem();
         tc::mbar_arrive(bar(C::B_QF + t));
       }
-      // the last key that the row sees (rows past the unit's: all, of zeros)
-      const int lim = live ? s.L - s.q + i : s.kend - 1;
-      const int min_lim = __reduce_min_sync(0xffffffffu, lim);
       float m = -kInf, l = 0.f;
       bool bad = false;
-      for (int j = s.j0; j < s.j1; ++j, ++count) {
-        const int jl = j - s.j0, g = ng % C::NGRP;
+      for (int j = j0; j < j1; ++j, ++count) {
+        const int jl = j - j0, g = ng % C::NGRP;
         if ((jl & 3) == 0) alive = alive && warp_wait(bar(C::B_INFOF + g), (ng / C::NGRP) & 1);
+        const Tile &tl = tile_s[g * 4 + (jl & 3)];
+        float a8[8], g8[8];
+        *reinterpret_cast<float4 *>(&a8[0]) = *reinterpret_cast<const float4 *>(&tl.a[0]);
+        *reinterpret_cast<float4 *>(&a8[4]) = *reinterpret_cast<const float4 *>(&tl.a[4]);
+        *reinterpret_cast<float4 *>(&g8[0]) = *reinterpret_cast<const float4 *>(&tl.g[0]);
+        *reinterpret_cast<float4 *>(&g8[4]) = *reinterpret_cast<const float4 *>(&tl.g[4]);
         const int sb = C::MT == 2 ? t : count & 1;                 // score buffer
         const int sn = C::MT == 2 ? count : count >> 1;            // its use
         alive = alive && warp_wait(bar(C::B_SF + sb), sn & 1);
         if (!alive) continue;
         tc::tc_fence_after();
-        const Box *bx = box_s + g * 32 + (jl & 3) * 8;
         const int k0 = j * kTile;
         const bool masked = k0 + kTile - 1 > min_lim;
         const uint32_t sc = tbase + lane_off + C::SCOL + sb * 128;
@@ -632,24 +668,23 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
           }
           tc::tmem_wait_st();
         }
-        // the row's scores, 32 at a time, the next requested before these are looked at
-        uint32_t r[2][32];
+        // the row's scores, 16 at a time, the next requested before these are looked at
+        uint32_t y[2][16];
         float mx = -kInf;
-        tc::tmem_ld32(sc, r[0]);
+        tc::tmem_ld16(sc, y[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t(&x)[32] = r[c & 1];
+        for (int k = 0; k < 8; ++k) {
+          uint32_t(&x)[16] = y[k & 1];
           tc::tmem_wait_ld();
-          tc::tmem_ld32(sc + 32 * ((c + 1) & 3), r[(c + 1) & 1]);
+          tc::tmem_ld16(sc + 16 * ((k + 1) & 7), y[(k + 1) & 1]);  // (from the first again)
+          auto score = [&](int e) -> float { return __uint_as_float(x[e]); };
+          float m0 = max3(score(0), score(1), score(2)), m1 = max3(score(8), score(9), score(10));
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            auto score = [&](int e) -> float { return __uint_as_float(x[16 * k + e]); };
-            float mb = max3(score(0), score(1), score(2));
-#pragma unroll
-            for (int e = 3; e < 15; e += 2) mb = max3(mb, score(e), score(e + 1));
-            mb = fmaxf(mb, score(15));
-            mx = fmaxf(mx, fmaf(mb, bx[2 * c + k].a, bx[2 * c + k].g));
+          for (int e = 3; e < 7; e += 2) {
+            m0 = max3(m0, score(e), score(e + 1));
+            m1 = max3(m1, score(e + 8), score(e + 9));
           }
+          mx = fmaxf(mx, fmaf(max3(m0, m1, fmaxf(score(7), score(15))), a8[k], g8[k]));
         }
         const bool raise = mx > m + kTau;
         if (__any_sync(0xffffffffu, raise)) {
@@ -657,8 +692,8 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
           const float f = raise ? (m == -kInf ? 0.f : fast_exp2(m - mn)) : 1.f;
           l *= f;
           m = mn;
-          if (j > s.j0) {
-            alive = values_done(count - 1);
+          if (j > j0) {
+            if constexpr (C::MT == 1) alive = values_done(count - 1);
             if (!alive) continue;
             tc::tc_fence_after();
 #pragma unroll 1
@@ -673,51 +708,50 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
           }
         }
         const float base = m == -kInf ? 0.f : m;
-        // weights of 32 keys from y into the place of 16 scores that have been read
-        auto weigh = [&](const uint32_t (&y)[32], int c) {
-          uint32_t h[16];
+        // weights of 16 keys at a time into the place of scores that have been read
+        float inv = tl.inv[0];
+        int badb = tl.bad[0];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float4 x = *reinterpret_cast<const float4 *>(&bx[2 * c + k].a);  // a, g, inv, bad
-            const float2 A = make_float2(x.x, x.x), B = make_float2(x.y - base, x.y - base);
-            float2 sum = make_float2(0.f, 0.f);
+        for (int k = 0; k < 8; ++k) {
+          uint32_t(&x)[16] = y[k & 1];
+          tc::tmem_wait_ld();
+          if (k < 7) tc::tmem_ld16(sc + 16 * (k + 1), y[(k + 1) & 1]);
+          const float2 A = make_float2(a8[k], a8[k]), B = make_float2(g8[k] - base, g8[k] - base);
+          float2 sum = make_float2(0.f, 0.f);
+          uint32_t h[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              float2 w = fma2(make_float2(__uint_as_float(y[16 * k + 2 * e]), __uint_as_float(y[16 * k + 2 * e + 1])),
-                              A, B);
-              w.x = fast_exp2(w.x);
-              w.y = fast_exp2(w.y);
-              sum = add2(sum, w);
-              h[8 * k + e] = pack_half2(w.x, w.y);
-            }
-            l = fmaf(sum.x + sum.y, x.z, l);
-            if (__float_as_int(x.w) && k0 + 16 * (2 * c + k) <= lim) bad = true;
+          for (int e = 0; e < 8; ++e) {
+            float2 w = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), A, B);
+            w.x = fast_exp2(w.x);
+            w.y = fast_exp2(w.y);
+            sum = add2(sum, w);
+            h[e] = pack_half2(w.x, w.y);
           }
-          tc::tmem_st16(sc + 16 * c, h);
-        };
-#pragma unroll 1
-        for (int c = 0; c < 4; c += 2) {
-          tc::tmem_wait_ld();
-          tc::tmem_ld32(sc + 32 * (c + 1), r[1]);
-          weigh(r[0], c);
-          tc::tmem_wait_ld();
-          if (c == 0) tc::tmem_ld32(sc + 64, r[0]);
-          weigh(r[1], c + 1);
+          l = fmaf(sum.x + sum.y, inv, l);
+          if (badb && k0 + 16 * k <= lim) bad = true;
+          if (k < 7) {
+            inv = tl.inv[k + 1];
+            badb = tl.bad[k + 1];
+          }
+          tc::tmem_st8(sc + 8 * k, h);
         }
         tc::tmem_wait_st();
         tc::tc_fence_before();
         tc::mbar_arrive(bar(C::B_PF + sb));
-        if ((jl & 3) == 3 || j == s.j1 - 1) {
+        if ((jl & 3) == 3 || j == j1 - 1) {
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(bar(C::B_INFOE + g));
           ++ng;
         }
       }
       // ---- the rows out of TMEM
-      alive = alive && values_done(count - 1);
+      alive = alive && last_done(count - 1, nlive++);
       if (!alive) continue;
       tc::tc_fence_after();
       if (bad) l = -1.f;
+      int i;
+      long long head;
+      const bool live = row_of(i, head);
       if (s.slot >= 0) {
         const int64_t at = (int64_t)s.slot * C::R + t * 128 + tr;
         *reinterpret_cast<float2 *>(p.ws_ml + at * 2) = make_float2(m, l);
@@ -754,6 +788,8 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
       }
       tc::tc_fence_before();
       tc::mbar_arrive(bar(C::B_OE + t));
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(seg_free);
     }
   }
 
