@@ -16,10 +16,10 @@ struct ChunkPlan {
 int plan_chunk(int64_t B, int64_t Hkv, int64_t G, int64_t Qmax, int64_t D, int64_t cap, int sms,
                ChunkPlan *o) {
   const int64_t R = chunk_rows((int)D);
-  // a CTA for every tile at most (each unit counts one more for its set-up)
+  // a group of CTAs for every tile at most (each unit counts one more for its set-up)
   const int64_t units = B * Hkv * ((Qmax * G + R - 1) / R);
   const int64_t tiles = units * ((cap + 127) / 128 + 1);
-  o->ctas = (int)std::min<int64_t>(std::min(sms, kMaxChunkCtas), tiles);
+  o->ctas = (int)std::min<int64_t>(std::max(1, std::min(sms, kMaxChunkCtas) / chunk_group((int)D)), tiles);
   o->split_off = kStatusBytes;
   o->ml_off = align_up(o->split_off + o->ctas * (int64_t)sizeof(ChunkSplit), 256);
   o->o_off = align_up(o->ml_off + 2ll * o->ctas * R * 2 * 4, 256);

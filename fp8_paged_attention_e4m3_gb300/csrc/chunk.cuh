@@ -23,15 +23,15 @@ constexpr int kMinTiles = 3;   // a CTA's share is at least this many tiles
 
 template <int D>
 struct Cfg {
-  static constexpr int MT = D <= 128 ? 2 : 1;  // row tiles
-  static constexpr int R = MT * 128;           // rows of a unit
-  static constexpr int RING = 4;               // pieces held, of K and of V
-  static constexpr int NC = D / 64;            // 16 KB pieces of a K or V tile
-  static constexpr int KPC = 128 / NC;         // keys per piece of V
-  static constexpr int PIECE = 16384;
-  // pieces that are passed on and given back together: a wait or an arrival between the
-  // products costs the tensor cores some 60 cycles
-  static constexpr int GR = NC < 2 ? 1 : 2, NG = NC / GR;
+  static constexpr int CG = chunk_group(D);    // CTAs that share a unit
+  static constexpr int MT = D <= 128 ? 2 : 1;  // row tiles per CTA
+  static constexpr int R = chunk_rows(D);      // rows of a unit
+  static_assert(R == MT * 128 * CG, "rows");
+  // K and V are decoded in pieces of 128 rows of 64 channels; of a tile a CTA has the
+  // keys (K) or the channels (V) of its half, or all
+  static constexpr int PIECE = 16384, RING = 4;  // bytes; pieces held, of K and of V
+  static constexpr int NC = D / 64 / CG;       // pieces of a K or V tile
+  static constexpr int KR = 128 / CG;          // keys of K that a CTA has
   static constexpr int QT = 128 * D * 2;       // one tile of queries
   static constexpr int NSW = 4 * MT;           // softmax warps
   // warps: softmax, decoders, MMA, plan; up to 16 in all leave each 128 registers
@@ -52,7 +52,7 @@ struct Cfg {
                        B_PF = B_SF + 2, B_PV = B_PF + 2, B_OE = B_PV + 2, B_DRAIN = B_OE + 2,
                        NBARS = B_DRAIN + 1;
   static constexpr int S_SCAL = 512, S_SEG = 576, S_INFO = S_SEG + NSEG * 64,
-                       S_ROW = S_INFO + NGRP * 4 * 256, SMALL = S_ROW + R * 8;
+                       S_ROW = S_INFO + NGRP * 4 * 256, SMALL = S_ROW + MT * 128 * 8;
   static constexpr int SMEM = OFF_SMALL + SMALL + 1024;
   static_assert(NBARS * 8 <= S_SCAL && SMEM <= 232448, "shared memory");
 };
@@ -153,7 +153,7 @@ static __device__ __noinline__ void plan_begin(const ChunkParams &p, int R, int 
 
 // The next segment with keys (j1 > j0), or the end (j1 = j0).  The whole warp calls
 // it with the same state.
-static __device__ __noinline__ Segment plan_next(const ChunkParams &p, int R, int cta, Plan &o) {
+static __device__ __noinline__ Segment plan_next(const ChunkParams &p, int R, int cta, bool write, Plan &o) {
   Segment s;
   s.j0 = s.j1 = 0;
   while (o.pos < o.end) {
@@ -196,7 +196,7 @@ static __device__ __noinline__ Segment plan_next(const ChunkParams &p, int R, in
     s.rows = last - u * R;
     const bool ends = s.j1 == nt;
     s.slot = s.j0 > 0 ? p.ctas + cta : ends ? -1 : cta;
-    if (s.j0 == 0 && !ends && (threadIdx.x & 31) == 0) {
+    if (s.j0 == 0 && !ends && write && (threadIdx.x & 31) == 0) {
       // the CTAs after this one that hold more of it: up to the one of its last place
       const int c1 = (int)((at + cost + o.share - 1) / o.share) - 1;
       ChunkSplit x;
@@ -291,27 +291,35 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
   Tile *tile_s = reinterpret_cast<Tile *>(gSm + C::S_INFO);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int cta = blockIdx.x;
+  const int cta = blockIdx.x / C::CG, rank = blockIdx.x % C::CG;  // group of CTAs, and place in it
 
   if (tid < C::NBARS) {
     uint32_t cnt = 1;
     if (tid >= C::B_SEGE && tid < C::B_SEGE + C::NSEG) cnt = C::NSW + C::ND + 1;
     if (tid >= C::B_INFOF && tid < C::B_INFOF + C::NGRP) cnt = 32;
     if (tid >= C::B_INFOE && tid < C::B_INFOE + C::NGRP) cnt = C::NSW + C::ND;
-    if ((tid >= C::B_KF && tid < C::B_KF + C::RING) || (tid >= C::B_VF && tid < C::B_VF + C::RING)) cnt = C::GR;
+    // (those below are the first CTA's, whose thread issues for the group)
+    if ((tid >= C::B_KF && tid < C::B_KF + C::RING) || (tid >= C::B_VF && tid < C::B_VF + C::RING))
+      cnt = C::NC * C::CG;
     if ((tid >= C::B_QF && tid < C::B_QF + 2) || (tid >= C::B_PF && tid < C::B_PF + 2) ||
         (tid >= C::B_OE && tid < C::B_OE + 2))
-      cnt = 128;
+      cnt = 4 * C::CG;
     tc::mbar_init(bar(tid), cnt);
   }
   if (tid == 0) *abort_f = 0;
   if (warp == C::W_MMA) {
-    tc::tmem_alloc(sSm + C::S_SCAL + 4, 512);
-    tc::tmem_relinquish();
+    if constexpr (C::CG == 2) {
+      tc::tmem_alloc_pair(sSm + C::S_SCAL + 4, 512);
+      tc::tmem_relinquish_pair();
+    } else {
+      tc::tmem_alloc(sSm + C::S_SCAL + 4, 512);
+      tc::tmem_relinquish();
+    }
   }
   tc::mbar_fence_init();
   tc::tc_fence_before();
   __syncthreads();
+  if constexpr (C::CG == 2) tc::cluster_sync();  // the barriers of both are there
   tc::tc_fence_after();
   const uint32_t tbase = *reinterpret_cast<volatile uint32_t *>(gSm + C::S_SCAL + 4);
   if (tbase != 0u) *abort_f = 1;  // never: all 512 columns are the CTA's, from column 0
@@ -321,17 +329,28 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
   auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool {  // one answer for the warp
     return __all_sync(0xffffffffu, tc::mbar_wait_brief(b, parity, abort_f, LIM));
   };
+  // a warp's arrival on a barrier of the CTA that issues; its earlier writes are visible
+  // there to who waits for it
+  auto arrive_first = [&](uint32_t b) {
+    __syncwarp();
+    if (lane == 0) {
+      if constexpr (C::CG == 2)
+        tc::mbar_arrive_at(b, 0);
+      else
+        tc::mbar_arrive(b);
+    }
+  };
   bool mma_issued = false;
 
   if (warp == C::W_PLAN) {
     // =============================== plan, pages and scales
     Plan plan;
-    if (lane == 0) p.split[cta].parts = 0;
+    if (lane == 0 && rank == 0) p.split[cta].parts = 0;
     plan_begin(p, C::R, cta, plan, lane);
     int ns = 0, ng = 0;
     bool ok = true;
     while (ok) {
-      const Segment s = plan_next(p, C::R, cta, plan);
+      const Segment s = plan_next(p, C::R, cta, rank == 0, plan);
       if (ns >= C::NSEG && !(ok = warp_wait(bar(C::B_SEGE + ns % C::NSEG), (ns / C::NSEG - 1) & 1))) break;
       if (lane == 0) {
         seg_s[ns % C::NSEG] = s;
@@ -383,11 +402,12 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
     // =============================== the products, issued by one elected lane
     // (what the issue depends on stays the same for the warp, in uniform registers, and
     // ring slots follow from a tile's number: the issue is one warp's serial code)
-    const uint32_t id_qk = tc::idesc_f16(128, 128, 0, 0) | (p.bf16 ? (1u << 7 | 1u << 10) : 0u);
-    constexpr uint32_t id_pv = tc::idesc_f16(128, D, 0, 1);
+    const uint32_t id_qk = tc::idesc_f16(128 * C::CG, 128, 0, 0) | (p.bf16 ? (1u << 7 | 1u << 10) : 0u);
+    constexpr uint32_t id_pv = tc::idesc_f16(128 * C::CG, D, 0, 1);
     const uint64_t dq = tc::smem_desc(sQ, 16, 1024), dk = tc::smem_desc(sK, 16, 1024),
-                   dv = tc::smem_desc(sV, C::KPC * 128, 1024);
-    constexpr int TPR = C::RING / C::NC;  // tiles that a ring holds
+                   dv = tc::smem_desc(sV, C::PIECE, 1024);
+    constexpr uint32_t TPR = C::RING / C::NC;  // tiles that a ring holds
+    constexpr uint32_t TILE16 = C::NC * C::PIECE / 16;
     int ns = 0;
     uint32_t kt = 0, vt = 0;     // tiles of K and V taken
     // parities, a bit each: weight tiles taken from a buffer, segments of a row tile; and
@@ -395,53 +415,66 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
     uint32_t np = 0, nq = 0, had = 0;
     uint32_t buf = 0;            // MT = 1: the next buffer for scores
     bool ok = true;
+    auto wait_all = [&](uint32_t b, uint32_t parity) {  // arrivals of the whole group
+      if (C::CG == 2 && LIM >= tc::kMinWaitLimit && __all_sync(0xffffffffu, tc::mbar_try_wait_cluster(b, parity)))
+        return;
+      ok = ok && warp_wait(b, parity);
+      if constexpr (C::CG == 2) ok = ok && __all_sync(0xffffffffu, tc::mbar_try_wait_cluster(b, parity));
+    };
+    auto commit = [&](uint32_t b) {
+      if constexpr (C::CG == 2)
+        tc::mma_commit_pair(b);
+      else
+        tc::mma_commit(b);
+    };
     // scores of row tile t into buffer s from the next tile of K
     auto scores = [&](auto t_, uint32_t s, bool last) {
       constexpr int t = decltype(t_)::value;
-      const uint32_t r = kt % TPR * C::NC, ph = (kt / TPR) & 1;
+      const uint32_t x = kt % TPR;
+      if (t == 0) wait_all(bar(C::B_KF + x), (kt / TPR) & 1);
+      tc::tc_fence_after();
+      if (ok && tc::elect_one()) {
+        const uint64_t b = dk + x * TILE16;
 #pragma unroll
-      for (int g = 0; g < C::NG; ++g) {
-        const uint32_t x = r + g * C::GR;  // the group's first piece in the ring
-        if (t == 0) ok = ok && warp_wait(bar(C::B_KF + x / C::GR), ph);
-        tc::tc_fence_after();
-        if (ok && tc::elect_one()) {
-#pragma unroll
-          for (int k = 0; k < 4 * C::GR; ++k)
-            tc::mma_ss(C::SCOL + s * 128,
-                       dq + (t * C::QT + g * C::GR * 16384) / 16 + (k >> 2) * 1024 + 2 * (k & 3),
-                       dk + x * (C::PIECE / 16) + (k >> 2) * 1024 + 2 * (k & 3), id_qk, g > 0 || k > 0);
-          if (g == C::NG - 1) tc::mma_commit(bar(C::B_SF + s));
-          if (last) tc::mma_commit(bar(C::B_KE + x / C::GR));
+        for (int k = 0; k < D / 16; ++k) {
+          // (64 channels of 128 rows of Q, of KR rows of K)
+          const uint64_t ak = dq + t * (C::QT / 16) + (k >> 2) * 1024 + 2 * (k & 3),
+                         bk = b + (k >> 2) * (C::KR * 8) + 2 * (k & 3);
+          if constexpr (C::CG == 2)
+            tc::mma_ss_pair(C::SCOL + s * 128, ak, bk, id_qk, k > 0);
+          else
+            tc::mma_ss(C::SCOL + s * 128, ak, bk, id_qk, k > 0);
         }
-        __syncwarp();
+        commit(bar(C::B_SF + s));
+        if (last) commit(bar(C::B_KE + x));
       }
+      __syncwarp();
       mma_issued = true;
       if (last) ++kt;
     };
-    // the accumulator of row tile t takes the weights in buffer s
+    // the accumulator of row tile t takes the weights in buffer s; done: PV is told
     auto values = [&](auto t_, uint32_t s, bool first, bool done, bool last) {
       constexpr int t = decltype(t_)::value;
-      const uint32_t r = vt % TPR * C::NC, ph = (vt / TPR) & 1;
-      constexpr int KP = C::KPC / 16;  // steps of 16 keys per piece
-      ok = ok && warp_wait(bar(C::B_PF + s), (np >> s) & 1);
+      const uint32_t x = vt % TPR;
+      wait_all(bar(C::B_PF + s), (np >> s) & 1);
       np ^= 1u << s;
-      if (first && ((had >> t) & 1)) ok = ok && warp_wait(bar(C::B_OE + t), ((nq >> t) & 1) ^ 1);
+      if (first && ((had >> t) & 1)) wait_all(bar(C::B_OE + t), ((nq >> t) & 1) ^ 1);
+      if (t == 0) wait_all(bar(C::B_VF + x), (vt / TPR) & 1);
+      tc::tc_fence_after();
+      if (ok && tc::elect_one()) {
+        const uint64_t b = dv + x * TILE16;
 #pragma unroll
-      for (int g = 0; g < C::NG; ++g) {
-        const uint32_t x = r + g * C::GR;
-        if (t == 0) ok = ok && warp_wait(bar(C::B_VF + x / C::GR), ph);
-        tc::tc_fence_after();
-        if (ok && tc::elect_one()) {
-#pragma unroll
-          for (int k = 0; k < KP * C::GR; ++k)
-            tc::mma_ts(C::OCOL + t * D, C::SCOL + s * 128 + (g * KP * C::GR + k) * 8,
-                       dv + x * (C::PIECE / 16) + (k / KP) * 1024 + 128 * (k % KP), id_pv,
-                       !first || g > 0 || k > 0);
-          if (last) tc::mma_commit(bar(C::B_VE + x / C::GR));
-          if (done && g == C::NG - 1) tc::mma_commit(bar(C::B_PV + s));
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t ak = C::SCOL + s * 128 + k * 8;
+          if constexpr (C::CG == 2)
+            tc::mma_ts_pair(C::OCOL + t * D, ak, b + 128 * k, id_pv, !first || k > 0);
+          else
+            tc::mma_ts(C::OCOL + t * D, ak, b + 128 * k, id_pv, !first || k > 0);
         }
-        __syncwarp();
+        if (last) commit(bar(C::B_VE + x));
+        if (done) commit(bar(C::B_PV + s));
       }
+      __syncwarp();
       if (last) ++vt;
     };
     constexpr std::integral_constant<int, 0> T0{};
@@ -450,13 +483,14 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
       if (!(ok = warp_wait(bar(C::B_SEGF + ns % C::NSEG), (ns / C::NSEG) & 1))) break;
       const Segment &sg = seg_s[ns % C::NSEG];
       const int tiles = __shfl_sync(0xffffffffu, sg.j1 - sg.j0, 0);
-      const bool two = C::MT == 2 && __shfl_sync(0xffffffffu, sg.rows, 0) > 128;
+      const bool two = C::MT == 2 && __shfl_sync(0xffffffffu, sg.rows, 0) > 128 * C::CG;
       __syncwarp();
       if (tc::elect_one()) tc::mbar_arrive(bar(C::B_SEGE + ns % C::NSEG));
       ++ns;
       if (tiles <= 0) break;
-      ok = warp_wait(bar(C::B_QF), nq & 1);
-      if (two) ok = ok && warp_wait(bar(C::B_QF + 1), (nq >> 1) & 1);
+      if (rank > 0) continue;  // (the first CTA issues for both)
+      wait_all(bar(C::B_QF), nq & 1);
+      if (two) wait_all(bar(C::B_QF + 1), (nq >> 1) & 1);
 #pragma unroll 1
       for (int j = -1; j < tiles && ok; ++j) {
         const bool more = j + 1 < tiles;
@@ -508,31 +542,31 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
           const int jl = turn / PPT, pc = turn % PPT, c = pc % C::NC;
           const bool isv = pc >= C::NC;
           const uint32_t x = (tiles + g0 + jl) * C::NC + c;  // the piece's number among K's or V's
-          // rows run over 128 keys of 64 channels (K), or over the piece's keys of
-          // 64 channels after another (V)
+          // the rows of a piece: the CTA's keys of 64 channels, or of 64 after another (K);
+          // 128 keys of 64 of the CTA's channels (V)
           const Tile &tl = tile_s[(ng % C::NGRP) * 4 + jl];
-          const long long *bx = isv ? tl.v + c * (C::KPC / 16) : tl.k;
-          const int left = kend - (j0 + g0 + jl) * kTile - (isv ? c * C::KPC : 0) - r8;  // keys from row r8 on
-          const uint8_t *base = (isv ? vb : kb + 64 * c);
+          const long long *bx = isv ? tl.v : tl.k + rank * (C::KR / 16);
+          const int left = kend - (j0 + g0 + jl) * kTile - (isv ? 0 : rank * C::KR) - r8;  // keys from row r8 on
+          const uint8_t *base = isv ? vb + rank * (D / C::CG) + 64 * c : kb + 64 * C::CG * c;
           const int64_t s8 = isv ? v8 : k8;
           uint4 raw[16];
           auto request = [&](auto wide_) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const int iv = i % (C::KPC / 8), dv0 = 64 * (i / (C::KPC / 8));  // V: row in the channels' group
-              const int b16 = isv ? iv >> 1 : i >> 1;
+              const int ik = i % (C::KR / 8), dk0 = 64 * (i / (C::KR / 8));  // K: row in the channels' group
+              const int b16 = isv ? i >> 1 : ik >> 1;
               const long long at = bx[b16];
-              const bool live = at >= 0 && (isv ? 8 * iv : 8 * i) < left;
+              const bool live = at >= 0 && 8 * (isv ? i : ik) < left;
               raw[i] = make_uint4(0u, 0u, 0u, 0u);
-              if (live) raw[i] = load_raw<decltype(wide_)::value>(base + at + (i & 1 ? s8 : 0) + (isv ? dv0 : 0));
+              if (live) raw[i] = load_raw<decltype(wide_)::value>(base + at + (i & 1 ? s8 : 0) + (isv ? 0 : dk0));
             }
           };
           if (p.wide)
             request(std::true_type{});
           else
             request(std::false_type{});
-          const uint32_t slot = x % C::RING, use = x / C::RING;
-          if (use > 0 && !(ok = warp_wait(bar((isv ? C::B_VE : C::B_KE) + slot / C::GR), (use - 1) & 1))) break;
+          const uint32_t slot = x % C::RING, use = x / C::RING, grp = slot / C::NC;
+          if (use > 0 && !(ok = warp_wait(bar((isv ? C::B_VE : C::B_KE) + grp), (use - 1) & 1))) break;
           const uint32_t to = (isv ? sV : sK) + slot * C::PIECE + dst;
           auto decode = [&](auto mode) {
             constexpr Decode M = decltype(mode)::value;
@@ -560,8 +594,7 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
             decode(std::integral_constant<Decode, Decode::E4M3_F16>{});
           }
           tc::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(bar((isv ? C::B_VF : C::B_KF) + slot / C::GR));
+          arrive_first(bar((isv ? C::B_VF : C::B_KF) + grp));
         }
         turn -= pieces;
         __syncwarp();
@@ -595,7 +628,7 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
       ++ns;
       const int j0 = s.j0, j1 = s.j1;
       if (j1 <= j0) break;
-      if (t * 128 >= s.rows) {  // no row of this tile: only the groups go by
+      if (t * 128 * C::CG >= s.rows) {  // no row of this tile in the group: only the groups go by
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(seg_free);
         for (int j = j0; j < j1; j += 4, ++ng) {
@@ -606,10 +639,10 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
       }
       // the row's query and head, and whether it is one of the unit's
       auto row_of = [&](int &i, long long &head) -> bool {
-        const int rr = s.row0 + t * 128 + tr;
+        const int r = (t * C::CG + rank) * 128 + tr, rr = s.row0 + r;
         i = rr / p.G;
         head = s.h * p.G + rr - i * p.G;
-        return t * 128 + tr < s.rows;
+        return r < s.rows;
       };
       int lim;  // the last key that the row sees (rows past the unit's: all, of zeros)
       {
@@ -633,7 +666,7 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
         }
         tc::cp_async_wait_all();
         tc::fence_proxy_async_smem();
-        tc::mbar_arrive(bar(C::B_QF + t));
+        arrive_first(bar(C::B_QF + t));
       }
       float m = -kInf, l = 0.f;
       bool bad = false;
@@ -737,7 +770,7 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
         }
         tc::tmem_wait_st();
         tc::tc_fence_before();
-        tc::mbar_arrive(bar(C::B_PF + sb));
+        arrive_first(bar(C::B_PF + sb));
         if ((jl & 3) == 3 || j == j1 - 1) {
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(bar(C::B_INFOE + g));
@@ -753,7 +786,7 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
       long long head;
       const bool live = row_of(i, head);
       if (s.slot >= 0) {
-        const int64_t at = (int64_t)s.slot * C::R + t * 128 + tr;
+        const int64_t at = (int64_t)s.slot * C::R + (t * C::CG + rank) * 128 + tr;
         *reinterpret_cast<float2 *>(p.ws_ml + at * 2) = make_float2(m, l);
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
@@ -787,27 +820,37 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
         }
       }
       tc::tc_fence_before();
-      tc::mbar_arrive(bar(C::B_OE + t));
+      arrive_first(bar(C::B_OE + t));
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(seg_free);
     }
   }
 
-  // ---- wind-down; after a wait that ran out: mark everything of the CTA invalid
+  // ---- wind-down; after a wait that ran out, in either CTA: mark everything of the group
+  // invalid, once both have stopped
   tc::cp_async_wait_all();
   __syncthreads();
-  const bool aborted = *abort_f != 0;
-  if (aborted) {
-    if (warp == C::W_MMA && mma_issued && tc::elect_one()) {
+  bool aborted = *abort_f != 0;
+  if (warp == C::W_MMA && aborted && mma_issued && tc::elect_one()) {
+    if constexpr (C::CG == 2)
+      tc::mma_commit_pair(bar(C::B_DRAIN));
+    else
       tc::mma_commit(bar(C::B_DRAIN));
-      volatile int no_abort = 0;
-      tc::mbar_wait_brief(bar(C::B_DRAIN), 0, &no_abort, p.drain_limit);
-    }
+    volatile int no_abort = 0;
+    tc::mbar_wait_brief(bar(C::B_DRAIN), 0, &no_abort, p.drain_limit);
+  }
+  __syncwarp();
+  if constexpr (C::CG == 2) {
+    tc::cluster_sync();  // nothing of the other CTA's reaches this one's memory any more
+    aborted = aborted || tc::ld_shared_at(sSm + C::S_SCAL, rank ^ 1) != 0;
+    tc::cluster_sync();
+  }
+  if (aborted) {
     Plan plan;
     if (warp == C::W_PLAN) plan_begin(p, C::R, cta, plan, lane);
     for (;;) {
       if (warp == C::W_PLAN) {
-        const Segment s = plan_next(p, C::R, cta, plan);
+        const Segment s = plan_next(p, C::R, cta, rank == 0, plan);
         if (lane == 0) seg_s[0] = s;
       }
       __syncthreads();
@@ -830,7 +873,12 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  if (warp == C::W_MMA) tc::tmem_dealloc(tbase, 512);
+  if (warp == C::W_MMA) {
+    if constexpr (C::CG == 2)
+      tc::tmem_dealloc_pair(tbase, 512);
+    else
+      tc::tmem_dealloc(tbase, 512);
+  }
 }
 
 template <int D>
@@ -849,7 +897,21 @@ cudaError_t launch_d(const ChunkParams &p, cudaStream_t stream) {
     if (dev >= 0 && dev < kDevs)
       configured[dev].store(current_context_id(), std::memory_order_release);
   }
-  return launch_dependent(chunk_kernel<D>, dim3((unsigned)p.ctas), C::NTHREADS, C::SMEM, stream, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.ctas * C::CG));
+  cfg.blockDim = dim3(C::NTHREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = C::CG;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = C::CG == 2 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, chunk_kernel<D>, p);
 }
 
 // one head dim each, compiled in a translation unit of its own

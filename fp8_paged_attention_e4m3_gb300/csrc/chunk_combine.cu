@@ -49,7 +49,7 @@ __device__ __forceinline__ Acc<VN> load_row(const float *o, int lane) {
 
 template <int D>
 __global__ void __launch_bounds__(32 * kWarps) chunk_combine_kernel(const __grid_constant__ ChunkParams p) {
-  constexpr int VN = D / 32, R = D <= 128 ? 256 : 128;
+  constexpr int VN = D / 32, R = chunk_rows(D);
   __shared__ float sums[kWarps][D];
   __shared__ float2 wl[kMaxChunkCtas];  // (weight, sum) of the parts
   __shared__ float red[kWarps][2];

@@ -40,13 +40,15 @@ struct ChunkParams {
   uint32_t *status;
   int32_t B, Qmax, Hkv, G, D, page;
   int32_t bf16, e5m2;
-  int32_t ctas;
+  int32_t ctas;                // groups of CTAs (chunk_group)
   float alpha;                 // softmax_scale log2(e)
   long long wait_limit, drain_limit;  // SM cycles
 };
 
-// Rows of a unit: two tiles of 128, one where a key's head is 256 wide.
-inline int chunk_rows(int D) { return D <= 128 ? 256 : 128; }
+// CTAs that share a unit, and its rows: each CTA has two tiles of 128, one where a key's
+// head is 256 wide.
+__host__ __device__ constexpr int chunk_group(int D) { return D == 64 ? 1 : 2; }
+__host__ __device__ constexpr int chunk_rows(int D) { return (D <= 128 ? 256 : 128) * chunk_group(D); }
 
 cudaError_t launch_chunk(const ChunkParams &p, cudaStream_t stream);
 cudaError_t launch_chunk_combine(const ChunkParams &p, cudaStream_t stream);
