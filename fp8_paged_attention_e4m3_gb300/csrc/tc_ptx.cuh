@@ -366,11 +366,13 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
       "h"((unsigned short)3)
       : "memory");
 }
-// Arrive on the barrier at `bar` of CTA `rank` of the cluster.
+// Arrive on the barrier at `bar` of CTA `rank` of the cluster.  Without a release at
+// cluster scope, which takes some 900 cycles: what the arrival tells of is tensor memory,
+// or shared memory behind a proxy fence, of this CTA, which the tensor cores alone read.
 __device__ __forceinline__ void mbar_arrive_at(uint32_t bar, uint32_t rank) {
   asm volatile(
       "{\n .reg .b32 r;\n mapa.shared::cluster.u32 r, %0, %1;\n"
-      " mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n}\n" ::"r"(bar),
+      " mbarrier.arrive.shared::cluster.b64 _, [r];\n}\n" ::"r"(bar),
       "r"(rank)
       : "memory");
 }
