@@ -52,7 +52,8 @@ struct Cfg {
                        B_PF = B_SF + 2, B_PV = B_PF + 2, B_OE = B_PV + 2, B_DRAIN = B_OE + 2,
                        NBARS = B_DRAIN + 1;
   static constexpr int S_SCAL = 512, S_SEG = 576, S_INFO = S_SEG + NSEG * 64,
-                       S_ROW = S_INFO + NGRP * 4 * 256, SMALL = S_ROW + MT * 128 * 8;
+                       S_ROW = S_INFO + NGRP * 4 * 256, S_END = S_ROW + MT * 128 * 8,
+                       SMALL = S_END + 128 * 8;
   static constexpr int SMEM = OFF_SMALL + SMALL + 1024;
   static_assert(NBARS * 8 <= S_SCAL && SMEM <= 232448, "shared memory");
 };
@@ -410,9 +411,9 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
     constexpr uint32_t TILE16 = C::NC * C::PIECE / 16;
     int ns = 0;
     uint32_t kt = 0, vt = 0;     // tiles of K and V taken
-    // parities, a bit each: weight tiles taken from a buffer, segments of a row tile; and
-    // whether a row tile has had one
-    uint32_t np = 0, nq = 0, had = 0;
+    // parities, a bit each: weight tiles taken from a buffer, segments of a row tile's
+    // queries and of an accumulator; and whether an accumulator has had one
+    uint32_t np = 0, nq = 0, no = 0, had = 0;
     uint32_t buf = 0;            // MT = 1: the next buffer for scores
     bool ok = true;
     auto wait_all = [&](uint32_t b, uint32_t parity) {  // arrivals of the whole group
@@ -427,18 +428,18 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
       else
         tc::mma_commit(b);
     };
-    // scores of row tile t into buffer s from the next tile of K
-    auto scores = [&](auto t_, uint32_t s, bool last) {
-      constexpr int t = decltype(t_)::value;
+    // scores of row tile qt's queries into buffer s from the next tile of K; fresh: the
+    // first products with it, last: the last
+    auto scores = [&](auto t_, uint32_t s, bool fresh, bool last, int qt) {
       const uint32_t x = kt % TPR;
-      if (t == 0) wait_all(bar(C::B_KF + x), (kt / TPR) & 1);
+      if (fresh) wait_all(bar(C::B_KF + x), (kt / TPR) & 1);
       tc::tc_fence_after();
       if (ok && tc::elect_one()) {
         const uint64_t b = dk + x * TILE16;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           // (64 channels of 128 rows of Q, of KR rows of K)
-          const uint64_t ak = dq + t * (C::QT / 16) + (k >> 2) * 1024 + 2 * (k & 3),
+          const uint64_t ak = dq + qt * (C::QT / 16) + (k >> 2) * 1024 + 2 * (k & 3),
                          bk = b + (k >> 2) * (C::KR * 8) + 2 * (k & 3);
           if constexpr (C::CG == 2)
             tc::mma_ss_pair(C::SCOL + s * 128, ak, bk, id_qk, k > 0);
@@ -453,13 +454,13 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
       if (last) ++kt;
     };
     // the accumulator of row tile t takes the weights in buffer s; done: PV is told
-    auto values = [&](auto t_, uint32_t s, bool first, bool done, bool last) {
+    auto values = [&](auto t_, uint32_t s, bool first, bool done, bool fresh, bool last) {
       constexpr int t = decltype(t_)::value;
       const uint32_t x = vt % TPR;
       wait_all(bar(C::B_PF + s), (np >> s) & 1);
       np ^= 1u << s;
-      if (first && ((had >> t) & 1)) wait_all(bar(C::B_OE + t), ((nq >> t) & 1) ^ 1);
-      if (t == 0) wait_all(bar(C::B_VF + x), (vt / TPR) & 1);
+      if (first && ((had >> t) & 1)) wait_all(bar(C::B_OE + t), ((no >> t) & 1) ^ 1);
+      if (fresh) wait_all(bar(C::B_VF + x), (vt / TPR) & 1);
       tc::tc_fence_after();
       if (ok && tc::elect_one()) {
         const uint64_t b = dv + x * TILE16;
@@ -491,24 +492,38 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
       if (rank > 0) continue;  // (the first CTA issues for both)
       wait_all(bar(C::B_QF), nq & 1);
       if (two) wait_all(bar(C::B_QF + 1), (nq >> 1) & 1);
+      if constexpr (C::MT == 2) {
+        if (two) {
 #pragma unroll 1
-      for (int j = -1; j < tiles && ok; ++j) {
-        const bool more = j + 1 < tiles;
-        if constexpr (C::MT == 2) {
-          if (j >= 0) values(T0, 0, j == 0, !more, !two);
-          if (more) scores(T0, 0, !two);
-          if (two) {
-            if (j >= 0) values(T1, 1, j == 0, !more, true);
-            if (more) scores(T1, 1, true);
+          for (int j = -1; j < tiles && ok; ++j) {
+            const bool more = j + 1 < tiles;
+            if (j >= 0) values(T0, 0, j == 0, !more, true, false);
+            if (more) scores(T0, 0, true, false, 0);
+            if (j >= 0) values(T1, 1, j == 0, !more, false, true);
+            if (more) scores(T1, 1, false, true, 1);
           }
-        } else {  // buffers alternate through all segments
-          if (more) scores(T0, buf, true);
-          if (j >= 0) values(T0, buf ^ 1, j == 0, true, true);
+        } else {  // one tile of rows: the key tiles go to the two accumulators in turn
+#pragma unroll 1
+          for (int j = 0; j < tiles + 2 && ok; j += 2) {
+            if (j >= 2) values(T0, 0, j == 2, j >= tiles, true, true);
+            if (j < tiles) scores(T0, 0, true, true, 0);
+            if (j >= 2 && j - 1 < tiles) values(T1, 1, j == 2, j + 1 >= tiles, true, true);
+            if (j + 1 < tiles) scores(T1, 1, true, true, 0);
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int j = -1; j < tiles && ok; ++j) {  // buffers alternate through all segments
+          const bool more = j + 1 < tiles;
+          if (more) scores(T0, buf, true, true, 0);
+          if (j >= 0) values(T0, buf ^ 1, j == 0, true, true, true);
           if (more) buf ^= 1;
         }
       }
+      // (queries: of the row tiles; accumulators: of those used)
       nq ^= two ? 3u : 1u;
-      had |= two ? 3u : 1u;
+      no ^= two || tiles > 1 ? 3u : 1u;
+      had |= two || tiles > 1 ? 3u : 1u;
     }
   } else if (warp >= C::W_DEC) {
     // =============================== decoders: a warp per piece
@@ -607,6 +622,7 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
     const int t = warp >> 2, tr = tid & 127;
     const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
     long long *row_s = reinterpret_cast<long long *>(gSm + C::S_ROW) + t * 128;
+    float2 *end_s = reinterpret_cast<float2 *>(gSm + C::S_END);
     int ns = 0, ng = 0, count = 0;
     bool alive = true;
     // The products run in the order of their issue.  With two row tiles the value product
@@ -628,18 +644,13 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
       ++ns;
       const int j0 = s.j0, j1 = s.j1;
       if (j1 <= j0) break;
-      if (t * 128 * C::CG >= s.rows) {  // no row of this tile in the group: only the groups go by
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(seg_free);
-        for (int j = j0; j < j1; j += 4, ++ng) {
-          alive = alive && warp_wait(bar(C::B_INFOF + ng % C::NGRP), (ng / C::NGRP) & 1);
-          if (alive && lane == 0) tc::mbar_arrive(bar(C::B_INFOE + ng % C::NGRP));
-        }
-        continue;
-      }
+      // One tile of rows: both groups of warps have its rows, and every other key tile each
+      // (a chain of scores, softmax and value product would leave the tensor cores idle).
+      const bool solo = C::MT == 2 && s.rows <= 128 * C::CG;
+      const int rt = solo ? 0 : t;  // row tile
       // the row's query and head, and whether it is one of the unit's
       auto row_of = [&](int &i, long long &head) -> bool {
-        const int r = (t * C::CG + rank) * 128 + tr, rr = s.row0 + r;
+        const int r = (rt * C::CG + rank) * 128 + tr, rr = s.row0 + r;
         i = rr / p.G;
         head = s.h * p.G + rr - i * p.G;
         return r < s.rows;
@@ -654,7 +665,7 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
       }
       const int min_lim = __reduce_min_sync(0xffffffffu, lim);
       tc::named_bar(1 + t, 128);
-      {
+      if (!solo || t == 0) {
         constexpr int QCH = D / 8;  // 16-byte pieces per row
         const __half *qb = static_cast<const __half *>(p.q);
 #pragma unroll 4
@@ -670,9 +681,21 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
       }
       float m = -kInf, l = 0.f;
       bool bad = false;
-      for (int j = j0; j < j1; ++j, ++count) {
+      int seen = 0;  // tiles of the segment
+      for (int j = j0; j < j1; ++j) {
         const int jl = j - j0, g = ng % C::NGRP;
         if ((jl & 3) == 0) alive = alive && warp_wait(bar(C::B_INFOF + g), (ng / C::NGRP) & 1);
+        auto group_end = [&]() {
+          if ((jl & 3) == 3 || j == j1 - 1) {
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(bar(C::B_INFOE + g));
+            ++ng;
+          }
+        };
+        if (solo && (jl & 1) != t) {
+          if (alive) group_end();
+          continue;
+        }
         const Tile &tl = tile_s[g * 4 + (jl & 3)];
         float a8[8], g8[8];
         *reinterpret_cast<float4 *>(&a8[0]) = *reinterpret_cast<const float4 *>(&tl.a[0]);
@@ -725,7 +748,7 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
           const float f = raise ? (m == -kInf ? 0.f : fast_exp2(m - mn)) : 1.f;
           l *= f;
           m = mn;
-          if (j > j0) {
+          if (seen > 0) {
             if constexpr (C::MT == 1) alive = values_done(count - 1);
             if (!alive) continue;
             tc::tc_fence_after();
@@ -771,56 +794,76 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
         tc::tmem_wait_st();
         tc::tc_fence_before();
         arrive_first(bar(C::B_PF + sb));
-        if ((jl & 3) == 3 || j == j1 - 1) {
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(bar(C::B_INFOE + g));
-          ++ng;
-        }
+        group_end();
+        ++count;
+        ++seen;
       }
       // ---- the rows out of TMEM
-      alive = alive && last_done(count - 1, nlive++);
-      if (!alive) continue;
+      if (seen > 0) alive = alive && last_done(count - 1, nlive++);
       tc::tc_fence_after();
       if (bad) l = -1.f;
-      int i;
-      long long head;
-      const bool live = row_of(i, head);
-      if (s.slot >= 0) {
-        const int64_t at = (int64_t)s.slot * C::R + (t * C::CG + rank) * 128 + tr;
-        *reinterpret_cast<float2 *>(p.ws_ml + at * 2) = make_float2(m, l);
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t r[32];
-          tc::tmem_ld32(tbase + lane_off + C::OCOL + t * D + c, r);
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            *reinterpret_cast<uint4 *>(p.ws_o + at * D + c + 4 * e) =
-                make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
-        }
-      } else {
-        const float inv = l <= 0.f ? 0.f : __fdiv_rn(1.f, l);  // (NaN if l is)
-        __half *o = static_cast<__half *>(p.out) + (live ? s.b * p.o_sb + i * p.o_si + head * p.o_sh : 0);
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t r[32], h[16];
-          tc::tmem_ld32(tbase + lane_off + C::OCOL + t * D + c, r);
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float x = __uint_as_float(r[2 * e]), y = __uint_as_float(r[2 * e + 1]);
-            h[e] = l <= 0.f ? 0u : pack16(x * inv, y * inv, p.bf16);
-          }
-          if (live) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              *reinterpret_cast<uint4 *>(o + c + 8 * e) =
-                  make_uint4(h[4 * e], h[4 * e + 1], h[4 * e + 2], h[4 * e + 3]);
-          }
+      float f0 = 1.f, f1 = 0.f;  // of the accumulators
+      if (solo) {  // the first group joins both and writes
+        if (t == 1) end_s[tr] = make_float2(m, l);
+        tc::tc_fence_before();
+        alive = !tc::named_bar_or(3, 256, !alive);
+        tc::tc_fence_after();
+        if (t == 0) {
+          const float2 o = end_s[tr];
+          const float M = fmaxf(l > 0.f ? m : -kInf, o.y > 0.f ? o.x : -kInf);
+          f0 = l <= 0.f ? 0.f : fast_exp2(m - M);
+          f1 = o.y <= 0.f ? 0.f : fast_exp2(o.x - M);
+          l = l < 0.f || o.y < 0.f ? -1.f : f0 * l + f1 * o.y;  // (NaN if one is)
+          m = M;
         }
       }
-      tc::tc_fence_before();
-      arrive_first(bar(C::B_OE + t));
+      if (alive && !(solo && t == 1)) {
+        const bool both = solo && j1 - j0 > 1;
+        int i;
+        long long head;
+        const bool live = row_of(i, head);
+        const uint32_t oc = tbase + lane_off + C::OCOL + t * D;
+        const int64_t at = (int64_t)s.slot * C::R + (t * C::CG + rank) * 128 + tr;
+        const float inv = l <= 0.f ? 0.f : __fdiv_rn(1.f, l);  // (NaN if l is)
+        __half *o = static_cast<__half *>(p.out) + (live ? s.b * p.o_sb + i * p.o_si + head * p.o_sh : 0);
+        if (s.slot >= 0) *reinterpret_cast<float2 *>(p.ws_ml + at * 2) = make_float2(m, l);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          uint32_t r[16];
+          tc::tmem_ld16(oc + c, r);
+          tc::tmem_wait_ld();
+          if (both) {
+            uint32_t q[16];
+            tc::tmem_ld16(oc + D + c, q);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              r[e] = __float_as_uint(fmaf(f1, __uint_as_float(q[e]), f0 * __uint_as_float(r[e])));
+          }
+          if (s.slot >= 0) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              *reinterpret_cast<uint4 *>(p.ws_o + at * D + c + 4 * e) =
+                  make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+          } else {
+            uint32_t h[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float x = __uint_as_float(r[2 * e]), y = __uint_as_float(r[2 * e + 1]);
+              h[e] = l <= 0.f ? 0u : pack16(x * inv, y * inv, p.bf16);
+            }
+            if (live) {
+              *reinterpret_cast<uint4 *>(o + c) = make_uint4(h[0], h[1], h[2], h[3]);
+              *reinterpret_cast<uint4 *>(o + c + 8) = make_uint4(h[4], h[5], h[6], h[7]);
+            }
+          }
+        }
+        tc::tc_fence_before();
+      }
+      // (what the first group has read of the second's may go)
+      if (solo && tc::named_bar_or(4, 256, !alive)) alive = false;
+      if (!alive) continue;
+      if (seen > 0) arrive_first(bar(C::B_OE + t));
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(seg_free);
     }
