@@ -74,20 +74,6 @@ __device__ __forceinline__ uint32_t fp8x2_to_f16x2(uint32_t two_bytes) {
     return cvt_e4m3x2(two_bytes);
 }
 
-// Two FP8 bytes -> bf16x2, exact for every finite code.  A code's magnitude bits moved
-// to the top of BF16's mantissa and the bottom of its exponent stand for the value
-// times 2^-120 (E4M3, bias 7 against 127) or 2^-112 (E5M2, bias 15), subnormals
-// included; one product with a power of two puts it right.
-template <bool E5M2>
-__device__ __forceinline__ uint32_t fp8x2_to_bf16x2(uint32_t two_bytes) {
-  const uint32_t t = __byte_perm(two_bytes, 0u, 0x1404);  // (b1 << 24) | (b0 << 8)
-  const uint32_t v = E5M2 ? ((t >> 3) & 0x0FE00FE0u) | (t & 0x80008000u)
-                          : ((t >> 4) & 0x07F007F0u) | (t & 0x80008000u);
-  uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;\n" : "=r"(d) : "r"(v), "r"(E5M2 ? 0x77807780u : 0x7B807B80u));
-  return d;
-}
-
 // 16 bytes -> 16 halves (two uint4 of f16x2).
 __device__ __forceinline__ void e4m3x16_to_f16x16(const uint4 &raw, uint4 &h0,
                                                   uint4 &h1) {
