@@ -187,7 +187,7 @@ int verify_attn_e4m3_fork_pages(const vae4_tensor *block_table, const vae4_tenso
 
 int64_t verify_attn_e4m3_pages_workspace_bytes(int64_t n_pages) {
   if (n_pages < 1 || n_pages > kMaxCells) return VAE4_ERR_SHAPE;
-  return align_up(4 * n_pages, 256);
+  return kPoolGrid * 32 * 8 + align_up(4 * n_pages, 256);  // sums of the warps | list
 }
 
 int verify_attn_e4m3_resize_pages(const vae4_tensor *block_table, const vae4_tensor *seq_lens,
@@ -219,9 +219,10 @@ int verify_attn_e4m3_resize_pages(const vae4_tensor *block_table, const vae4_ten
   p.page = page_tokens;
   p.copies = static_cast<int32_t *>(copies->data);
   p.copies_sb = copies->stride[0];
-  p.list = static_cast<int32_t *>(workspace->data);
+  p.sums = static_cast<int2 *>(workspace->data);
+  p.list = reinterpret_cast<int32_t *>(p.sums + kPoolGrid * 32);
   if (p.pool.B == 0) return VAE4_OK;
-  if (!p.pool.bt || !p.pool.counts || !p.seq || !p.copies || !p.list) return VAE4_ERR_NULL;
+  if (!p.pool.bt || !p.pool.counts || !p.seq || !p.copies || !workspace->data) return VAE4_ERR_NULL;
   if (launch_resize_pages(p, cu(stream)) != cudaSuccess) return VAE4_ERR_CUDA;
   return VAE4_OK;
 }

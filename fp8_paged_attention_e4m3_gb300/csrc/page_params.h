@@ -10,6 +10,8 @@ namespace vae4 {
 constexpr int kMaxForkRows = 8192;     // a column tile of the table is held in shared memory
 constexpr int kMaxResizeRows = 16384;  // (pages, first written page) of every row are held there
 
+constexpr int kPoolGrid = 128;         // CTAs of 1024 threads that share a large pool
+
 // What a page holds of one tensor: n[0] x n[1] x n[2] runs of `run` vectors of
 // `vec` bytes, the runs' starts s[0 .. 2] bytes apart; neighbouring dimensions that
 // lie end to end are merged.
@@ -58,6 +60,7 @@ struct ResizeParams {
   int32_t *copies;         // i32 [B][2]
   int64_t copies_sb;
   int32_t *list;           // i32 [n_pages]: scratch
+  int2 *sums;              // [kPoolGrid * 32]: scratch
 };
 
 struct CompactParams {

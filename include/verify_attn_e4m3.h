@@ -653,8 +653,10 @@ int64_t verify_attn_e4m3_sparse_workspace_bytes(int B, int Hq, int Hkv, int Qmax
  * BAD_SCALE); the others of the sequence are not concerned.  A query with a score of
  * NaN or +infinity gives a row of NaN, one whose scores are all -infinity zeros.
  * Scores, sums and weighted sums are FP32 and a weight enters its product in FP16, as
- * for verify_attn_e4m3_block_scaled and with its bound; K enters the scores exactly,
- * as FP16 or (with BF16 queries) BF16.
+ * for verify_attn_e4m3_block_scaled and with its bound.  FP16 queries and K enter the
+ * scores exactly; a row of BF16 queries enters as FP16, scaled by a power of two, which
+ * is exact down to 2^-28 of the row's largest magnitude (what is smaller is off by at
+ * most 2^-39 of it).
  * The batch is divided evenly among the SMs on the device, from the lengths of the
  * call, long contexts of few queries too.  Repeated calls give the same bits.
  */
@@ -691,7 +693,9 @@ int64_t verify_attn_e4m3_chunk_workspace_bytes(int B, int Hq, int Hkv, int Qmax,
  *  dev_status  optional device pointer to a status word (NULL = none).  An entry
  *              that is neither -1 nor a page's id sets BAD_BLOCK and stays, and
  *              a page that an entry holds although its count is 0 sets BAD_COUNT
- *              where it should be counted down or up, and stays 0.
+ *              where it should be counted down or up, and stays 0.  (A count below
+ *              the number of entries is the caller's mistake: it ends at 0, but a
+ *              fork that counts the page's entries both up and down may leave more.)
  * At most 2^30 table entries and pages.
  * ---------------------------------------------------------------------------
  */
@@ -735,7 +739,8 @@ int verify_attn_e4m3_fork_pages(const vae4_tensor *block_table, const vae4_tenso
  *              BAD_LENGTH); the row of an invalid pair stays.
  *  copies      I32 [B][2], stride[1] == 1, written in full.
  *  workspace   U8, at least verify_attn_e4m3_pages_workspace_bytes(n_pages) bytes,
- *              256-byte aligned; nothing in it has to be set or kept.
+ *              256-byte aligned; nothing in it has to be set or kept, but calls
+ *              that overlap, on different pools, need one each.
  * In this order:
  *  1. entries at or past ceil(L / page_tokens) are given back: they become -1, and
  *     their pages' counts go down (L = 0 frees a sequence, a smaller L gives

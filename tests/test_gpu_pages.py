@@ -254,6 +254,46 @@ def test_resize_with_too_few_pages(extra):
     assert short[0]
 
 
+@pytest.mark.parametrize("extra", [0, 1, 5000])
+def test_resize_of_a_large_pool_that_runs_short(extra):
+    """A pool for which the whole GPU is used: too few pages, invalid entries and lengths,
+    pages that nothing counts; then a call that finds room."""
+    B, cols, page = 130, 300, 16
+    table, counts = pool(21, B, cols, extra=extra, share=0.8, kept=7)
+    seq = lengths(22, table, page)
+    seq[7], seq[8], seq[9] = (cols * page + 1, 1), (5, 6), (-1, 0)
+    table[3][1], table[4][0] = len(counts), -2
+    t, c, st = dev(table), dev(counts), status()
+    copies = torch.empty((B, 2), dtype=torch.int32, device="cuda")
+    ws = vae4.alloc_pages_workspace(len(counts))
+    for full in (True, False):
+        now = [(cols * page, cols * page) if full and b % 3 == 0 else x for b, x in enumerate(seq)]
+        vae4.verify_attn_e4m3_resize_pages(t, dev(now), c, copies, ws, page_tokens=page, status=st.zero_())
+        table, counts, wcp, wst = plain_resize(table, counts, now, page)
+        assert t.tolist() == table and c.tolist() == counts and copies.tolist() == wcp and int(st) == wst
+        assert not full or wst & vae4.STATUS_NO_PAGES
+
+
+def test_counts_below_the_entries():
+    """Pages that more entries give up than their counts say: the counts end at zero, which
+    is reported, never below it (such a page would be kept for good)."""
+    B, cols = 200, 40
+    for low in (-2 ** 31, -1, 0, 1, 2):
+        counts = [low] * cols + [0] * 5
+        table = [list(range(cols)) for _ in range(B)]
+        for what in ("release", "replace", "fork"):
+            t, c, st = dev(table), dev(counts), status()
+            if what == "fork":
+                vae4.verify_attn_e4m3_fork_pages(t, c, dev([-1] * B), status=st)
+                want, wc, wst = plain_fork([list(x) for x in table], list(counts), [-1] * B)
+            else:
+                seq = [(0, 0)] * B if what == "release" else [(cols * 16, 16)] * B
+                copies, ws = torch.empty((B, 2), dtype=torch.int32, device="cuda"), vae4.alloc_pages_workspace(len(counts))
+                vae4.verify_attn_e4m3_resize_pages(t, dev(seq), c, copies, ws, page_tokens=16, status=st)
+                want, wc, _, wst = plain_resize([list(x) for x in table], list(counts), seq, 16)
+            assert t.tolist() == want and c.tolist() == wc and int(st) == wst, (low, what)
+
+
 def test_resize_reports():
     table, counts = pool(4, 8, 6, share=0, kept=0)
     table[0][5], table[1][0] = len(counts) + 3, -4

@@ -34,7 +34,7 @@ def base():
     return dict(k=_t(U8, [NPG, PAGE, HKV, D]), v=_t(U8, [NPG, PAGE, HKV, D]), pairs=_t(I32, [N, 2]),
                 sc=_t(F32, [NPG, 2, HKV, NB]), bd=_t(U8, [NPG, HKV, NB, 2, D]), bt=_t(I32, [B, MP]),
                 rc=_t(I32, [NPG]), par=_t(I32, [B]), seq=_t(I32, [B, 2]), cp=_t(I32, [B, 2]),
-                ws=_t(U8, [4096]), mv=_t(I32, [N, 2]))
+                ws=_t(U8, [1 << 16]), mv=_t(I32, [N, 2]))
 
 
 NEEDS = {"copy": ("k", "v", "pairs", "sc", "bd"), "fork": ("bt", "rc", "par"),
@@ -111,7 +111,7 @@ def call(lib, name, a, page=PAGE):
     (POOL, dict(rc=_t(I32, [NPG], data=FAKE + 2)), ALIGN),
     # workspace
     (("resize",), dict(ws=_t(U8, [128])), WS),
-    (("resize",), dict(ws=_t(U8, [4096], data=FAKE + 64)), WS),
+    (("resize",), dict(ws=_t(U8, [1 << 16], data=FAKE + 64)), WS),
 ])
 def test_refusals(lib, names, over, code):
     for name in names:
@@ -147,8 +147,9 @@ def test_nothing_to_do_is_no_error(lib):
 
 
 def test_workspace_bytes():
-    assert vae4.pages_workspace_bytes(1) == 256
-    assert vae4.pages_workspace_bytes(1 << 30) == 1 << 32
+    sums = 128 * 32 * 8  # of the warps of the grid that shares a large pool
+    assert vae4.pages_workspace_bytes(1) == sums + 256
+    assert vae4.pages_workspace_bytes(1 << 30) == sums + (1 << 32)
     for bad in (0, -1, (1 << 30) + 1):
         with pytest.raises(vae4.Vae4Error):
             vae4.pages_workspace_bytes(bad)
