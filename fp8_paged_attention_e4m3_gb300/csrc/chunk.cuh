@@ -34,13 +34,19 @@ struct Cfg {
   static constexpr int KR = 128 / CG;          // keys of K that a CTA has
   static constexpr int QT = 128 * D * 2;       // one tile of queries
   static constexpr int NSW = 4 * MT;           // softmax warps
-  // warps: softmax, decoders, MMA, plan; up to 16 in all leave each 128 registers
-  static constexpr int ND = MT == 2 ? 6 : 8;
-  static constexpr int W_DEC = NSW, W_MMA = NSW + ND, W_PLAN = W_MMA + 1;
+  // warps: softmax, decoders, MMA (one per accumulator), plan; up to 16 in all leave each
+  // 128 registers
+  // (MT = 2: 3 decoders decode 64 queries' 131072 keys in 137 us, 4 in 125, 5 in 130)
+  static constexpr int ND = MT == 2 ? 4 : 8;
+  static constexpr int W_DEC = NSW, W_MMA = NSW + ND, W_PLAN = W_MMA + MT;
   static constexpr int NTHREADS = 32 * (W_PLAN + 1);
   // A decoder that waits for a place has passed the one before it of any other warp's
   // (no more pieces are under way than the rings hold), so parities are unambiguous.
   static_assert(ND <= 2 * RING, "decoders");
+  // Scores are made KW keys at a time, into one of two buffers of the row tile, so that
+  // the next ones are there when the softmax is through with these.
+  static constexpr int KW = MT == 2 ? 64 : 128, SPT = 128 / KW;  // steps per key tile
+  static constexpr int BPS = KW / CG / 16;     // boxes of 16 keys of a step that a CTA has of K
   // TMEM columns: scores (and weights in their place), accumulators
   static constexpr int SCOL = 0, OCOL = 256;
   static constexpr int NSEG = 4, NGRP = 4;     // segments, groups of four tiles held
@@ -49,8 +55,9 @@ struct Cfg {
   static constexpr int B_SEGF = 0, B_SEGE = B_SEGF + NSEG, B_INFOF = B_SEGE + NSEG,
                        B_INFOE = B_INFOF + NGRP, B_KF = B_INFOE + NGRP, B_KE = B_KF + RING,
                        B_VF = B_KE + RING, B_VE = B_VF + RING, B_QF = B_VE + RING, B_SF = B_QF + 2,
-                       B_PF = B_SF + 2, B_PV = B_PF + 2, B_OE = B_PV + 2, B_DRAIN = B_OE + 2,
-                       NBARS = B_DRAIN + 1;
+                       B_PF = B_SF + 2 * MT, B_PV = B_PF + 2 * MT, B_OE = B_PV + 2 * MT,
+                       B_DRAIN = B_OE + 2,
+                       NBARS = B_DRAIN + MT;
   static constexpr int S_SCAL = 512, S_SEG = 576, S_INFO = S_SEG + NSEG * 64,
                        S_ROW = S_INFO + NGRP * 4 * 256, S_END = S_ROW + MT * 128 * 8,
                        SMALL = S_END + 128 * 8;
@@ -325,13 +332,14 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
 
   if (tid < C::NBARS) {
     uint32_t cnt = 1;
-    if (tid >= C::B_SEGE && tid < C::B_SEGE + C::NSEG) cnt = C::NSW + C::ND + 1;
+    if (tid >= C::B_SEGE && tid < C::B_SEGE + C::NSEG) cnt = C::NSW + C::ND + C::MT;
     if (tid >= C::B_INFOF && tid < C::B_INFOF + C::NGRP) cnt = 32;
     if (tid >= C::B_INFOE && tid < C::B_INFOE + C::NGRP) cnt = C::NSW + C::ND;
     // (those below are the first CTA's, whose thread issues for the group)
     if ((tid >= C::B_KF && tid < C::B_KF + C::RING) || (tid >= C::B_VF && tid < C::B_VF + C::RING))
       cnt = C::NC * C::CG;
-    if ((tid >= C::B_QF && tid < C::B_QF + 2) || (tid >= C::B_PF && tid < C::B_PF + 2) ||
+    if ((tid >= C::B_KE && tid < C::B_KE + C::RING) || (tid >= C::B_VE && tid < C::B_VE + C::RING)) cnt = C::MT;
+    if ((tid >= C::B_QF && tid < C::B_QF + 2) || (tid >= C::B_PF && tid < C::B_PF + 2 * C::MT) ||
         (tid >= C::B_OE && tid < C::B_OE + 2))
       cnt = 4 * C::CG;
     tc::mbar_init(bar(tid), cnt);
@@ -428,22 +436,26 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
         tc::mbar_arrive(bar(C::B_INFOF + ng % C::NGRP));
       }
     }
-  } else if (warp == C::W_MMA) {
+  } else if (warp >= C::W_MMA) {
     // =============================== the products, issued by one elected lane
-    // (what the issue depends on stays the same for the warp, in uniform registers, and
-    // ring slots follow from a tile's number: the issue is one warp's serial code)
-    constexpr uint32_t id_qk = tc::idesc_f16(128 * C::CG, 128, 0, 0);
+    // A warp per accumulator, as the issue is a warp's serial code: one warp for both bound
+    // the kernel (8192 tokens of 64 heads of 128: 1121 us instead of 863).  Both run the
+    // same code (two copies of it: 879, and 708 instead of 656 for 4096 behind 12288 of 32
+    // heads of 64: the fetch of instructions is what the roles share).  What the issue
+    // depends on stays the same for the warp, in uniform registers, and ring slots follow
+    // from a tile's number.
+    constexpr uint32_t id_qk = tc::idesc_f16(128 * C::CG, C::KW, 0, 0);
     constexpr uint32_t id_pv = tc::idesc_f16(128 * C::CG, D, 0, 1);
     const uint64_t dq = tc::smem_desc(sQ, 16, 1024), dk = tc::smem_desc(sK, 16, 1024),
                    dv = tc::smem_desc(sV, C::PIECE, 1024);
     constexpr uint32_t TPR = C::RING / C::NC;  // tiles that a ring holds
     constexpr uint32_t TILE16 = C::NC * C::PIECE / 16;
+    const int t = __shfl_sync(0xffffffffu, warp - C::W_MMA, 0);
     int ns = 0;
-    uint32_t kt = 0, vt = 0;     // tiles of K and V taken
-    // parities, a bit each: weight tiles taken from a buffer, segments of a row tile's
-    // queries and of an accumulator; and whether an accumulator has had one
-    uint32_t np = 0, nq = 0, no = 0, had = 0;
-    uint32_t buf = 0;            // MT = 1: the next buffer for scores
+    uint32_t tiles0 = 0;       // key tiles of earlier segments
+    uint32_t done = 0;         // key tiles that the accumulator has taken in them
+    uint32_t no = 0;           // parity of the segments with tiles for the accumulator
+    bool had = false;          // has it had one?
     bool ok = true;
     auto wait_all = [&](uint32_t b, uint32_t parity) {  // arrivals of the whole group
       if (C::CG == 2 && LIM >= tc::kMinWaitLimit && __all_sync(0xffffffffu, tc::mbar_try_wait_cluster(b, parity)))
@@ -457,102 +469,109 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
       else
         tc::mma_commit(b);
     };
-    // scores of row tile qt's queries into buffer s from the next tile of K; fresh: the
-    // first products with it, last: the last
-    auto scores = [&](auto t_, uint32_t s, bool fresh, bool last, int qt) {
-      const uint32_t x = kt % TPR;
-      if (fresh) wait_all(bar(C::B_KF + x), (kt / TPR) & 1);
-      tc::tc_fence_after();
-      if (ok && tc::elect_one()) {
-        const uint64_t b = dk + x * TILE16;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          // (64 channels of 128 rows of Q, of KR rows of K)
-          const uint64_t ak = dq + qt * (C::QT / 16) + (k >> 2) * 1024 + 2 * (k & 3),
-                         bk = b + (k >> 2) * (C::KR * 8) + 2 * (k & 3);
-          if constexpr (C::CG == 2)
-            tc::mma_ss_pair(C::SCOL + s * 128, ak, bk, id_qk, k > 0);
-          else
-            tc::mma_ss(C::SCOL + s * 128, ak, bk, id_qk, k > 0);
-        }
-        commit(bar(C::B_SF + s));
-        if (last) commit(bar(C::B_KE + x));
-      }
-      __syncwarp();
-      mma_issued = true;
-      if (last) ++kt;
-    };
-    // the accumulator of row tile t takes the weights in buffer s; done: PV is told
-    auto values = [&](auto t_, uint32_t s, bool first, bool done, bool fresh, bool last) {
-      constexpr int t = decltype(t_)::value;
-      const uint32_t x = vt % TPR;
-      wait_all(bar(C::B_PF + s), (np >> s) & 1);
-      np ^= 1u << s;
-      if (first && ((had >> t) & 1)) wait_all(bar(C::B_OE + t), ((no >> t) & 1) ^ 1);
-      if (fresh) wait_all(bar(C::B_VF + x), (vt / TPR) & 1);
-      tc::tc_fence_after();
-      if (ok && tc::elect_one()) {
-        const uint64_t b = dv + x * TILE16;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t ak = C::SCOL + s * 128 + k * 8;
-          if constexpr (C::CG == 2)
-            tc::mma_ts_pair(C::OCOL + t * D, ak, b + 128 * k, id_pv, !first || k > 0);
-          else
-            tc::mma_ts(C::OCOL + t * D, ak, b + 128 * k, id_pv, !first || k > 0);
-        }
-        if (last) commit(bar(C::B_VE + x));
-        if (done) commit(bar(C::B_PV + s));
-      }
-      __syncwarp();
-      if (last) ++vt;
-    };
-    constexpr std::integral_constant<int, 0> T0{};
-    constexpr std::integral_constant<int, C::MT - 1> T1{};
+    // A step's buffer, and the parity of its use: step h of the accumulator's tile n.
+    auto buffer = [&](uint32_t n, int h) -> uint32_t { return 2 * t + (C::SPT == 2 ? h : n & 1); };
+    auto parity = [&](uint32_t n) -> uint32_t { return (C::SPT == 2 ? n : n >> 1) & 1; };
     while (ok) {
       if (!(ok = warp_wait(bar(C::B_SEGF + ns % C::NSEG), (ns / C::NSEG) & 1))) break;
       const Segment &sg = seg_s[ns % C::NSEG];
       const int tiles = __shfl_sync(0xffffffffu, sg.j1 - sg.j0, 0);
-      const bool two = C::MT == 2 && __shfl_sync(0xffffffffu, sg.rows, 0) > 128 * C::CG;
+      const bool solo = C::MT == 2 && __shfl_sync(0xffffffffu, sg.rows, 0) <= 128 * C::CG;
       __syncwarp();
       if (tc::elect_one()) tc::mbar_arrive(bar(C::B_SEGE + ns % C::NSEG));
       ++ns;
       if (tiles <= 0) break;
       if (rank > 0) continue;  // (the first CTA issues for both)
-      wait_all(bar(C::B_QF), nq & 1);
-      if (two) wait_all(bar(C::B_QF + 1), (nq >> 1) & 1);
-      if constexpr (C::MT == 2) {
-        if (two) {
-#pragma unroll 1
-          for (int j = -1; j < tiles && ok; ++j) {
-            const bool more = j + 1 < tiles;
-            if (j >= 0) values(T0, 0, j == 0, !more, true, false);
-            if (more) scores(T0, 0, true, false, 0);
-            if (j >= 0) values(T1, 1, j == 0, !more, false, true);
-            if (more) scores(T1, 1, false, true, 1);
+      // One tile of rows: the key tiles go to the two accumulators in turn.  Each gives
+      // back the other's tile beside its own, so that neither is a ring ahead.
+      const int qt = solo ? 0 : t, step = solo ? 2 : 1, n = solo ? (tiles + 1 - t) / 2 : tiles;
+      const uint32_t first = tiles0 + (solo ? t : 0);
+      auto other = [&](int i) -> int { return 2 * i + 1 - t; };
+      // scores of step h of the accumulator's tile i
+      auto scores = [&](int i, int h) {
+        const uint32_t kt = first + i * step, x = kt % TPR, buf = buffer(done + i, h);
+        if (h == 0) wait_all(bar(C::B_KF + x), (kt / TPR) & 1);
+        tc::tc_fence_after();
+        if (ok && tc::elect_one()) {
+          const uint64_t b = dk + x * TILE16 + h * (C::KR * 4);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            // (64 channels of 128 rows of Q, of KR rows of K)
+            const uint64_t ak = dq + qt * (C::QT / 16) + (k >> 2) * 1024 + 2 * (k & 3),
+                           bk = b + (k >> 2) * (C::KR * 8) + 2 * (k & 3);
+            if constexpr (C::CG == 2)
+              tc::mma_ss_pair(C::SCOL + buf * C::KW, ak, bk, id_qk, k > 0);
+            else
+              tc::mma_ss(C::SCOL + buf * C::KW, ak, bk, id_qk, k > 0);
           }
-        } else {  // one tile of rows: the key tiles go to the two accumulators in turn
-#pragma unroll 1
-          for (int j = 0; j < tiles + 2 && ok; j += 2) {
-            if (j >= 2) values(T0, 0, j == 2, j >= tiles, true, true);
-            if (j < tiles) scores(T0, 0, true, true, 0);
-            if (j >= 2 && j - 1 < tiles) values(T1, 1, j == 2, j + 1 >= tiles, true, true);
-            if (j + 1 < tiles) scores(T1, 1, true, true, 0);
+          commit(bar(C::B_SF + buf));
+          if (h == C::SPT - 1) {
+            commit(bar(C::B_KE + x));
+            if (solo && other(i) < tiles) commit(bar(C::B_KE + (tiles0 + other(i)) % TPR));
           }
         }
-      } else {
+        __syncwarp();
+      };
+      // the accumulator takes the step's weights
+      auto values = [&](int i, int h) {
+        const uint32_t vt = first + i * step, x = vt % TPR, buf = buffer(done + i, h);
+        wait_all(bar(C::B_PF + buf), parity(done + i));
+        if (h == 0) {
+          if (i == 0 && had) wait_all(bar(C::B_OE + t), no ^ 1);
+          wait_all(bar(C::B_VF + x), (vt / TPR) & 1);
+        }
+        tc::tc_fence_after();
+        if (ok && tc::elect_one()) {
+          const uint64_t b = dv + x * TILE16 + h * (C::KW * 8);
+#pragma unroll
+          for (int k = 0; k < C::KW / 16; ++k) {
+            const uint32_t ak = C::SCOL + buf * C::KW + k * 8;
+            if constexpr (C::CG == 2)
+              tc::mma_ts_pair(C::OCOL + t * D, ak, b + 128 * k, id_pv, i > 0 || h > 0 || k > 0);
+            else
+              tc::mma_ts(C::OCOL + t * D, ak, b + 128 * k, id_pv, i > 0 || h > 0 || k > 0);
+          }
+          if (h == C::SPT - 1) {
+            commit(bar(C::B_VE + x));
+            if (solo && other(i) < tiles) commit(bar(C::B_VE + (tiles0 + other(i)) % TPR));
+          }
+          commit(bar(C::B_PV + buf));
+        }
+        __syncwarp();
+      };
+      if (n > 0) wait_all(bar(C::B_QF + t), no);
+      mma_issued = true;
+      // The scores two steps on follow the value product that frees their buffer.
+      if (n > 0) {
+        scores(0, 0);
+        if (C::SPT == 2) scores(0, 1);
+        if (C::SPT == 1 && n > 1) scores(1, 0);
+      }
 #pragma unroll 1
-        for (int j = -1; j < tiles && ok; ++j) {  // buffers alternate through all segments
-          const bool more = j + 1 < tiles;
-          if (more) scores(T0, buf, true, true, 0);
-          if (j >= 0) values(T0, buf ^ 1, j == 0, true, true, true);
-          if (more) buf ^= 1;
+      for (int i = 0; i < n && ok; ++i) {
+        const int to = i + 2 / C::SPT;
+#pragma unroll
+        for (int h = 0; h < C::SPT; ++h) {
+          values(i, h);
+          if (to < n) scores(to, h);
         }
       }
-      // (queries: of the row tiles; accumulators: of those used)
-      nq ^= two ? 3u : 1u;
-      no ^= two || tiles > 1 ? 3u : 1u;
-      had |= two || tiles > 1 ? 3u : 1u;
+      if (t == 1 && solo && (tiles & 1)) {  // the last tile has no other
+        const uint32_t kt = tiles0 + tiles - 1, x = kt % TPR;
+        wait_all(bar(C::B_KF + x), (kt / TPR) & 1);  // (the one before it in its place is done with)
+        wait_all(bar(C::B_VF + x), (kt / TPR) & 1);
+        if (ok && tc::elect_one()) {
+          commit(bar(C::B_KE + x));
+          commit(bar(C::B_VE + x));
+        }
+        __syncwarp();
+      }
+      tiles0 += tiles;
+      done += n;
+      if (n > 0) {
+        no ^= 1;
+        had = true;
+      }
     }
   } else if (warp >= C::W_DEC) {
     // =============================== decoders: a warp per piece
@@ -586,11 +605,11 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
           const int jl = turn / PPT, pc = turn % PPT, c = pc % C::NC;
           const bool isv = pc >= C::NC;
           const uint32_t x = (tiles + g0 + jl) * C::NC + c;  // the piece's number among K's or V's
-          // the rows of a piece: the CTA's keys of 64 channels, or of 64 after another (K);
-          // 128 keys of 64 of the CTA's channels (V)
+          // the rows of a piece: the CTA's keys (its part of each step's) of 64 channels, or
+          // of 64 after another (K); 128 keys of 64 of the CTA's channels (V)
           const Tile &tl = tile_s[(ng % C::NGRP) * 4 + jl];
-          const long long *bx = isv ? tl.v : tl.k + rank * (C::KR / 16);
-          const int left = kend - (j0 + g0 + jl) * kTile - (isv ? 0 : rank * C::KR) - r8;  // keys from row r8 on
+          const long long *bx = isv ? tl.v : tl.k + rank * C::BPS;
+          const int left = kend - (j0 + g0 + jl) * kTile - (isv ? 0 : rank * C::BPS * 16) - r8;  // keys from row r8 on
           const uint8_t *base = isv ? vb + rank * (D / C::CG) + 64 * c : kb + 64 * C::CG * c;
           const int64_t s8 = isv ? v8 : k8;
           uint4 raw[16];
@@ -598,9 +617,10 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const int ik = i % (C::KR / 8), dk0 = 64 * (i / (C::KR / 8));  // K: row in the channels' group
-              const int b16 = isv ? i >> 1 : ik >> 1;
+              const int kb16 = (ik >> 1) / C::BPS * (C::KW / 16) + (ik >> 1) % C::BPS;
+              const int b16 = isv ? i >> 1 : kb16;
               const long long at = bx[b16];
-              const bool live = at >= 0 && 8 * (isv ? i : ik) < left;
+              const bool live = at >= 0 && 16 * b16 + 8 * (i & 1) < left;
               raw[i] = make_uint4(0u, 0u, 0u, 0u);
               if (live) raw[i] = load_raw<decltype(wide_)::value>(base + at + (i & 1 ? s8 : 0) + (isv ? 0 : dk0));
             }
@@ -648,16 +668,8 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
     float2 *end_s = reinterpret_cast<float2 *>(gSm + C::S_END);
     int ns = 0, ng = 0, count = 0;
     bool alive = true;
-    // The products run in the order of their issue.  With two row tiles the value product
-    // of a tile is issued before the scores of the next, so it is done when they are
-    // there, and only a segment's last one has an arrival of its own (of segment n of the
-    // row tile).  With one the scores come first, up to two value products (of tiles x of
-    // all segments) are under way, and each buffer's has one.
-    auto values_done = [&](int x) -> bool { return warp_wait(bar(C::B_PV + (x & 1)), (x >> 1) & 1); };
-    auto last_done = [&](int x, int n) -> bool {
-      return C::MT == 2 ? warp_wait(bar(C::B_PV + t), n & 1) : values_done(x);
-    };
-    int nlive = 0;
+    // The value product of the row tile's step x of all segments.
+    auto values_done = [&](int x) -> bool { return warp_wait(bar(C::B_PV + 2 * t + (x & 1)), (x >> 1) & 1); };
     for (;;) {
       alive = alive && warp_wait(bar(C::B_SEGF + ns % C::NSEG), (ns / C::NSEG) & 1);
       // One answer for all softmax warps: they enter a segment, with its barriers that have no
@@ -710,6 +722,7 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
         }
         tc::fence_proxy_async_smem();
         arrive_first(bar(C::B_QF + t));
+        if (solo && j1 - j0 > 1) arrive_first(bar(C::B_QF + 1));  // (the other has tiles too)
       }
       if (solo && p.bf16) {  // the second group needs the rows' factors too
         tc::named_bar(4, 256);
@@ -717,7 +730,7 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
       }
       float m = -kInf, l = 0.f;
       bool bad = false;
-      int seen = 0;  // tiles of the segment
+      int seen = 0;  // steps of the segment
       for (int j = j0; j < j1; ++j) {
         const int jl = j - j0, g = ng % C::NGRP;
         if ((jl & 3) == 0) alive = alive && warp_wait(bar(C::B_INFOF + g), (ng / C::NGRP) & 1);
@@ -733,111 +746,117 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
           continue;
         }
         const Tile &tl = tile_s[g * 4 + (jl & 3)];
-        float a8[8], g8[8];
-        *reinterpret_cast<float4 *>(&a8[0]) = *reinterpret_cast<const float4 *>(&tl.a[0]);
-        *reinterpret_cast<float4 *>(&a8[4]) = *reinterpret_cast<const float4 *>(&tl.a[4]);
-        *reinterpret_cast<float4 *>(&g8[0]) = *reinterpret_cast<const float4 *>(&tl.g[0]);
-        *reinterpret_cast<float4 *>(&g8[4]) = *reinterpret_cast<const float4 *>(&tl.g[4]);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) a8[k] *= qs;
-        const int sb = C::MT == 2 ? t : count & 1;                 // score buffer
-        const int sn = C::MT == 2 ? count : count >> 1;            // its use
-        alive = alive && warp_wait(bar(C::B_SF + sb), sn & 1);
-        if (!alive) continue;
-        tc::tc_fence_after();
-        const int k0 = j * kTile;
-        const bool masked = k0 + kTile - 1 > min_lim;
-        const uint32_t sc = tbase + lane_off + C::SCOL + sb * 128;
-        if (masked) {  // what the row does not see becomes -infinity in place
-          int see = lim - k0;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c, see -= 32) {
-            uint32_t x[32];
-            tc::tmem_ld32(sc + 32 * c, x);
-            tc::tmem_wait_ld();
+        for (int half = 0; half < C::SPT; ++half) {
+          constexpr int NK = C::KW / 16;  // boxes of 16 keys
+          float a8[NK], g8[NK];
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (e > see) x[e] = 0xff800000u;
-            tc::tmem_st32(sc + 32 * c, x);
+          for (int k = 0; k < NK; k += 4) {
+            *reinterpret_cast<float4 *>(&a8[k]) = *reinterpret_cast<const float4 *>(&tl.a[half * NK + k]);
+            *reinterpret_cast<float4 *>(&g8[k]) = *reinterpret_cast<const float4 *>(&tl.g[half * NK + k]);
           }
-          tc::tmem_wait_st();
-        }
-        // the row's scores, 16 at a time, the next requested before these are looked at
-        uint32_t y[2][16];
-        float mx = -kInf;
-        tc::tmem_ld16(sc, y[0]);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          uint32_t(&x)[16] = y[k & 1];
-          tc::tmem_wait_ld();
-          tc::tmem_ld16(sc + 16 * ((k + 1) & 7), y[(k + 1) & 1]);  // (from the first again)
-          auto score = [&](int e) -> float { return __uint_as_float(x[e]); };
-          float m0 = max3(score(0), score(1), score(2)), m1 = max3(score(8), score(9), score(10));
-#pragma unroll
-          for (int e = 3; e < 7; e += 2) {
-            m0 = max3(m0, score(e), score(e + 1));
-            m1 = max3(m1, score(e + 8), score(e + 9));
-          }
-          mx = fmaxf(mx, fmaf(max3(m0, m1, fmaxf(score(7), score(15))), a8[k], g8[k]));
-        }
-        const bool raise = mx > m + kTau;
-        if (__any_sync(0xffffffffu, raise)) {
-          const float mn = raise ? mx : m;
-          const float f = raise ? (m == -kInf ? 0.f : fast_exp2(m - mn)) : 1.f;
-          l *= f;
-          m = mn;
-          if (seen > 0) {
-            if constexpr (C::MT == 1) alive = values_done(count - 1);
-            if (!alive) continue;
-            tc::tc_fence_after();
+          for (int k = 0; k < NK; ++k) a8[k] *= qs;
+          const int sb = 2 * t + (count & 1);  // score buffer
+          alive = alive && warp_wait(bar(C::B_SF + sb), (count >> 1) & 1);
+          if (!alive) break;
+          tc::tc_fence_after();
+          const int k0 = j * kTile + half * C::KW;
+          const bool masked = k0 + C::KW - 1 > min_lim;
+          const uint32_t sc = tbase + lane_off + C::SCOL + sb * C::KW;
+          if (masked) {  // what the row does not see becomes -infinity in place
+            int see = lim - k0;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-              uint32_t r[16];
-              tc::tmem_ld16(tbase + lane_off + C::OCOL + t * D + c, r);
+            for (int c = 0; c < C::KW / 32; ++c, see -= 32) {
+              uint32_t x[32];
+              tc::tmem_ld32(sc + 32 * c, x);
               tc::tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
-              tc::tmem_st16(tbase + lane_off + C::OCOL + t * D + c, r);
+              for (int e = 0; e < 32; ++e)
+                if (e > see) x[e] = 0xff800000u;
+              tc::tmem_st32(sc + 32 * c, x);
+            }
+            tc::tmem_wait_st();
+          }
+          // The row's scores, 16 at a time, the next requested before these are looked at.
+          // (64 of them held in registers, or one pass whose sums tell whether the weights
+          // fit, took as long; rolled into loops that wait for each request, 8 % longer.)
+          uint32_t y[2][16];
+          float mx = -kInf;
+          tc::tmem_ld16(sc, y[0]);
+#pragma unroll
+          for (int k = 0; k < NK; ++k) {
+            uint32_t(&x)[16] = y[k & 1];
+            tc::tmem_wait_ld();
+            tc::tmem_ld16(sc + 16 * ((k + 1) % NK), y[(k + 1) & 1]);  // (from the first again)
+            auto score = [&](int e) -> float { return __uint_as_float(x[e]); };
+            float m0 = max3(score(0), score(1), score(2)), m1 = max3(score(8), score(9), score(10));
+#pragma unroll
+            for (int e = 3; e < 7; e += 2) {
+              m0 = max3(m0, score(e), score(e + 1));
+              m1 = max3(m1, score(e + 8), score(e + 9));
+            }
+            mx = fmaxf(mx, fmaf(max3(m0, m1, fmaxf(score(7), score(15))), a8[k], g8[k]));
+          }
+          const bool raise = mx > m + kTau;
+          if (__any_sync(0xffffffffu, raise)) {
+            const float mn = raise ? mx : m;
+            const float f = raise ? (m == -kInf ? 0.f : fast_exp2(m - mn)) : 1.f;
+            l *= f;
+            m = mn;
+            if (seen > 0) {
+              alive = values_done(count - 1);
+              if (!alive) break;
+              tc::tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < D; c += 16) {
+                uint32_t r[16];
+                tc::tmem_ld16(tbase + lane_off + C::OCOL + t * D + c, r);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+                tc::tmem_st16(tbase + lane_off + C::OCOL + t * D + c, r);
+              }
             }
           }
-        }
-        const float base = m == -kInf ? 0.f : m;
-        // weights of 16 keys at a time into the place of scores that have been read
-        float inv = tl.inv[0];
-        int badb = tl.bad[0];
+          const float base = m == -kInf ? 0.f : m;
+          // weights of 16 keys at a time into the place of scores that have been read
+          float inv = tl.inv[half * NK];
+          int badb = tl.bad[half * NK];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          uint32_t(&x)[16] = y[k & 1];
-          tc::tmem_wait_ld();
-          if (k < 7) tc::tmem_ld16(sc + 16 * (k + 1), y[(k + 1) & 1]);
-          const float2 A = make_float2(a8[k], a8[k]), B = make_float2(g8[k] - base, g8[k] - base);
-          float2 sum = make_float2(0.f, 0.f);
-          uint32_t h[8];
+          for (int k = 0; k < NK; ++k) {
+            uint32_t(&x)[16] = y[k & 1];
+            tc::tmem_wait_ld();
+            if (k < NK - 1) tc::tmem_ld16(sc + 16 * (k + 1), y[(k + 1) & 1]);
+            const float2 A = make_float2(a8[k], a8[k]), B = make_float2(g8[k] - base, g8[k] - base);
+            float2 sum = make_float2(0.f, 0.f);
+            uint32_t h[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float2 w = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), A, B);
-            w.x = fast_exp2(w.x);
-            w.y = fast_exp2(w.y);
-            sum = add2(sum, w);
-            h[e] = pack_half2(w.x, w.y);
+            for (int e = 0; e < 8; ++e) {
+              float2 w = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), A, B);
+              w.x = fast_exp2(w.x);
+              w.y = fast_exp2(w.y);
+              sum = add2(sum, w);
+              h[e] = pack_half2(w.x, w.y);
+            }
+            l = fmaf(sum.x + sum.y, inv, l);
+            if (badb && k0 + 16 * k <= lim) bad = true;
+            if (k < NK - 1) {
+              inv = tl.inv[half * NK + k + 1];
+              badb = tl.bad[half * NK + k + 1];
+            }
+            tc::tmem_st8(sc + 8 * k, h);
           }
-          l = fmaf(sum.x + sum.y, inv, l);
-          if (badb && k0 + 16 * k <= lim) bad = true;
-          if (k < 7) {
-            inv = tl.inv[k + 1];
-            badb = tl.bad[k + 1];
-          }
-          tc::tmem_st8(sc + 8 * k, h);
+          tc::tmem_wait_st();
+          tc::tc_fence_before();
+          arrive_first(bar(C::B_PF + sb));
+          ++count;
+          ++seen;
         }
-        tc::tmem_wait_st();
-        tc::tc_fence_before();
-        arrive_first(bar(C::B_PF + sb));
-        group_end();
-        ++count;
-        ++seen;
+        if (alive) group_end();
       }
       // ---- the rows out of TMEM
-      if (seen > 0) alive = alive && last_done(count - 1, nlive++);
+      if (seen > 0) alive = alive && values_done(count - 1);
       tc::tc_fence_after();
       if (bad) l = -1.f;
       float f0 = 1.f, f1 = 0.f;  // of the accumulators
@@ -912,13 +931,14 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
   tc::cp_async_wait_all();
   __syncthreads();
   bool aborted = *abort_f != 0;
-  if (warp == C::W_MMA && aborted && mma_issued && tc::elect_one()) {
+  if (aborted && mma_issued && tc::elect_one()) {  // (of an issuing warp, its products)
+    const uint32_t drain = bar(C::B_DRAIN + warp - C::W_MMA);
     if constexpr (C::CG == 2)
-      tc::mma_commit_pair(bar(C::B_DRAIN));
+      tc::mma_commit_pair(drain);
     else
-      tc::mma_commit(bar(C::B_DRAIN));
+      tc::mma_commit(drain);
     volatile int no_abort = 0;
-    tc::mbar_wait_brief(bar(C::B_DRAIN), 0, &no_abort, p.drain_limit);
+    tc::mbar_wait_brief(drain, 0, &no_abort, p.drain_limit);
   }
   __syncwarp();
   if constexpr (C::CG == 2) {

@@ -469,3 +469,19 @@ def test_repeated_calls_give_the_same_bits(D, sms):
         vae4.verify_attn_e4m3_chunk(qd, k, v, bt, seq, sc, out, ws, num_sms=sms)
     assert bool((outs == outs[0]).all()) and vae4.read_status(ws) == 0
     check(outs[0], *reference(c, q))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("sms", [2, 12])
+def test_units_of_every_number_of_tiles_in_turn(D, sms):
+    """Few rows and many, one tile of keys and several, one unit after another on the
+    same SMs: two accumulators that take the tiles in turn, or one alone."""
+    lens = []
+    for n in range(1, 12):
+        lens += [(128 * n - 5, 1), (3, 1), (128 * n + 131, 130), (100, 40), (64, 64), (700, 1)]
+    c = Cache(lens, 2, D, 32, 16, seed=D)
+    q = queries(c, 130, 3)
+    got, status = attend(c, q, num_sms=sms)
+    assert status == 0
+    check(got, *reference(c, q))
+    assert torch.equal(got, attend(c, q, num_sms=sms)[0])
