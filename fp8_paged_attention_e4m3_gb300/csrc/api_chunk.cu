@@ -19,6 +19,10 @@ int plan_chunk(int64_t B, int64_t Hkv, int64_t G, int64_t Qmax, int64_t D, int64
   // a group of CTAs for every tile at most (each unit counts one more for its set-up)
   const int64_t units = B * Hkv * ((Qmax * G + R - 1) / R);
   const int64_t tiles = units * ((cap + 127) / 128 + 1);
+  // The device counts the batch's work in G-ths of a key, and divides a unit's by products
+  // with its tiles: both have to stay inside 63 bits.
+  if ((double)G * cap * (cap / 128 + 1) >= 0x1p62 || (double)units * G * (cap + 1024) >= 0x1p62)
+    return VAE4_ERR_SHAPE;
   o->ctas = (int)std::min<int64_t>(std::max(1, std::min(sms, kMaxChunkCtas) / chunk_group((int)D)), tiles);
   o->split_off = kStatusBytes;
   o->ml_off = align_up(o->split_off + o->ctas * (int64_t)sizeof(ChunkSplit), 256);

@@ -669,7 +669,9 @@ int verify_attn_e4m3_chunk(const vae4_tensor *q, const vae4_tensor *k_cache,
 /* Bytes of workspace of a verify_attn_e4m3_chunk call: the status word, and for each
  * SM (up to 1024; fewer if the batch has fewer tiles of 128 keys) 32 bytes and two
  * FP32 partial states, (max, sum) and unnormalised P.V of 256 rows (D = 256: 128).
- * Arguments and errors as verify_attn_e4m3_workspace_bytes. */
+ * Arguments and errors as verify_attn_e4m3_workspace_bytes.  VAE4_ERR_SHAPE, here and in
+ * the call, where (Hq / Hkv) max_seq_len^2 / 128, or the batch's work counted in keys of
+ * units of 128 to 512 rows times Hq / Hkv, pass 62 bits. */
 int64_t verify_attn_e4m3_chunk_workspace_bytes(int B, int Hq, int Hkv, int Qmax, int D,
                                                int max_seq_len, int num_sms);
 
