@@ -573,10 +573,14 @@ __global__ void __launch_bounds__(256) compact_counts_kernel(const __grid_consta
 }
 
 // The limit of a kernel's dynamic shared memory, raised once per context to the most
-// that any call needs (as for the visit lists).
+// that any call needs (as for the visit lists).  The 48 KB that every launch may have are
+// for a kernel's static arrays too.
+constexpr size_t kStaticSmem = 1024;  // at least what any of them declares
+static_assert(sizeof(ClusterSums) + 64 <= kStaticSmem && kPoolThreads / 32 * sizeof(int4) <= kStaticSmem,
+              "static shared memory");
 template <auto Kernel>
 cudaError_t allow_smem(size_t most, size_t smem) {
-  if (smem <= 48 * 1024) return cudaSuccess;
+  if (smem + kStaticSmem <= 48 * 1024) return cudaSuccess;
   constexpr int kDevs = 64;
   static std::atomic<unsigned long long> configured[kDevs] = {};
   int dev = 0;
