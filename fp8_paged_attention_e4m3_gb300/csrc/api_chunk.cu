@@ -180,7 +180,12 @@ int verify_attn_e4m3_chunk(const vae4_tensor *q, const vae4_tensor *k_cache, con
   p.bf16 = q->dtype == VAE4_BF16;
   p.e5m2 = (o.flags & VAE4_FLAG_KV_E5M2) != 0;
   p.ctas = plan.ctas;
-  p.alpha = (o.softmax_scale > 0.f ? o.softmax_scale : 1.0f / sqrtf((float)D)) * 1.4426950408889634f;
+  // (the product of two FP32 numbers is exact in 64 bits, and may be too small or too large
+  // for 32)
+  const double alpha = (double)(o.softmax_scale > 0.f ? o.softmax_scale : 1.0f / sqrtf((float)D)) * 1.4426950408889634f;
+  int e = 1;
+  p.alpha = (float)(2 * (std::isfinite(alpha) ? std::frexp(alpha, &e) : alpha));
+  p.alpha_e = e - 1;
   p.wait_limit = (o.flags & VAE4_FLAG_TEST_SHORT_WAITS) ? kShortWaitCycles : kWaitLimitCycles;
   p.drain_limit = kWaitLimitCycles;
   if (launch_chunk(p, cu(stream)) != cudaSuccess) return VAE4_ERR_CUDA;

@@ -29,6 +29,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <limits.h>
+
 #include <atomic>
 #include <type_traits>
 
@@ -100,7 +102,7 @@ static_assert(sizeof(Segment) == 64, "layout");
 // What the roles have to know of a tile, for each of its boxes of 16 keys.
 struct alignas(16) Tile {
   long long k[8], v[8];  // where the rows start, from the caches' bases; -1: no keys, or invalid
-  float a[8], g[8];      // a score in log2 units per raw product, log2 s_V
+  float a[8], g[8];      // s_K, log2 s_V
   float inv[8];          // 1 / s_V
   int bad[8];
 };
@@ -269,10 +271,10 @@ __device__ __forceinline__ void st_shared16(uint32_t at, uint32_t a, uint32_t b,
 // five operations, 8192 tokens of 64 heads of 128 took 1485 us).  The row is multiplied
 // with the power of two that brings its largest magnitude to 2^14 .. 2^15: BF16's 8 bits
 // then are FP16's down to 2^-28 of that, and what is smaller is off by at most 2^-39 of it,
-// far less than the FP32 sum of the products is off by.  Returns the power's inverse (1 for
-// a row of zeros; infinities and NaN stay what they are).
+// far less than the FP32 sum of the products is off by.  Returns the exponent of the power's
+// inverse (0 for a row of zeros; infinities and NaN stay what they are).
 template <int D>
-__device__ __forceinline__ float row_to_f16(uint8_t *q, int r) {
+__device__ __forceinline__ int row_to_f16(uint8_t *q, int r) {
   auto at = [&](int c) -> uint4 * {
     return reinterpret_cast<uint4 *>(q + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
   };
@@ -299,7 +301,7 @@ __device__ __forceinline__ float row_to_f16(uint8_t *q, int r) {
     v.w = pack_half2(__uint_as_float(v.w << 16) * f, __uint_as_float(v.w & 0xFFFF0000u) * f);
     *at(c) = v;
   }
-  return __int_as_float((e - 14) << 23);
+  return e - 141;
 }
 
 __device__ __forceinline__ uint32_t pack16(float a, float b, int bf16) {
@@ -437,7 +439,7 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
             if (sk >= kMinScale && sk <= kMaxScale && sv >= kMinScale && sv <= kMaxScale) {
               xk = (long long)page * p.k_ps + slot * p.k_ts + s.h * p.k_hs;
               xv = (long long)page * p.v_ps + slot * p.v_ts + s.h * p.v_hs;
-              xa = p.alpha * sk;
+              xa = sk;
               xg = __log2f(sv);
               xi = __fdividef(1.f, sv);
               bits = 0;
@@ -723,10 +725,10 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
         row_s[tr] = live ? s.b * p.q_sb + i * p.q_si + head * p.q_sh : -1;
         lim = live ? s.L - s.q + i : s.kend - 1;
       }
-      const int min_lim = __reduce_min_sync(0xffffffffu, lim);
+      int min_lim = __reduce_min_sync(0xffffffffu, lim);
       tc::named_bar(2 + t, 128);
       const bool has_q = !solo || t == 0;  // the group stages the queries
-      float qs = 1.f;  // what a raw score of the row has to be multiplied with
+      int qe = 0;  // the row's queries have to be multiplied with 2^qe
       if (has_q) {
         constexpr int QCH = D / 8;  // 16-byte pieces per row
         const __half *qb = static_cast<const __half *>(p.q);  // (or BF16)
@@ -740,8 +742,8 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
         tc::cp_async_wait_all();
         if (p.bf16) {
           tc::named_bar(2 + t, 128);
-          qs = row_to_f16<D>(gbase + C::OFF_Q + t * C::QT, tr);
-          if (solo) end_s[tr].x = qs;
+          qe = row_to_f16<D>(gbase + C::OFF_Q + t * C::QT, tr);
+          if (solo) end_s[tr].x = __int_as_float(qe);
         }
         tc::fence_proxy_async_smem();
         arrive_first(bar(C::B_QF + t));
@@ -749,8 +751,18 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
       }
       if (solo && p.bf16) {  // the second group needs the rows' factors too
         tc::named_bar(4, 256);
-        qs = end_s[tr].x;
+        qe = __float_as_int(end_s[tr].x);
       }
+      // A raw score times s_K of 2^-40 .. 2^40 and `qs` is one in log2 units.  Where that
+      // factor would leave FP32's normal range, so that a zero could become NaN, and the
+      // -infinity of a hidden key too, raw scores are first multiplied with `pre`, in the
+      // pass that hides keys.  (A power past FP32's own range takes every score to zero or
+      // infinity, as the true one would.)
+      qe += p.alpha_e;
+      const int ce = min(max(qe, -86), 86);
+      const float qs = p.alpha * __int_as_float((127 + ce) << 23);
+      const float pre = __int_as_float((127 + min(max(qe - ce, -126), 127)) << 23);
+      if (__any_sync(0xffffffffu, qe != ce)) min_lim = INT_MIN;  // the pass at every step
       float m = -kInf, l = 0.f;
       bool bad = false;
       int seen = 0;  // steps of the segment
@@ -787,7 +799,7 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
           const int k0 = j * kTile + half * C::KW;
           const bool masked = k0 + C::KW - 1 > min_lim;
           const uint32_t sc = tbase + lane_off + C::SCOL + sb * C::KW;
-          if (masked) {  // what the row does not see becomes -infinity in place
+          if (masked) {  // in place: what the row does not see becomes -infinity
             int see = lim - k0;
 #pragma unroll 1
             for (int c = 0; c < C::KW / 32; ++c, see -= 32) {
@@ -796,7 +808,7 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
               tc::tmem_wait_ld();
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (e > see) x[e] = 0xff800000u;
+                x[e] = e > see ? 0xff800000u : __float_as_uint(__uint_as_float(x[e]) * pre);
               tc::tmem_st32(sc + 32 * c, x);
             }
             tc::tmem_wait_st();

@@ -41,7 +41,8 @@ struct ChunkParams {
   int32_t B, Qmax, Hkv, G, D, page;
   int32_t bf16, e5m2;
   int32_t ctas;                // groups of CTAs (chunk_group)
-  float alpha;                 // softmax_scale log2(e)
+  float alpha;                 // softmax_scale log2(e) = alpha 2^alpha_e, 1 <= alpha <= 2
+  int32_t alpha_e;
   long long wait_limit, drain_limit;  // SM cycles
 };
 
