@@ -29,8 +29,6 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <limits.h>
-
 #include <atomic>
 #include <type_traits>
 
@@ -340,6 +338,7 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
   extern __shared__ uint8_t smem_raw[];
   const float kInf = __int_as_float(0x7f800000);
   constexpr float kTau = 15.0f;  // weights up to 2^15, inside FP16
+  constexpr float kLarge = 0x1p12f;  // references from here on take rounded scores
 
   const uint32_t raw_addr = smem_u32(smem_raw);
   const uint32_t sbase = (raw_addr + 1023u) & ~1023u;
@@ -725,7 +724,7 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
         row_s[tr] = live ? s.b * p.q_sb + i * p.q_si + head * p.q_sh : -1;
         lim = live ? s.L - s.q + i : s.kend - 1;
       }
-      int min_lim = __reduce_min_sync(0xffffffffu, lim);
+      const int min_lim = __reduce_min_sync(0xffffffffu, lim);
       tc::named_bar(2 + t, 128);
       const bool has_q = !solo || t == 0;  // the group stages the queries
       int qe = 0;  // the row's queries have to be multiplied with 2^qe
@@ -755,14 +754,17 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
       }
       // A raw score times s_K of 2^-40 .. 2^40 and `qs` is one in log2 units.  Where that
       // factor would leave FP32's normal range, so that a zero could become NaN, and the
-      // -infinity of a hidden key too, raw scores are first multiplied with `pre`, in the
-      // pass that hides keys.  (A power past FP32's own range takes every score to zero or
-      // infinity, as the true one would.)
+      // -infinity of a hidden key too, raw scores are first multiplied with `pre`.  (A power
+      // past FP32's own range takes every score to zero or infinity, as the true one would.)
       qe += p.alpha_e;
       const int ce = min(max(qe, -86), 86);
       const float qs = p.alpha * __int_as_float((127 + ce) << 23);
       const float pre = __int_as_float((127 + min(max(qe - ce, -126), 127)) << 23);
-      if (__any_sync(0xffffffffu, qe != ce)) min_lim = INT_MIN;  // the pass at every step
+      // Are the row's scores rounded to log2 units, in place, before anything else?  As a
+      // rule one operation makes the exponent of a weight from a raw score and log2 s_V - m,
+      // two roundings off by 2^-24 |m| each: below kLarge 2^-12 in all, but past 2^24 the
+      // weight of the largest key itself would be past FP16, or nothing.
+      bool rounded = qe != ce, any_rounded = __any_sync(0xffffffffu, rounded);
       float m = -kInf, l = 0.f;
       bool bad = false;
       int seen = 0;  // steps of the segment
@@ -799,42 +801,70 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
           const int k0 = j * kTile + half * C::KW;
           const bool masked = k0 + C::KW - 1 > min_lim;
           const uint32_t sc = tbase + lane_off + C::SCOL + sb * C::KW;
-          if (masked) {  // in place: what the row does not see becomes -infinity
-            int see = lim - k0;
-#pragma unroll 1
-            for (int c = 0; c < C::KW / 32; ++c, see -= 32) {
-              uint32_t x[32];
-              tc::tmem_ld32(sc + 32 * c, x);
-              tc::tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                x[e] = e > see ? 0xff800000u : __float_as_uint(__uint_as_float(x[e]) * pre);
-              tc::tmem_st32(sc + 32 * c, x);
-            }
-            tc::tmem_wait_st();
-          }
           // The row's scores, 16 at a time, the next requested before these are looked at.
           // (64 of them held in registers, or one pass whose sums tell whether the weights
           // fit, took as long; rolled into loops that wait for each request, 8 % longer.)
           uint32_t y[2][16];
-          float mx = -kInf;
-          tc::tmem_ld16(sc, y[0]);
+          float mx;
+          bool raise, some, round = rounded;
+#pragma unroll 1
+          for (;;) {
+            if (masked || any_rounded) {  // in place: what the row does not see becomes -infinity
+              int see = lim - k0;
+#pragma unroll 1
+              for (int c = 0; c < C::KW / 32; ++c, see -= 32) {
+                uint32_t x[32];
+                tc::tmem_ld32(sc + 32 * c, x);
+                tc::tmem_wait_ld();
+                if (round) {
 #pragma unroll
-          for (int k = 0; k < NK; ++k) {
-            uint32_t(&x)[16] = y[k & 1];
-            tc::tmem_wait_ld();
-            tc::tmem_ld16(sc + 16 * ((k + 1) % NK), y[(k + 1) & 1]);  // (from the first again)
-            auto score = [&](int e) -> float { return __uint_as_float(x[e]); };
-            float m0 = max3(score(0), score(1), score(2)), m1 = max3(score(8), score(9), score(10));
+                  for (int b = 0; b < 2; ++b) {
+                    const int k = half * NK + 2 * c + b;
+                    const float f = tl.a[k] * qs, g2 = tl.g[k];
 #pragma unroll
-            for (int e = 3; e < 7; e += 2) {
-              m0 = max3(m0, score(e), score(e + 1));
-              m1 = max3(m1, score(e + 8), score(e + 9));
+                    for (int e = 16 * b; e < 16 * b + 16; ++e)
+                      x[e] = __float_as_uint(fmaf(__uint_as_float(x[e]) * pre, f, g2));
+                  }
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (e > see) x[e] = 0xff800000u;
+                tc::tmem_st32(sc + 32 * c, x);
+              }
+              tc::tmem_wait_st();
             }
-            mx = fmaxf(mx, fmaf(max3(m0, m1, fmaxf(score(7), score(15))), a8[k], g8[k]));
+            if (round) {
+#pragma unroll
+              for (int k = 0; k < NK; ++k) {
+                a8[k] = 1.f;
+                g8[k] = 0.f;
+              }
+            }
+            mx = -kInf;
+            tc::tmem_ld16(sc, y[0]);
+#pragma unroll
+            for (int k = 0; k < NK; ++k) {
+              uint32_t(&x)[16] = y[k & 1];
+              tc::tmem_wait_ld();
+              tc::tmem_ld16(sc + 16 * ((k + 1) % NK), y[(k + 1) & 1]);  // (from the first again)
+              auto score = [&](int e) -> float { return __uint_as_float(x[e]); };
+              float m0 = max3(score(0), score(1), score(2)), m1 = max3(score(8), score(9), score(10));
+#pragma unroll
+              for (int e = 3; e < 7; e += 2) {
+                m0 = max3(m0, score(e), score(e + 1));
+                m1 = max3(m1, score(e + 8), score(e + 9));
+              }
+              mx = fmaxf(mx, fmaf(max3(m0, m1, fmaxf(score(7), score(15))), a8[k], g8[k]));
+            }
+            raise = mx > m + kTau;
+            some = __any_sync(0xffffffffu, raise);
+            if (!some) break;
+            round = raise && !rounded && fabsf(mx) >= kLarge;  // from this step on
+            if (!__any_sync(0xffffffffu, round)) break;
+            rounded |= round;
+            any_rounded = true;
           }
-          const bool raise = mx > m + kTau;
-          if (__any_sync(0xffffffffu, raise)) {
+          if (some) {
             const float mn = raise ? mx : m;
             const float f = raise ? (m == -kInf ? 0.f : fast_exp2(m - mn)) : 1.f;
             l *= f;

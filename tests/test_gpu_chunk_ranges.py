@@ -77,3 +77,80 @@ def test_factors_past_32_bits(D, kind, power, scale):
     got, status = attend(c, q, softmax_scale=scale)
     assert status == 0
     check(got, *reference(c, q, scale))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("sign", ["any", "negative"])
+@pytest.mark.parametrize("kind,size,scale_k", [("f16", 60000.0, -6), ("f16", 60000.0, 0), ("f16", 60000.0, 20), ("f16", 60000.0, 40),
+                                               ("bf16", 2.0 ** 40, 0), ("f16", 64.0, 9)])
+def test_large_scores(D, sign, kind, size, scale_k):
+    """Scores of 2^13 to 2^60, of both signs or all below zero.  A query is one channel of
+    the keys, so scores are exact products, equal codes give equal ones, and the largest of a
+    row stand apart by a sixteenth of themselves at least."""
+    c = Cache([(300, 300), (1100, 50), (17, 1)], 2, D, 32, 16, seed=D + scale_k)
+    if sign == "negative":
+        for k in (c.codes[0],):
+            k.copy_(torch.where(k == 0x7F, k, (k & 0x7F).clamp(0x20, 0x7E) | 0x80))
+    c.scales[:, 0] = torch.where(c.scales[:, 0].isnan(), c.scales[:, 0], 2.0 ** scale_k)
+    c.scales[:, 1] = torch.where(c.scales[:, 1].isnan(), c.scales[:, 1], 2.0 ** -8)  # (2^z s_V is what is rounded)
+    q = torch.zeros(3, 300, 4, D)
+    i = torch.arange(300)
+    q[:, i, :, i % D] = size
+    q[:, ::7] *= 2.0 ** -30 if kind == "bf16" else 2.0 ** -12  # ordinary rows beside them
+    q = q.to(KIND[kind][0])
+    for b, (_, n) in enumerate(c.lens):
+        q[b, n:] = float("nan")
+    got, status = attend(c, q)
+    assert status == 0
+    check(got, *reference(c, q))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("sms", [2, 0])
+def test_large_scores_that_come_late(D, sms):
+    """Ordinary scores, then some of 2^33, in the rows of one unit: what was summed before
+    them is forgotten, in parts of units too."""
+    c = Cache([(5000, 200)], 1, D, 64, 64, seed=D)
+    c.scales[:, 0] = torch.where(c.scales[:, 0].isnan(), c.scales[:, 0], 2.0 ** -9)
+    c.scales[:, 1] = torch.where(c.scales[:, 1].isnan(), c.scales[:, 1], 2.0 ** -8)
+    q = torch.zeros(1, 200, 2, D)
+    i = torch.arange(200)
+    q[:, i, :, i % D] = 8.0
+    q[:, 3::5] *= 4096
+    for t in (1900, 4400, 4850):
+        pg = int(c.table[0, t // 64])
+        c.scales[pg, 0] = 2.0 ** 24
+    q = q.half()
+    got, status = attend(c, q, num_sms=sms)
+    assert status == 0
+    check(got, *reference(c, q))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("kind,power,scale", FACTORS)
+def test_scores_past_32_bits(D, kind, power, scale):
+    """Scores that are +infinity in 32 bits, from a late key on: rows that see it are NaN, the
+    others are not concerned."""
+    c, q = past_32_bits(D, [(300, 150), (300, 300)], (0, 0x80), kind, power, scale)
+    c.codes[0][c.table[0, :6].long()] = 0  # the first such key is 193, the first query that sees it 43
+    got, status = attend(c, q, softmax_scale=scale)
+    assert status == 0
+    ref, tol = reference(c, q, scale)
+    assert bool(got[0, 43:150].isnan().all())
+    got[0, 43:150] = 0
+    ref[0, 43:150] = tol[0, 43:150] = 0
+    check(got, ref, tol)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_large_scores_do_not_concern_other_rows(D):
+    """Rows of large scores beside ordinary ones in one warp: the others keep their bits."""
+    c = Cache([(700, 300)], 1, D, 32, 16, seed=D)
+    q = queries(c, 300, 2)
+    want, _ = attend(c, q)
+    large = torch.rand(300, 2, generator=torch.Generator().manual_seed(D)) < 0.1
+    q[0][large] *= 2.0 ** 11
+    got, status = attend(c, q)
+    assert status == 0
+    assert torch.equal(got[0][~large], want[0][~large])
+    assert not got.isnan().any() and bool((got[0][large] != want[0][large]).any())
