@@ -653,7 +653,8 @@ int64_t verify_attn_e4m3_sparse_workspace_bytes(int B, int Hq, int Hkv, int Qmax
  * BAD_SCALE); the others of the sequence are not concerned.  A query with a score of
  * NaN or +infinity gives a row of NaN, one whose scores are all -infinity zeros.
  * Scores, sums and weighted sums are FP32 and a weight enters its product in FP16, as
- * for verify_attn_e4m3_block_scaled and with its bound.  FP16 queries and K enter the
+ * for verify_attn_e4m3_block_scaled and with its bound, but for 2^-27 W in the place of
+ * 2^-25 W where the row's largest score is within 2^21.  FP16 queries and K enter the
  * scores exactly; a row of BF16 queries enters as FP16, scaled by a power of two, which
  * is exact down to 2^-28 of the row's largest magnitude (what is smaller is off by at
  * most 2^-39 of it).

@@ -7,7 +7,7 @@ import torch
 
 import fp8_paged_attention_e4m3_gb300 as vae4
 from test_gpu_blocks import Cache
-from test_gpu_chunk import KIND, attend, check, queries, reference
+from test_gpu_chunk import KIND, attend, check, codes, queries, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -154,3 +154,42 @@ def test_large_scores_do_not_concern_other_rows(D):
     assert status == 0
     assert torch.equal(got[0][~large], want[0][~large])
     assert not got.isnan().any() and bool((got[0][large] != want[0][large]).any())
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_a_first_key_that_outweighs_all_others(D, kind):
+    """The first key has some 2^24 times the weight of any other, and values of zero, so the
+    output is the sum of the others, all in one CTA's part of the keys.  The reference of the
+    weights goes down to 2^-10 of the first key's after the first step of at most 128 keys
+    (there 2^-2): a weight is off by 2^-11 of itself, or by 2^-25 of the reference."""
+    L, n = 70000, 40
+    c = Cache([(L, n)], 1, D, 64, 64, seed=D)
+    g = torch.Generator().manual_seed(D)
+    c.codes[0][:] = 0
+    pg = c.table[0, :-(-L // 64)].long()
+    c.codes[0][pg, :, :, 0] = (torch.randint(0, 0x59, (len(pg), 64, 1), generator=g) + 0x80 *  # up to 16
+                               torch.randint(0, 2, (len(pg), 64, 1), generator=g)).to(torch.uint8)
+    c.codes[0][pg[0], 0, 0, 0] = 0x7E  # 448
+    c.codes[1][pg[0], 0] = 0
+    c.codes[1][pg] &= 0x7F  # (sums that do not cancel)
+    c.scales = torch.where(c.scales.isnan(), c.scales, torch.ones(()))
+    q = torch.zeros(1, n, 2, D)
+    q[..., 0] = (0.92 + torch.arange(n) / 250.0)[None, :, None]
+    q = q.to(KIND[kind][0])
+    scale = 24.5 / 448 / math.log2(math.e)
+    ref, _ = reference(c, q, scale)
+    got, status = attend(c, q, softmax_scale=scale, num_sms=1)
+    assert status == 0
+    half = KIND[kind][1]
+    (K, _), (V, _) = codes(c, 0, 0), codes(c, 1, 0)
+    x = q[0, :, 0, 0].cuda().double()
+    z = x[:, None] * K[:, 0, 0] * scale
+    z.masked_fill_(torch.arange(L, device="cuda") > (L - n + torch.arange(n, device="cuda"))[:, None], float("-inf"))
+    e = torch.exp(z - z.amax(-1, keepdim=True))
+    l = e.sum(-1, keepdim=True)
+    A = e @ V[:, 0].abs() / l
+    small = (2.0 ** -27 * V[:128, 0].abs().sum(0) + 2.0 ** -35 * V[128:, 0].abs().sum(0)) / l  # W = 1: the first key's
+    tol = half * ref[0].abs() + (2.0 ** -10 * (A + ref[0, :, 0].abs()) + small)[:, None] + 2.0 ** -25
+    assert float(tol.max() / ref[0].max()) < 0.02
+    check(got[0], ref[0], tol)
