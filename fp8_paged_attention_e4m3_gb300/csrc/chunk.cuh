@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
 
   if (tid < C::NBARS) {
     uint32_t cnt = 1;
-    if (tid >= C::B_SEGE && tid < C::B_SEGE + C::NSEG) cnt = C::NSW + C::ND + C::MT;
+    if (tid >= C::B_SEGE && tid < C::B_SEGE + C::NSEG) cnt = C::NSW + C::ND + (rank == 0 ? C::MT : 0);
     if (tid >= C::B_INFOF && tid < C::B_INFOF + C::NGRP) cnt = 32;
     if (tid >= C::B_INFOE && tid < C::B_INFOE + C::NGRP) cnt = C::NSW + C::ND;
     // (those below are the first CTA's, whose thread issues for the group)
@@ -474,7 +474,8 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
     // same code (two copies of it: 879, and 708 instead of 656 for 4096 behind 12288 of 32
     // heads of 64: the fetch of instructions is what the roles share).  What the issue
     // depends on stays the same for the warp, in uniform registers, and ring slots follow
-    // from a tile's number.
+    // from a tile's number.  The first CTA of a pair issues for both; the other's warps have
+    // nothing to do, and do not wait for segments, which may take longer than any wait.
     constexpr uint32_t id_qk = tc::idesc_f16(128 * C::CG, C::KW, 0, 0);
     constexpr uint32_t id_pv = tc::idesc_f16(128 * C::CG, D, 0, 1);
     const uint64_t dq = tc::smem_desc(sQ, 16, 1024), dk = tc::smem_desc(sK, 16, 1024),
@@ -487,7 +488,7 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
     uint32_t done = 0;         // key tiles that the accumulator has taken in them
     uint32_t no = 0;           // parity of the segments with tiles for the accumulator
     bool had = false;          // has it had one?
-    bool ok = true;
+    bool ok = rank == 0;
     auto wait_all = [&](uint32_t b, uint32_t parity) {  // arrivals of the whole group
       if (C::CG == 2 && LIM >= tc::kMinWaitLimit && __all_sync(0xffffffffu, tc::mbar_try_wait_cluster(b, parity)))
         return;
@@ -512,7 +513,6 @@ __global__ void __launch_bounds__(Cfg<D>::NTHREADS, 1) chunk_kernel(const __grid
       if (tc::elect_one()) tc::mbar_arrive(bar(C::B_SEGE + ns % C::NSEG));
       ++ns;
       if (tiles <= 0) break;
-      if (rank > 0) continue;  // (the first CTA issues for both)
       // One tile of rows: the key tiles go to the two accumulators in turn.  Each gives
       // back the other's tile beside its own, so that neither is a ring ahead.
       const int qt = solo ? 0 : t, step = solo ? 2 : 1, n = solo ? (tiles + 1 - t) / 2 : tiles;

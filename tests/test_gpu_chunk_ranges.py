@@ -193,3 +193,24 @@ def test_a_first_key_that_outweighs_all_others(D, kind):
     tol = half * ref[0].abs() + (2.0 ** -10 * (A + ref[0, :, 0].abs()) + small)[:, None] + 2.0 ** -25
     assert float(tol.max() / ref[0].max()) < 0.02
     check(got[0], ref[0], tol)
+
+
+@pytest.mark.parametrize("D,q,G", [(128, 1, 1), (128, 130, 4), (256, 3, 2), (64, 2, 1)])
+def test_a_unit_of_seconds(D, q, G):
+    """One unit over 2^28 keys on one pair of CTAs takes longer than any wait may.  The first
+    4095 entries of its row are one page, whose keys have no weight beside the last one's,
+    which are alike: sums of powers of two, of which the output is the value."""
+    page, L = 65536, 1 << 28
+    k = torch.zeros(2, page, 1, D, dtype=torch.uint8, device="cuda")
+    k[0] = 0xFE  # -448
+    v = (0x38 + 8 * (torch.arange(D, device="cuda") % 3)).to(torch.uint8).expand(2, page, 1, D).contiguous()  # 1, 2, 4
+    bt = torch.zeros(1, L // page, dtype=torch.int32, device="cuda")
+    bt[0, -1] = 1
+    seq = torch.tensor([[L, q]], dtype=torch.int32, device="cuda")
+    x = torch.full((1, q, G, D), 0.25, dtype=torch.float16, device="cuda")
+    out = torch.zeros_like(x)
+    ws = torch.zeros(vae4.chunk_workspace_bytes(1, G, 1, q, D, L, 2), dtype=torch.uint8, device="cuda")
+    vae4.verify_attn_e4m3_chunk(x, k, v, bt, seq, torch.ones(1, 2, device="cuda"), out, ws, num_sms=2)
+    torch.cuda.synchronize()
+    assert vae4.read_status(ws) == 0
+    assert torch.equal(out, v[:1, :1].view(torch.float8_e4m3fn).half().expand_as(out))
