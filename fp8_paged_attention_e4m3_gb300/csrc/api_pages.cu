@@ -240,8 +240,8 @@ int verify_attn_e4m3_compact_pages(const vae4_tensor *block_table, const vae4_te
   p.moves = static_cast<int32_t *>(moves->data);
   p.moves_sb = moves->stride[0];
   p.n = (int32_t)moves->shape[0];
-  if (p.n == 0) return VAE4_OK;
-  if ((!p.pool.bt && p.pool.B > 0) || !p.pool.counts || !p.moves) return VAE4_ERR_NULL;
+  if (p.n == 0 && (!dev_status || p.pool.B == 0)) return VAE4_OK;  // (else entries are looked at)
+  if ((!p.pool.bt && p.pool.B > 0) || !p.pool.counts || (!p.moves && p.n > 0)) return VAE4_ERR_NULL;
   if (launch_compact_pages(p, cu(stream)) != cudaSuccess) return VAE4_ERR_CUDA;
   return VAE4_OK;
 }

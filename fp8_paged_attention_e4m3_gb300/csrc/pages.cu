@@ -534,7 +534,9 @@ __global__ void __launch_bounds__(kPoolThreads, 1)
     __stcg(p.moves + r * p.moves_sb, -1);
     __stcg(p.moves + r * p.moves_sb + 1, -1);
   }
-  if (moved == 0) return;  // the same for the whole cluster, and no remote access is left
+  // (the same for the whole cluster, and no remote access is left; without moves the
+  // table's entries are looked at for the status alone)
+  if (moved == 0 && (SPLIT || !o.status)) return;
   cl.sync();
   for (int r = first; r < moved; r += kPoolCtas * kPoolThreads) {
     const int from = __ldcg(p.moves + r * p.moves_sb), to = __ldcg(p.moves + r * p.moves_sb + 1);
@@ -555,7 +557,8 @@ __global__ void __launch_bounds__(kPoolThreads, 1)
 
 __global__ void __launch_bounds__(kPoolThreads) compact_table_kernel(const __grid_constant__ CompactParams p) {
   await_previous();
-  if (load_dep(p.moves) < 0) return;  // nothing moves
+  // nothing moves, and nobody asks for invalid entries
+  if (!p.pool.status && (p.n == 0 || load_dep(p.moves) < 0)) return;
   unsigned bad = 0;
   const int warps = gridDim.x * (kPoolThreads / 32), gwarp = blockIdx.x * (kPoolThreads / 32) + (threadIdx.x >> 5);
   each_entry(p.pool, share((int64_t)p.pool.B * p.pool.cols, gwarp, warps), [&](int b, int j, int e, bool in) {
@@ -659,6 +662,7 @@ cudaError_t launch_resize_pages(const ResizeParams &p, cudaStream_t stream) {
 }
 
 cudaError_t launch_compact_pages(const CompactParams &p, cudaStream_t stream) {
+  if (p.n == 0) return launch_dependent(compact_table_kernel, dim3(kPoolGrid), kPoolThreads, 0, stream, p);
   // (32 rows of 16384 entries, 16384 moves: 34 us, on a cluster 70)
   if ((int64_t)p.pool.B * p.pool.cols <= kSmallPool)
     return launch_cluster(compact_pages_kernel<false>, 0, stream, p);
