@@ -130,7 +130,8 @@ __global__ void __launch_bounds__(kListThreads) block_list_kernel(const ListPara
 cudaError_t launch_block_list(const ListParams &p, cudaStream_t stream) {
   const int nblk = (p.capacity + p.blk - 1) / p.blk;
   const int smem = (nblk + 7) / 8 * 16;
-  if (smem > 48 * 1024) {  // beyond the default dynamic shared-memory limit
+  // beyond the default limit of 48 KB, which is for the static array too
+  if (smem + kListWarps * (int)sizeof(int) > 48 * 1024) {
     // The limit belongs to the function in the device's context, whatever host
     // thread sets it: once per context, to the most that any call needs, so that
     // none lowers it between another's setting and launch.
