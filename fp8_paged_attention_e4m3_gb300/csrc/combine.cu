@@ -25,6 +25,8 @@
 // rows, computed in every block from the lengths), so the warps share them
 // evenly; rows without a live query are zero-filled before the grid
 // dependency wait (the split kernel does not touch the output).
+#include <algorithm>
+
 #include "combine_rows.cuh"
 #include "common.cuh"
 #include "kernels.h"
@@ -43,6 +45,7 @@ namespace {
 // one after another.
 constexpr int kCombineThreads = 512;
 constexpr int kWarps = kCombineThreads / 32;
+constexpr int kMostPartitions = 8192;  // of a sequence
 constexpr int kCacheB = 2048;   // lengths cached in shared memory up to this batch
 constexpr int kCacheTab = 2048; // device-plan stream entries cached up to this many
 
@@ -384,9 +387,13 @@ cudaError_t launch_combine(const CombineParams &p, cudaStream_t stream) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const int smem = (int)cfg.dynamicSmemBytes;
-    if (smem > 48 * 1024) {  // beyond the default dynamic shared-memory limit
+    // beyond the default limit of 48 KB, which is for the static arrays too; to the most
+    // that a call needs, so that none lowers it between another's setting and launch
+    constexpr int kStatic = kRowThreads / 32 * sizeof(float) + kRowGroups * kRowLanes * sizeof(float4);
+    if (smem + kStatic > 48 * 1024) {
       const cudaError_t e = cudaFuncSetAttribute(combine_rows_kernel,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 std::max(smem, kMostPartitions * 2 * (int)sizeof(float)));
       if (e != cudaSuccess) return e;
     }
     return cudaLaunchKernelEx(&cfg, combine_rows_kernel, p);

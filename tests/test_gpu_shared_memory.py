@@ -49,3 +49,17 @@ def sparse(blocks):
 @pytest.mark.parametrize("blocks", [24512, 24544, 24576, 24584])
 def test_visit_lists(blocks):
     alone(f"sparse({blocks})")
+
+
+def partitions(n):
+    q, k, v, bt, seq = pages(n)
+    out = torch.zeros_like(q)
+    ws = vae4.alloc_workspace(1, 1, 1, 1, 64, 16 * n, 16)
+    vae4.verify_attn_e4m3_kv(q, k, v, bt, seq, torch.ones(1, 2, device="cuda"), out, ws, partition_tokens=16)
+    assert vae4.read_status(ws) == 0
+    assert bool(((out.double() - 7 / 3).abs() <= 7 / 3 * 2.0 ** -10).all())  # n is a multiple of 3
+
+
+@pytest.mark.parametrize("n", [5625, 5631, 6000, 6144, 6147, 8190])
+def test_partitions_of_one_sequence(n):
+    alone(f"partitions({n})")
