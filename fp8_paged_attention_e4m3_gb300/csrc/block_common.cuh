@@ -2,6 +2,7 @@
 // programmatic dependent launches, waits and elections of the tcgen05 kernel.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -16,6 +17,15 @@ namespace vae4 {
 // over x / (n / 16) is below x / 2^38 < 2^-12 <= 1 / (n / 16).
 __device__ __forceinline__ int div16(int key, unsigned long long m) {
   return (int)((unsigned long long)(unsigned)(key >> 4) * m >> 38);
+}
+
+// Two outputs, each rounded once.
+__device__ __forceinline__ uint32_t pack16(float a, float b, int bf16) {
+  if (bf16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+  }
+  return pack_half2(a, b);
 }
 
 // Programmatic dependent launch.  A kernel launched so may be placed while the

@@ -302,14 +302,6 @@ __device__ __forceinline__ int row_to_f16(uint8_t *q, int r) {
   return e - 141;
 }
 
-__device__ __forceinline__ uint32_t pack16(float a, float b, int bf16) {
-  if (bf16) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&v);
-  }
-  return pack_half2(a, b);
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));

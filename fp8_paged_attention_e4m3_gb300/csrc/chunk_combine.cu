@@ -6,8 +6,6 @@
 // the row zeros.  Parts of the unit that starts in CTA c lie in slots c, ctas + c + 1,
 // ctas + c + 2, ...  CTAs past those of the units report invalid lengths and zero the
 // rows of sequences without tokens.
-#include <cuda_bf16.h>
-
 #include <algorithm>
 
 #include "block_common.cuh"
@@ -20,14 +18,6 @@ namespace vae4 {
 namespace {
 
 constexpr int kWarps = 8, kRowsPerCta = 8, kZeroCtas = 32;
-
-__device__ __forceinline__ uint32_t pack2(float a, float b, int bf16) {
-  if (bf16) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&v);
-  }
-  return pack_half2(a, b);
-}
 
 // lane's channels of a row: VN of them from VN * lane on
 template <int VN>
@@ -90,7 +80,7 @@ __global__ void __launch_bounds__(32 * kWarps) chunk_combine_kernel(const __grid
     const float inv = zero ? 0.f : __fdiv_rn(1.f, l);
 #pragma unroll
     for (int e = 0; e < VN; e += 2)
-      *reinterpret_cast<uint32_t *>(o + e) = zero ? 0u : pack2(a.v[e] * inv, a.v[e + 1] * inv, p.bf16);
+      *reinterpret_cast<uint32_t *>(o + e) = zero ? 0u : pack16(a.v[e] * inv, a.v[e + 1] * inv, p.bf16);
   };
   const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml);
   if (nP <= 2 * kWarps) {  // a warp per row
