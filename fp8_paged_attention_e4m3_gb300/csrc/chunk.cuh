@@ -10,19 +10,21 @@
 //
 // Both products are FP16: FP8 becomes FP16 exactly, in one conversion, and the tensor cores
 // add in FP32.  4 D operations per score against one exp2 and some four other instructions:
-// the tensor cores bound the kernel (D = 256: 0.88 of the measured dense rate), below that
-// the softmax, whose warps wait for the fetch of instructions and for tensor memory more
-// than for any unit (D = 128: 0.66; two softmax warps, a decoder and half an issuing warp per
-// scheduler issue in half of the cycles).
+// the tensor cores bound the kernel (D = 256: 0.87 of the measured dense rate), below that
+// the softmax's chain: its warps wait for the fetch of instructions and for tensor memory,
+// and no unit is full (D = 128: 0.66, tensor cores at work in 54 % of the cycles, instructions
+// issued in 46 %; D = 64: 0.38).
 //
 // A unit is R = 512 (D = 64 and 256: 256) rows of a KV head's queries: K and V are read and
 // decoded once for all of them, and where a tile of 128 keys would not leave room for two
 // tiles of rows (D >= 128), a pair of CTAs shares it, each decoding half.
 //
-// Measured: 8192 tokens of 64 heads on 8 of 128, FP16 863 us (1273 TFLOP/s), BF16 939; 2048
-// behind 65536 of 6 heads on 1 of 256, 480 us (1690); 4096 behind 12288 of 32 on 8 of 64,
-// 656 us (733), of 256 behind 4096, 576 us (1431); 64 tokens of 8 on 8 of 128 behind 131072,
-// 125 us (2.1 TB/s of keys: a row tile a quarter full, one pass of decoding per 64 rows).
+// Measured: 8192 tokens of 64 heads on 8 of 128, FP16 869 us (1266 TFLOP/s), BF16 944; 2048
+// behind 65536 of 6 heads on 1 of 256, 482 to 488 us (1670); 4096 behind 12288 of 32 on 8 of
+// 64, 656 us (733), of 256 behind 4096, 576 to 585 us (1420); 64 tokens of 8 on 8 of 128
+// behind 131072, 125 us (2.1 TB/s of keys: a row tile a quarter full, one pass of decoding per
+// 64 rows).  Scores that keep growing cost rescaled accumulators: the first with a standard
+// deviation of 4 in the place of 1 863 us, of 8 1078.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -41,8 +43,14 @@ namespace vae4 {
 namespace chunk {
 
 constexpr int kTile = 128;     // keys per tile
-constexpr int kUnitCost = 3;   // key tiles of time that a unit's set-up and end take
-constexpr int kMinTiles = 3;   // a CTA's share is at least this many tiles
+// Key tiles of time that a unit's set-up and end take.  (64 single tokens behind 500 to 2831,
+// 32 heads on 8 of 128: 171 us with 1, 160 with 2, 149 with 3, 140 with 5, 146 with 8; a batch of
+// chunks and single tokens, 24 heads on 8: 1446, 1441, 1435, 1436 and 1443, of 64 channels 592,
+// 587, 587, 590 and 597.)
+constexpr int kUnitCost = 3;
+// A CTA's share is at least this many tiles.  (32 of 1024 tokens of 2 heads on 1 of 64: 12.8 us
+// with 1, 12.2 with 2, 14.0 with 3, 15.8 with 5; larger calls do not tell.)
+constexpr int kMinTiles = 3;
 
 template <int D>
 struct Cfg {

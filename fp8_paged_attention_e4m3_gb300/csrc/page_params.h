@@ -10,7 +10,9 @@ namespace vae4 {
 constexpr int kMaxForkRows = 8192;     // a column tile of the table is held in shared memory
 constexpr int kMaxResizeRows = 16384;  // (pages, first written page) of every row are held there
 
-constexpr int kPoolGrid = 128;         // CTAs of 1024 threads that share a large pool
+// CTAs of 1024 threads that share a large pool (256 rows of 2048, 246 thousand pages: 39.6 us
+// with 32, 30.3 with 64, 29.3 with 128 and 152)
+constexpr int kPoolGrid = 128;
 
 // What a page holds of one tensor: n[0] x n[1] x n[2] runs of `run` vectors of
 // `vec` bytes, the runs' starts s[0 .. 2] bytes apart; neighbouring dimensions that

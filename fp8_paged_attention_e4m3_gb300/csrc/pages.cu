@@ -196,7 +196,11 @@ __global__ void __launch_bounds__(kForkThreads) fork_pages_kernel(const __grid_c
 // and atomics: 13 us for 8 rows of 64 entries, 11 to 13 for 64 moves.
 constexpr int kPoolThreads = 1024, kPoolCtas = 8;
 constexpr int kPoolWarps = kPoolThreads / 32 * kPoolCtas;
-constexpr int64_t kSmallPool = 1 << 15;  // entries and pages up to which a cluster is quicker
+// Entries and pages (compaction: entries) up to which a cluster takes all steps.  Resize, a page
+// more for each row: 17 us against 31 at 2^15 entries and pages, 25 against 31 at 2^16, 25 against
+// 29 at 2^17, 40 against 31 at 2^18.  Compaction, an eighth of the pages at most: 15.0 against
+// 15.0 at 2^14 entries beside as many pages, 17 against 16 at 2^15, 21 against 18 at 2^16.
+constexpr int64_t kSmallPool = 1 << 15;
 
 struct ClusterSums {
   int2 warp[kPoolThreads / 32];
